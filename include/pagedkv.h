@@ -357,6 +357,99 @@ size_t pkv_paged_varlen_prefill_workspace_bytes(int32_t batch, int32_t num_q_hea
                                                 int32_t num_kv_heads, int32_t head_dim,
                                                 int32_t max_seqlen_q);
 
+/*
+ * Score modifiers: attention whose scores are capped, biased by distance, or
+ * cut by a document, window or prefix mask, over the same caches.  These
+ * calls are additions of this library (the pages' attention has none).  With
+ * p the query's absolute position, t the key's and h the query head:
+ *   s = scale * q . K_t
+ *   s = softcap * tanh(s / softcap)             when softcap > 0
+ *   s = s - alibi_slopes[h] * |p - t|           when alibi_slopes is given
+ *   out = sum_t softmax(s)_t V_t over the keys the row sees; a row that sees
+ *   none is written as zeros.
+ * Which keys a row sees: t < nk (its sequence's length) and
+ *   t >= first_keys[row]                        when first_keys is given
+ *   t <= p, or t < prefix_lens[sequence]        (prefix_lens: when given; causal only)
+ * first_keys is the start of the row's document when several are packed into
+ * one sequence, or max(0, p + 1 - W) for a window of W keys: any value is
+ * taken (below 0 means 0; at or past the last key the row sees nothing).  A
+ * key before every first_keys value of a tile of rows is not read, and neither
+ * is the table entry of a block that holds only such keys.
+ *
+ * softcap         0 = none, else finite and > 0
+ * alibi_slopes    device, float32 [num_q_heads], or NULL
+ * first_keys      device, int32, or NULL: [batch] for decode, [total_q] for the prefill call
+ * prefix_lens     device, int32 [batch], or NULL: any value (clamped to [0, nk]); needs causal = 1
+ *
+ * Scores, softmax statistics and sums are float32 (a product q k beyond its
+ * range makes the score an infinity, or undefined where both signs occur; a
+ * cap takes an infinity to +-softcap).  In the bf16 calls the
+ * weights enter the P V product as bf16 and the row sums add the same rounded
+ * weights.  Values of keys that no row of the sequence sees are never used;
+ * V of a key that some rows see must be finite, since a row that does not see
+ * it weighs it by 0.
+ *
+ * paged_decode_attn_mod: pkv_paged_decode_attn with these modifiers (the query
+ * sits at position context_lens[b] - 1); every other argument, the workspace
+ * and its size function are pkv_paged_decode_attn's.  The split of the work
+ * counts visible keys only.
+ */
+int pkv_paged_decode_attn_mod(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, int32_t max_blocks_per_seq,
+                              const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                              int32_t num_blocks, float scale, float softcap,
+                              const float* alibi_slopes, const int32_t* first_keys, int32_t num_splits,
+                              void* workspace, size_t workspace_bytes, pkv_dtype dtype,
+                              pkv_stream_t stream);
+
+/*
+ * paged_varlen_prefill_attn_mod: pkv_paged_varlen_prefill_attn with the score
+ * modifiers above; every other argument, the range checks, the optional
+ * workspace and its size function are pkv_paged_varlen_prefill_attn's.
+ * Supported: BF16; head_dim 64 or 128; G in {1, 2, 4, 8}; every block size
+ * (a tile is gathered in pieces of gcd(block_size, 128) rows, so sizes that
+ * share few factors of 2 with 128 take more copies).
+ */
+int pkv_paged_varlen_prefill_attn_mod(void* out, const void* q, const void* k, const void* v,
+                                      const void* k_cache, const void* v_cache,
+                                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                      int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      int32_t batch, int32_t total_q, int32_t total_k,
+                                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t block_size, int32_t num_blocks, float scale,
+                                      int32_t causal, float softcap, const float* alibi_slopes,
+                                      const int32_t* first_keys, const int32_t* prefix_lens,
+                                      void* workspace, size_t workspace_bytes, pkv_dtype dtype,
+                                      pkv_stream_t stream);
+
+/*
+ * paged_varlen_prefill_attn_fp8: a chunk of new tokens per sequence over an
+ * FP8 E4M3 cache (chunked prefill, or the drafted tokens of a verify pass):
+ * the same result as pkv_paged_varlen_prefill_attn on the dequantized cache
+ * (value(code) * scale).  The new rows are stored first with
+ * pkv_kv_store_fp8.  Always paged: block_tables must not be NULL.
+ *
+ *   q, out          device, bf16 [total_q, num_q_heads, head_dim]
+ *   k_cache,v_cache device, E4M3 bytes [num_blocks, block_size, num_kv_heads, head_dim]
+ *   k_scale,v_scale finite and > 0
+ *   other arguments, range checks, workspace and its size function as for
+ *   pkv_paged_varlen_prefill_attn
+ * The weights enter the P V product as f16 (the row sums add the same rounded
+ * weights), q as f16 after a power-of-two scaling of each row.
+ * Supported: head_dim 64 or 128; G in {1, 2, 4, 8}; every block size.
+ */
+int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                      int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                      int32_t num_blocks, float scale, float k_scale, float v_scale,
+                                      int32_t causal, void* workspace, size_t workspace_bytes,
+                                      pkv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,32 +37,6 @@ extern "C" size_t pkv_paged_decode_workspace_bytes(int32_t batch, int32_t num_q_
   return workspace_layout(batch, num_q_heads, head_dim, num_splits, info.sms, &a, &b);
 }
 
-namespace {
-
-// Host-side argument checks of pkv_paged_decode_attn (everything but the
-// workspace): PKV_OK when a launch may follow, 1 when batch is 0 (nothing to
-// do), else the negative status to return.
-int check_decode_args(const void* out, const void* q, const void* k_cache, const void* v_cache,
-                      const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
-                      int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                      int32_t block_size, int32_t num_blocks, int32_t num_splits, pkv_dtype dtype) {
-  if (batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
-      num_blocks < 0 || max_blocks_per_seq < 0 || num_splits < 0)
-    return PKV_EINVAL;
-  if (num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
-  if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_EUNSUPPORTED;
-  if (head_dim != 64 && head_dim != 128) return PKV_EUNSUPPORTED;
-  if (num_kv_heads > 8) return PKV_EUNSUPPORTED;
-  if (static_cast<long long>(max_blocks_per_seq) * block_size > INT32_MAX) return PKV_EINVAL;
-  if (batch == 0) return 1;
-  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_EINVAL;
-  if (!pkv::aligned16(out) || !pkv::aligned16(q) || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache))
-    return PKV_EALIGN;
-  return PKV_OK;
-}
-
-}  // namespace
-
 extern "C" int pkv_paged_decode_attn(void* out, const void* q, const void* k_cache, const void* v_cache,
                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
                                      const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
@@ -73,47 +47,9 @@ extern "C" int pkv_paged_decode_attn(void* out, const void* q, const void* k_cac
                                     num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, num_splits, dtype);
   if (chk != PKV_OK) return chk > 0 ? PKV_OK : chk;
 
-  pkv::DeviceInfo info;
-  if (pkv::device_info(&info) != PKV_OK) return PKV_ECUDA;
-  int st = PKV_OK;
-  unsigned int* err = pkv::device_error_word(&st);
-  if (st != PKV_OK) return st;
-
-  Params p{};
-  size_t off_o = 0, off_ml = 0;
-  const size_t need = workspace_layout(batch, num_q_heads, head_dim, num_splits, info.sms, &off_o, &off_ml);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return PKV_EWORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_EALIGN;
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
-    p.counters = reinterpret_cast<int32_t*>(ws);
-    p.part_o = reinterpret_cast<float*>(ws + off_o);
-    p.part_ml = reinterpret_cast<float*>(ws + off_ml);
-  }
-  p.out = out;
-  p.q = q;
-  p.k_cache = static_cast<const unsigned char*>(k_cache);
-  p.v_cache = static_cast<const unsigned char*>(v_cache);
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.err = err;
-  p.max_blocks = max_blocks_per_seq;
-  p.batch = batch;
-  p.hq = num_q_heads;
-  p.ql = 1;
-  p.hkv = num_kv_heads;
-  p.block_size = block_size;
-  p.num_blocks = num_blocks;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.v_scale = 1.f;
-  p.num_splits = num_splits;
-  const int group = num_q_heads / num_kv_heads;
-  if (dtype == PKV_BF16) {
-    if (head_dim == 128) return dispatch_g<__nv_bfloat16, 128>(p, group, info.sms, stream);
-    return dispatch_g<__nv_bfloat16, 64>(p, group, info.sms, stream);
-  }
-  if (head_dim == 128) return dispatch_g<float, 128>(p, group, info.sms, stream);
-  return dispatch_g<float, 64>(p, group, info.sms, stream);
+  return run_decode<false>(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, batch, num_q_heads,
+                           num_kv_heads, head_dim, block_size, num_blocks, scale, pkv::ScoreMod{}, num_splits, workspace,
+                           workspace_bytes, dtype, stream);
 }
 
 // ------------------------------------------------------------------ no-allocation variant

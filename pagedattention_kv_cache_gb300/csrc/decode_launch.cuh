@@ -88,7 +88,7 @@ size_t workspace_layout(int batch, int hq, int d, int num_splits, int sms, size_
   return *off_ml + align256(slots * hq * 2 * sizeof(float));
 }
 
-template <typename T, typename TC, int D, int G, int QL>
+template <typename T, typename TC, int D, int G, int QL, bool kMod = false>
 int launch(Params& p, int sms, cudaStream_t stream) {
   const LaunchShape ls = launch_shape<TC, D, G * QL>(p.hkv);
   if (ls.stages < 2) return PKV_EUNSUPPORTED;
@@ -97,7 +97,7 @@ int launch(Params& p, int sms, cudaStream_t stream) {
   p.t_stage = ls.t_stage;
   p.stages = ls.stages;
   p.stage_bytes = ls.stage_bytes;
-  auto kernel = paged_decode_kernel<T, TC, D, G, QL>;
+  auto kernel = paged_decode_kernel<T, TC, D, G, QL, kMod>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ls.smem)) !=
       cudaSuccess)
     return PKV_ECUDA;
@@ -111,7 +111,7 @@ int launch(Params& p, int sms, cudaStream_t stream) {
                                                                                                        : PKV_ECUDA;
 }
 
-template <int G, int QL, typename TC = __nv_bfloat16>
+template <int G, int QL, typename TC = __nv_bfloat16, bool kMod = false>
 int launch_mma(Params& p, int sms, cudaStream_t stream) {
   constexpr int ES = static_cast<int>(sizeof(TC));
   constexpr int R = G * QL;
@@ -146,7 +146,7 @@ int launch_mma(Params& p, int sms, cudaStream_t stream) {
   p.t_stage = ls.t_stage;
   p.stages = ls.stages;
   p.stage_bytes = ls.stage_bytes;
-  auto kernel = paged_decode_mma_kernel<G, QL, TC>;
+  auto kernel = paged_decode_mma_kernel<G, QL, TC, kMod>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ls.smem)) !=
       cudaSuccess)
     return PKV_ECUDA;
@@ -162,23 +162,97 @@ int launch_mma(Params& p, int sms, cudaStream_t stream) {
              : PKV_ECUDA;
 }
 
-template <typename T, int D>
+template <typename T, int D, int G, bool kMod>
+int launch_g(Params& p, int sms, cudaStream_t stream) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && D == 128)
+    return launch_mma<G, 1, __nv_bfloat16, kMod>(p, sms, stream);
+  else
+    return launch<T, T, D, G, 1, kMod>(p, sms, stream);
+}
+
+template <typename T, int D, bool kMod = false>
 int dispatch_g(Params& p, int group, int sms, cudaStream_t stream) {
   switch (group) {
-    case 1:
-      if constexpr (std::is_same<T, __nv_bfloat16>::value && D == 128) return launch_mma<1, 1>(p, sms, stream);
-      return launch<T, T, D, 1, 1>(p, sms, stream);
-    case 2:
-      if constexpr (std::is_same<T, __nv_bfloat16>::value && D == 128) return launch_mma<2, 1>(p, sms, stream);
-      return launch<T, T, D, 2, 1>(p, sms, stream);
-    case 4:
-      if constexpr (std::is_same<T, __nv_bfloat16>::value && D == 128) return launch_mma<4, 1>(p, sms, stream);
-      return launch<T, T, D, 4, 1>(p, sms, stream);
-    case 8:
-      if constexpr (std::is_same<T, __nv_bfloat16>::value && D == 128) return launch_mma<8, 1>(p, sms, stream);
-      return launch<T, T, D, 8, 1>(p, sms, stream);
+    case 1: return launch_g<T, D, 1, kMod>(p, sms, stream);
+    case 2: return launch_g<T, D, 2, kMod>(p, sms, stream);
+    case 4: return launch_g<T, D, 4, kMod>(p, sms, stream);
+    case 8: return launch_g<T, D, 8, kMod>(p, sms, stream);
     default: return PKV_EUNSUPPORTED;
   }
+}
+
+// Argument checks shared by the decode entry points (everything but the
+// workspace): PKV_OK when a launch may follow, 1 when batch is 0 (nothing to
+// do), else the negative status to return.
+int check_decode_args(const void* out, const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                      int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                      int32_t block_size, int32_t num_blocks, int32_t num_splits, pkv_dtype dtype) {
+  if (batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
+      num_blocks < 0 || max_blocks_per_seq < 0 || num_splits < 0)
+    return PKV_EINVAL;
+  if (num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
+  if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_EUNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128) return PKV_EUNSUPPORTED;
+  if (num_kv_heads > 8) return PKV_EUNSUPPORTED;
+  if (static_cast<long long>(max_blocks_per_seq) * block_size > INT32_MAX) return PKV_EINVAL;
+  if (batch == 0) return 1;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_EINVAL;
+  if (!pkv::aligned16(out) || !pkv::aligned16(q) || !pkv::aligned16(k_cache) || !pkv::aligned16(v_cache))
+    return PKV_EALIGN;
+  return PKV_OK;
+}
+
+// Runs decode on arguments that check_decode_args accepted: the workspace
+// check, the parameters, and the kernel for the type and head_dim.
+template <bool kMod>
+int run_decode(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+               int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+               int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+               const pkv::ScoreMod& mod, int32_t num_splits, void* workspace, size_t workspace_bytes,
+               pkv_dtype dtype, cudaStream_t stream) {
+  pkv::DeviceInfo info;
+  if (pkv::device_info(&info) != PKV_OK) return PKV_ECUDA;
+  int st = PKV_OK;
+  unsigned int* err = pkv::device_error_word(&st);
+  if (st != PKV_OK) return st;
+
+  Params p{};
+  size_t off_o = 0, off_ml = 0;
+  const size_t need = workspace_layout(batch, num_q_heads, head_dim, num_splits, info.sms, &off_o, &off_ml);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return PKV_EWORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_EALIGN;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    p.counters = reinterpret_cast<int32_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(ws + off_o);
+    p.part_ml = reinterpret_cast<float*>(ws + off_ml);
+  }
+  p.out = out;
+  p.q = q;
+  p.k_cache = static_cast<const unsigned char*>(k_cache);
+  p.v_cache = static_cast<const unsigned char*>(v_cache);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.err = err;
+  p.max_blocks = max_blocks_per_seq;
+  p.batch = batch;
+  p.hq = num_q_heads;
+  p.ql = 1;
+  p.hkv = num_kv_heads;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.v_scale = 1.f;
+  p.num_splits = num_splits;
+  p.mod = mod;
+  const int group = num_q_heads / num_kv_heads;
+  if (dtype == PKV_BF16) {
+    if (head_dim == 128) return dispatch_g<__nv_bfloat16, 128, kMod>(p, group, info.sms, stream);
+    return dispatch_g<__nv_bfloat16, 64, kMod>(p, group, info.sms, stream);
+  }
+  if (head_dim == 128) return dispatch_g<float, 128, kMod>(p, group, info.sms, stream);
+  return dispatch_g<float, 64, kMod>(p, group, info.sms, stream);
 }
 
 }  // namespace

@@ -65,7 +65,7 @@ __host__ __device__ constexpr int mma_chunks_per_warp() {
   return std::is_same<TC, __nv_fp8_e4m3>::value ? 2 : 1;
 }
 
-template <int G, int QL, typename TC = __nv_bfloat16>
+template <int G, int QL, typename TC = __nv_bfloat16, bool kMod = false>
 __global__ void __launch_bounds__(288, 1)
     paged_decode_mma_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
@@ -121,16 +121,16 @@ __global__ void __launch_bounds__(288, 1)
     pkv::fence_mbar_init();
   }
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    if (context_len(p, b) != 0) continue;
+    if (covered_len<kMod>(p, b) != 0) continue;
     T* o = static_cast<T*>(p.out) + static_cast<size_t>(b) * rows_per_seq * D;
     for (int i = tid; i < rows_per_seq * D; i += blockDim.x) o[i] = static_cast<T>(0.0f);
   }
   Plan plan;
   if (p.num_splits > 0) {
-    plan_fixed(p, plan);
+    plan_fixed<kMod>(p, plan);
     __syncthreads();
   } else {
-    plan_auto(p, plan, sh);
+    plan_auto<kMod>(p, plan, sh);
   }
 
   if (warp == nw) {
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(288, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
       }
-      for_each_segment(p, plan, [&](const Segment& seg) -> bool {
+      for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
         const int32_t* table = p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks;
         for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
           const int s = it % p.stages;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(288, 1)
       });
       return;
     }
-    for_each_segment(p, plan, [&](const Segment& seg) -> bool {
+    for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
       const int32_t* table = p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks;
       for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
         const int s = it % p.stages;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(288, 1)
   const uint32_t v8b = cbase + (2 * c + 1) * rs + ((vq ^ (p.tma ? 2u * c + 1u : 0u)) << 4);
   int it = 0;
 
-  for_each_segment(p, plan, [&](const Segment& seg) -> bool {
+  for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
     // Q as the A operand: rows r0 / r0 + 8, columns 16 kk + 2c (+1) and + 8
     // (bf16), or 16 kk + 4c (+1) and 16 kk + 4c + 2 (+3) as scaled f16 (FP8)
     uint32_t qf[8][4];
@@ -315,6 +315,12 @@ __global__ void __launch_bounds__(288, 1)
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY};
     float l[2] = {0.f, 0.f};
+    // distance bias of the fragment rows' heads, per key of distance, in the exp2 domain
+    static_assert(!kMod || (QL == 1 && kT), "score modifiers: decode only");
+    float slope = 0.f;
+    if constexpr (kMod) {
+      if (p.mod.slopes && r0 < R) slope = __ldg(p.mod.slopes + g * G + r0) * pkv::kLog2e;
+    }
 
     for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
       const int s = it % p.stages;
@@ -346,6 +352,19 @@ __global__ void __launch_bounds__(288, 1)
                   make_uint4(0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
+          }
+          if constexpr (kMod) {
+            // keys before the first visible one share its chunk: their V rows are zeroed
+            // too, whatever they hold
+            const int hidden = seg.lo - (t + tt0);
+            if (hidden > 0) {
+              unsigned char* vrows = stage_base + s * p.stage_bytes + p.stage_bytes / 2 + sub * csub + cbase;
+              for (int idx = lane; idx < hidden * 8 * NH; idx += 32)
+                *reinterpret_cast<uint4*>(vrows + (idx / (8 * NH)) * rs + ((idx % (8 * NH)) / 8) * hs + (idx % 8) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+            }
           }
           // S = Q K^T for 16 keys (two n-tiles of 8)
           if constexpr (kFp8) {
@@ -381,7 +400,14 @@ __global__ void __launch_bounds__(288, 1)
             for (int e = 0; e < 2 * HH; ++e) {
               const int key = nb * 8 + 2 * c + (e & 1);
               float x = sacc[sub][nb][e] * qmul[e >> 1];
-              const bool visible = key < nv && (QL == 1 || t + tt0 + key <= ((e < 2) ? lim0 : lim1));
+              bool visible = key < nv && (QL == 1 || t + tt0 + key <= ((e < 2) ? lim0 : lim1));
+              if constexpr (kMod) {
+                if (p.mod.cap_log2 > 0.f)
+                  x = p.mod.cap_log2 * pkv::tanh_by_exp(sacc[sub][nb][e] * p.mod.raw_to_x);
+                // the query sits at ctx - 1, so the distance is ctx - 1 - t >= 0
+                x = fmaf(slope, static_cast<float>(t + tt0 + key - (seg.ctx - 1)), x);
+                visible = visible && t + tt0 + key >= seg.lo;
+              }
               x = visible ? x : -INFINITY;
               sacc[sub][nb][e] = x;
               mt[e >> 1] = fmaxf(mt[e >> 1], x);

@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "score_mod.cuh"
 
 namespace {
 
@@ -82,6 +83,7 @@ struct Params {
   size_t stage_bytes;
   int align;  // split points fall on multiples of this many tokens of a sequence (0 or 1: anywhere)
   int tma;    // mma kernel: stages filled by 4-D tensor copies of 16-token boxes (block_size % 16 == 0)
+  pkv::ScoreMod mod;  // score modifiers (kernels instantiated with kMod)
 };
 
 // One contiguous piece of work: tokens [t0, t1) of sequence b.
@@ -92,6 +94,7 @@ struct Segment {
   int nparts;      // CTAs sharing sequence b
   int first_slot;  // workspace slot of the sequence's first part
   int slot;        // this part's slot
+  int lo;          // first visible key (0 without modifiers)
 };
 
 // Bounded pipeline wait.  On a timeout the CTA raises PKV_DERR_WAIT_TIMEOUT,
@@ -120,6 +123,28 @@ __device__ __forceinline__ int context_len(const Params& p, int b) {
   return n;
 }
 
+// First visible key of sequence b of length n (kMod with first_keys; else 0), in [0, n].
+template <bool kMod>
+__device__ __forceinline__ int first_key(const Params& p, int b, int n) {
+  if constexpr (!kMod) return 0;
+  if (!p.mod.first_keys) return 0;
+  return min(max(__ldg(p.mod.first_keys + b), 0), n);
+}
+
+// Where the tokens a CTA plan covers begin: the first visible key, down to the
+// split alignment (a 16-token box that holds it), so that earlier blocks are
+// neither read nor counted in the split.
+__device__ __forceinline__ int cover_start(const Params& p, int lo) { return lo - lo % align_tokens(p); }
+
+// Tokens of sequence b that the plan covers: its context, from cover_start on; 0 when it sees no key.
+template <bool kMod>
+__device__ __forceinline__ int covered_len(const Params& p, int b) {
+  const int n = context_len(p, b);
+  if constexpr (!kMod) return n;
+  const int lo = first_key<kMod>(p, b, n);
+  return lo >= n ? 0 : n - cover_start(p, lo);
+}
+
 // Work plan of this CTA, computed identically by every thread.
 struct Plan {
   // automatic mode
@@ -133,6 +158,7 @@ struct Plan {
 
 // Block-wide sum over context lengths and search for the first sequence
 // overlapping this CTA's token range (automatic mode).
+template <bool kMod>
 __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
   const int tid = threadIdx.x;
   const int nthreads = blockDim.x;
@@ -141,7 +167,7 @@ __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
   if (p.batch <= nthreads) {
     // one pass when the batch fits the block: each thread loads one length,
     // one block-wide scan gives the total and the prefix that holds `start`
-    const long long n = tid < p.batch ? round_up(context_len(p, tid), A) : 0;
+    const long long n = tid < p.batch ? round_up(covered_len<kMod>(p, tid), A) : 0;
     long long incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -174,7 +200,7 @@ __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
     return;
   }
   long long local = 0;
-  for (int b = tid; b < p.batch; b += nthreads) local += round_up(context_len(p, b), A);
+  for (int b = tid; b < p.batch; b += nthreads) local += round_up(covered_len<kMod>(p, b), A);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) local += __shfl_xor_sync(0xffffffffu, local, off);
   if (tid % 32 == 0) sh[tid / 32] = local;
@@ -195,7 +221,7 @@ __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
   long long running = 0;
   for (int base = 0; base < p.batch; base += nthreads) {
     const int b = base + tid;
-    const long long n = b < p.batch ? round_up(context_len(p, b), A) : 0;
+    const long long n = b < p.batch ? round_up(covered_len<kMod>(p, b), A) : 0;
     long long incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -224,24 +250,28 @@ __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
   __syncthreads();
 }
 
+template <bool kMod>
 __device__ void plan_fixed(const Params& p, Plan& plan) {
   const int S = p.num_splits;
   const int b = blockIdx.x / S;
   const int j = blockIdx.x % S;
   plan.fixed_valid = false;
   if (b >= p.batch) return;
-  const int n = context_len(p, b);
-  if (n == 0) return;
+  const int ctx = context_len(p, b);
+  const int lo = first_key<kMod>(p, b, ctx);
+  if (lo >= ctx) return;
+  const int start = kMod ? cover_start(p, lo) : 0;
+  const int n = ctx - start;
   const int chunk = static_cast<int>(round_up((n + S - 1) / S, align_tokens(p)));
   const int t0 = j * chunk;
   if (t0 >= n) return;
   const int t1 = t0 + chunk < n ? t0 + chunk : n;
-  plan.fixed = Segment{b, n, t0, t1, (n + chunk - 1) / chunk, b * S, b * S + j};
+  plan.fixed = Segment{b, ctx, start + t0, start + t1, (n + chunk - 1) / chunk, b * S, b * S + j, lo};
   plan.fixed_valid = true;
 }
 
 // Calls fn(segment) for every segment of this CTA, in order.
-template <typename Fn>
+template <bool kMod, typename Fn>
 __device__ __forceinline__ bool for_each_segment(const Params& p, const Plan& plan, Fn&& fn) {
   if (p.num_splits > 0) {
     if (plan.fixed_valid) return fn(plan.fixed);
@@ -253,15 +283,18 @@ __device__ __forceinline__ bool for_each_segment(const Params& p, const Plan& pl
   const int A = align_tokens(p);
   long long cu = plan.cu_first;
   for (int b = plan.b_first; b < p.batch && cu < plan.end; ++b) {
-    const int n = context_len(p, b);
+    const int ctx = context_len(p, b);
+    const int lo = first_key<kMod>(p, b, ctx);
+    const int start = kMod ? cover_start(p, lo) : 0;
+    const int n = lo < ctx ? ctx - start : 0;
     const long long np = round_up(n, A);
     if (n > 0) {
       const long long s0 = plan.start > cu ? plan.start : cu;
       const long long s1 = plan.end < cu + np ? plan.end : cu + np;
       const int c0 = static_cast<int>(cu / plan.per);
       const int c1 = static_cast<int>((cu + np - 1) / plan.per);
-      Segment seg{b, n, static_cast<int>(s0 - cu), static_cast<int>(s1 - cu < n ? s1 - cu : n), c1 - c0 + 1,
-                  c0 + b, static_cast<int>(blockIdx.x) + b};
+      Segment seg{b, ctx, start + static_cast<int>(s0 - cu), start + static_cast<int>(s1 - cu < n ? s1 - cu : n),
+                  c1 - c0 + 1, c0 + b, static_cast<int>(blockIdx.x) + b, lo};
       if (!fn(seg)) return false;
     }
     cu += np;

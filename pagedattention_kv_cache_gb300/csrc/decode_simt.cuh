@@ -10,7 +10,7 @@ namespace {
 // holds R = G * QL rows: row rho is query token rho / G, head g * G + rho % G.
 // T is the q / out element type, TC the cache's (T: an FP8 cache runs on the
 // tensor-core kernel of decode_mma.cuh).
-template <typename T, typename TC, int D, int G, int QL>
+template <typename T, typename TC, int D, int G, int QL, bool kMod = false>
 __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
   pkv::pdl_enter();
   constexpr int R = G * QL;
@@ -42,17 +42,17 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
 
   // context length 0 rows: zeros, nothing read (section 5 padding)
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    if (context_len(p, b) != 0) continue;
+    if (covered_len<kMod>(p, b) != 0) continue;
     T* o = static_cast<T*>(p.out) + static_cast<size_t>(b) * rows_per_seq * D;
     for (int i = tid; i < rows_per_seq * D; i += blockDim.x) o[i] = static_cast<T>(0.0f);
   }
 
   Plan plan;
   if (p.num_splits > 0) {
-    plan_fixed(p, plan);
+    plan_fixed<kMod>(p, plan);
     __syncthreads();
   } else {
-    plan_auto(p, plan, sh);
+    plan_auto<kMod>(p, plan, sh);
   }
 
   if (warp == nw) {
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
     const uint64_t policy = pkv::l2_evict_first_policy();
     const size_t head_row = static_cast<size_t>(p.hkv) * S::ROW_BYTES;  // bytes per token, all heads
     int it = 0;
-    for_each_segment(p, plan, [&](const Segment& seg) -> bool {
+    for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
       const int32_t* table = p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks;
       for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
         const int s = it % p.stages;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
   const int nthreads_c = nw * 32;
   int it = 0;
 
-  for_each_segment(p, plan, [&](const Segment& seg) -> bool {
+  for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
     // q of the R rows sharing KV head g, pre-scaled into the exp2 domain
     float qr[R][S::EPL];
 #pragma unroll
@@ -117,8 +117,12 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
           Chunk<T>::unpack(c, &qr[h][k * S::EPC + u * Chunk<T>::N]);
         }
 #pragma unroll
-      for (int e = 0; e < S::EPL; ++e) qr[h][e] *= p.scale_log2;
+      for (int e = 0; e < S::EPL; ++e) qr[h][e] *= kMod && p.mod.cap_log2 > 0.f ? p.mod.raw_to_x : p.scale_log2;
     }
+    float slope[R];
+#pragma unroll
+    for (int h = 0; h < R; ++h)
+      slope[h] = kMod && p.mod.slopes ? __ldg(p.mod.slopes + g * G + h % G) * pkv::kLog2e : 0.f;
     float acc[R][S::EPL];
     float m[R], l[R];
 #pragma unroll
@@ -170,6 +174,12 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
           for (int off = 1; off < S::LPT; off <<= 1) dot[h] += __shfl_xor_sync(0xffffffffu, dot[h], off);
           // query token h / G sits at position ctx - QL + h / G and sees keys up to it
           const bool visible = QL == 1 || t + tt <= seg.ctx - QL + h / G;
+          if constexpr (kMod) {
+            // q carries the scale that takes a dot product to tanh's argument.  Splits start at
+            // the first visible key (no alignment here), so every token of a stage is visible.
+            if (p.mod.cap_log2 > 0.f) dot[h] = p.mod.cap_log2 * tanhf(dot[h]);
+            dot[h] = fmaf(slope[h], static_cast<float>(t + tt - (seg.ctx - 1)), dot[h]);
+          }
           sc[r][h] = (valid && visible) ? dot[h] : -INFINITY;
         }
       }

@@ -1,8 +1,8 @@
-// Arguments shared by the two prefill kernels (tcgen05 and mma.sync) and the
-// C entry point that chooses between them.
+// Arguments shared by the prefill kernels and their C entry points.
 #pragma once
 
 #include "common.cuh"
+#include "score_mod.cuh"
 
 namespace pkv {
 
@@ -32,6 +32,9 @@ struct PrefillArgs {
   int head_dim;  // 64 or 128 (the mma.sync kernel: 128 only)
   void* workspace;         // split of long items (tcgen05 path), or null
   size_t workspace_bytes;
+  float k_scale = 1.f;  // FP8 cache
+  float v_scale = 1.f;
+  ScoreMod mod;
 };
 
 // Tensor-core (tcgen05 + TMEM + TMA) path; requires head_dim 64 or 128, bf16, and

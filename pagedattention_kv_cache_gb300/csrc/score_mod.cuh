@@ -1,0 +1,53 @@
+// Score modifiers of the *_mod entry points: softcap, distance bias and first
+// visible keys.  Scores live in the exp2 domain (natural score x log2 e), so
+//     capped:  c log2e tanh(s / c)          (s = raw * scale, c the cap)
+//     biased:  - slope_h log2e |p - t|
+#pragma once
+
+#include "common.cuh"
+
+namespace pkv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Device-side form of the modifiers (host constants folded once per call).
+struct ScoreMod {
+  float cap_log2 = 0.f;        // c log2e (0: no cap)
+  float raw_to_x = 0.f;        // raw score -> s / c, the argument of tanh
+  const float* slopes = nullptr;     // [num_q_heads], natural units
+  const int32_t* first_keys = nullptr;   // decode: [batch]; prefill: [total_q]
+  const int32_t* prefix_lens = nullptr;  // prefill only: [batch]
+};
+
+// `raw_scale` takes a raw q . k to the natural score (scale, and an FP8 cache's K scale).
+inline ScoreMod make_score_mod(float raw_scale, float softcap, const float* slopes, const int32_t* first_keys,
+                               const int32_t* prefix_lens) {
+  ScoreMod m;
+  if (softcap > 0.f) {
+    m.cap_log2 = softcap * kLog2e;
+    m.raw_to_x = raw_scale / softcap;
+  }
+  m.slopes = slopes;
+  m.first_keys = first_keys;
+  m.prefix_lens = prefix_lens;
+  return m;
+}
+
+// 0 or finite and positive (a NaN fails both).
+inline bool softcap_valid(float softcap) { return softcap >= 0.f && softcap <= 3.0e38f; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(x) = 1 - 2 / (1 + e^2x): two special-function operations.  Its error is
+// absolute, about 2^-22 (the sum 1 + e^2x is rounded once, the quotient once),
+// which is what counts in a score: c log2e 2^-22 is 2e-5 for a cap of 50.
+// Overflow of e^2x gives 1, underflow -1, a NaN stays one.
+__device__ __forceinline__ float tanh_by_exp(float x) {
+  return 1.f - __fdividef(2.f, 1.f + ex2(x * (2.f * kLog2e)));
+}
+
+}  // namespace pkv

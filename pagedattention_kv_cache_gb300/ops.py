@@ -10,6 +10,7 @@ in the library's CUDA kernels; nothing here computes.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -366,6 +367,169 @@ def paged_varlen_prefill_attn(q: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_se
         total_k, hq, hkv, d, bs, nb, ctypes.c_float(scale), 1 if causal else 0, _ptr(workspace), ws_bytes,
         _dtype_code(q), _stream(stream, dev))
     _lib.check("pkv_paged_varlen_prefill_attn", st)
+    return out
+
+
+def _on_stream(stream):
+    """Allocations of a call belong to the stream it runs on (its pool, and the zero fill in its order)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _workspace_args(workspace, nbytes: int, device: torch.device):
+    """(tensor, pointer, bytes) of a split workspace: the caller's, none (False), or a zero-filled one for this call."""
+    if workspace is False or (workspace is None and nbytes == 0):
+        return None, None, 0
+    if workspace is None:
+        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", device=device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _need_modifiers(device, num_q_heads: int, alibi_slopes, first_keys, rows: int, prefix_lens=None, batch: int = 0):
+    if alibi_slopes is not None:
+        _need(alibi_slopes, "alibi_slopes", dtype=torch.float32, device=device, shape=(num_q_heads,))
+    if first_keys is not None:
+        _need(first_keys, "first_keys", dtype=torch.int32, device=device, shape=(rows,))
+    if prefix_lens is not None:
+        _need(prefix_lens, "prefix_lens", dtype=torch.int32, device=device, shape=(batch,))
+
+
+def paged_decode_attn_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, *,
+                          softcap: float = 0.0, alibi_slopes: torch.Tensor | None = None,
+                          first_keys: torch.Tensor | None = None, num_splits: int = 0,
+                          workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """paged_decode_attn with modified scores; returns out [B, Hq, D] (same dtype as q).
+
+    softcap: scores become softcap * tanh(score / softcap) (0 = none).
+    alibi_slopes: float32 [Hq]; head h's scores fall by alibi_slopes[h] per position of distance.
+    first_keys: int32 [B]; keys before it are not seen (window, or the start of the document).
+    workspace: from decode_workspace(); allocated (zero-filled) for the call when None.
+    """
+    dev = _device(q, "q")
+    _need(q, "q", ndim=3)
+    _need(k_cache, "k_cache", dtype=q.dtype, ndim=4, device=dev)
+    _need(v_cache, "v_cache", dtype=q.dtype, ndim=4, device=dev, shape=k_cache.shape)
+    _need(block_tables, "block_tables", dtype=torch.int32, ndim=2, device=dev)
+    _need(context_lens, "context_lens", dtype=torch.int32, ndim=1, device=dev)
+    B, hq, d = q.shape
+    nb, bs, hkv, d2 = k_cache.shape
+    if d2 != d or block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("inconsistent shapes between q, caches, block_tables and context_lens")
+    _need_modifiers(dev, hq, alibi_slopes, first_keys, B)
+    handle = _stream(stream, dev)
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
+        workspace, ws_ptr, ws_bytes = _workspace_args(
+            workspace, decode_workspace_bytes(B, hq, d, num_splits) if workspace is None else 0, dev)
+    st = _lib.load().pkv_paged_decode_attn_mod(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+        _ptr(context_lens), B, hq, hkv, d, bs, nb, ctypes.c_float(scale), ctypes.c_float(softcap), _ptr(alibi_slopes),
+        _ptr(first_keys), num_splits, ws_ptr, ws_bytes, _dtype_code(q), handle)
+    _lib.check("pkv_paged_decode_attn_mod", st)
+    return out
+
+
+def paged_varlen_prefill_attn_mod(q: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                                  max_seqlen_q: int, max_seqlen_k: int, scale: float, *,
+                                  k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+                                  k_cache: torch.Tensor | None = None, v_cache: torch.Tensor | None = None,
+                                  block_tables: torch.Tensor | None = None, causal: bool = True,
+                                  softcap: float = 0.0, alibi_slopes: torch.Tensor | None = None,
+                                  first_keys: torch.Tensor | None = None, prefix_lens: torch.Tensor | None = None,
+                                  workspace: torch.Tensor | bool | None = None,
+                                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """paged_varlen_prefill_attn with modified scores; keys through block_tables (cache) or from packed k/v.
+
+    softcap, alibi_slopes: as for paged_decode_attn_mod.
+    first_keys: int32 [total_q]; the row does not see keys before it (document or window mask).
+    prefix_lens: int32 [B]; every row of the sequence sees keys below it besides the causal ones.
+    workspace: None = a zero-filled one for this call where a split needs it; False = never
+    split long query tiles; or a tensor from prefill_workspace().
+    """
+    dev = _device(q, "q")
+    _need(q, "q", ndim=3)
+    _need(cu_seqlens_q, "cu_seqlens_q", dtype=torch.int32, ndim=1, device=dev)
+    _need(cu_seqlens_k, "cu_seqlens_k", dtype=torch.int32, ndim=1, device=dev, shape=cu_seqlens_q.shape)
+    if cu_seqlens_q.shape[0] < 1:
+        raise ValueError("cu_seqlens_q must hold batch + 1 offsets")
+    B = cu_seqlens_q.shape[0] - 1
+    total_q, hq, d = q.shape
+    if block_tables is not None:
+        _need(block_tables, "block_tables", dtype=torch.int32, ndim=2, device=dev)
+        _need(k_cache, "k_cache", dtype=q.dtype, ndim=4, device=dev)
+        _need(v_cache, "v_cache", dtype=q.dtype, ndim=4, device=dev, shape=k_cache.shape)
+        nb, bs, hkv, d2 = k_cache.shape
+        mb, total_k = block_tables.shape[1], 0
+        if block_tables.shape[0] != B:
+            raise ValueError("block_tables rows must equal the batch")
+    else:
+        if k is None or v is None:
+            raise ValueError("without block_tables the packed k and v are required")
+        _need(k, "k", dtype=q.dtype, ndim=3, device=dev)
+        _need(v, "v", dtype=q.dtype, ndim=3, device=dev, shape=k.shape)
+        total_k, hkv, d2 = k.shape
+        nb = bs = mb = 0
+    if d2 != d:
+        raise ValueError("the keys' head_dim differs from q's")
+    _need_modifiers(dev, hq, alibi_slopes, first_keys, total_q, prefix_lens, B)
+    handle = _stream(stream, dev)
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
+        workspace, ws_ptr, ws_bytes = _workspace_args(
+            workspace, prefill_workspace_bytes(B, hq, hkv, d, int(max_seqlen_q)) if workspace is None else 0, dev)
+    st = _lib.load().pkv_paged_varlen_prefill_attn_mod(
+        _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q),
+        _ptr(cu_seqlens_k), int(max_seqlen_q), int(max_seqlen_k), _ptr(block_tables), mb, B, total_q,
+        total_k, hq, hkv, d, bs, nb, ctypes.c_float(scale), 1 if causal else 0, ctypes.c_float(softcap),
+        _ptr(alibi_slopes), _ptr(first_keys), _ptr(prefix_lens), ws_ptr, ws_bytes, _dtype_code(q), handle)
+    _lib.check("pkv_paged_varlen_prefill_attn_mod", st)
+    return out
+
+
+def paged_varlen_prefill_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                                  cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int, scale: float,
+                                  k_scale: float, v_scale: float, *, causal: bool = True,
+                                  workspace: torch.Tensor | bool | None = None,
+                                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Varlen prefill attention of new tokens over an E4M3 cache (uint8 or float8_e4m3fn tensors)
+    with per-tensor scales; q / out bf16 [total_q, Hq, D].  The new rows are stored first
+    (kv_store_fp8).  workspace: as for paged_varlen_prefill_attn_mod."""
+    dev = _device(q, "q")
+    _need(q, "q", dtype=torch.bfloat16, ndim=3)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(t, name, ndim=4, device=dev, shape=k_cache.shape)
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError(f"{name} must hold E4M3 codes (uint8 or float8_e4m3fn)")
+    _need(block_tables, "block_tables", dtype=torch.int32, ndim=2, device=dev)
+    _need(cu_seqlens_q, "cu_seqlens_q", dtype=torch.int32, ndim=1, device=dev)
+    _need(cu_seqlens_k, "cu_seqlens_k", dtype=torch.int32, ndim=1, device=dev, shape=cu_seqlens_q.shape)
+    B = cu_seqlens_q.shape[0] - 1
+    total_q, hq, d = q.shape
+    nb, bs, hkv, d2 = k_cache.shape
+    if d2 != d:
+        raise ValueError("k_cache head_dim differs from q's")
+    if block_tables.shape[0] != B:
+        raise ValueError("block_tables rows must equal the batch")
+    handle = _stream(stream, dev)
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        _need(out, "out", dtype=torch.bfloat16, device=dev, shape=q.shape)
+        workspace, ws_ptr, ws_bytes = _workspace_args(
+            workspace, prefill_workspace_bytes(B, hq, hkv, d, int(max_seqlen_q)) if workspace is None else 0, dev)
+    st = _lib.load().pkv_paged_varlen_prefill_attn_fp8(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(max_seqlen_q),
+        int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], B, total_q, hq, hkv, d, bs, nb,
+        ctypes.c_float(scale), ctypes.c_float(k_scale), ctypes.c_float(v_scale), 1 if causal else 0, ws_ptr, ws_bytes,
+        handle)
+    _lib.check("pkv_paged_varlen_prefill_attn_fp8", st)
     return out
 
 

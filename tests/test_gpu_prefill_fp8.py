@@ -1,0 +1,243 @@
+"""GPU parity of paged_varlen_prefill_attn_fp8 (a chunk of new tokens over an E4M3 cache) against the
+float64 oracle on the dequantized cache."""
+
+import numpy as np
+import pytest
+import torch
+
+import pagedattention_kv_cache_gb300 as pkv
+from pagedattention_kv_cache_gb300 import _lib
+from pagedattention_kv_cache_gb300 import metadata as md
+from pagedattention_kv_cache_gb300 import workloads as wl
+from oracle import fp8 as of8
+from oracle import modified as omod
+
+from _harness import as_np
+from _modified import check, i32
+
+pytestmark = pytest.mark.gpu
+
+K_SCALE, V_SCALE = 1.0 / 64, 3.0 / 256
+CACHED, NEW = [0, 16, 0, 130, 300, 5], [1, 40, 129, 0, 260, 3]
+
+
+def _codes(shape, gen, scale):
+    return torch.from_numpy(of8.quantize(torch.randn(shape, generator=gen).bfloat16().float().numpy(), scale))
+
+
+class Case:
+    def __init__(self, seed, cached, new, *, block_size=16, hq=8, hkv=2, d=128, q_scale=1.0):
+        rng, gen = np.random.default_rng(seed), torch.Generator().manual_seed(seed)
+        self.new, self.bs, self.hq, self.hkv, self.d, self.scale = new, block_size, hq, hkv, d, d ** -0.5
+        self.totals = [c + n for c, n in zip(cached, new)]
+        blocks = sum(-(-n // block_size) for n in self.totals) + 5
+        self.tables = wl._assign_blocks(rng, self.totals, block_size, blocks)
+        self.table = i32(md.table_matrix(self.tables))
+        self.kc, self.vc = [_codes((blocks, block_size, hkv, d), gen, s) for s in (K_SCALE, V_SCALE)]
+        self.q = (torch.randn(sum(new), hq, d, generator=gen) * q_scale).bfloat16()
+        self.cu_q, self.cu_k = i32([0] + np.cumsum(new).tolist()), i32([0] + np.cumsum(self.totals).tolist())
+
+    def poison(self):
+        """The E4M3 NaN in every slot that holds no key of a sequence."""
+        seen = torch.zeros(self.kc.shape[:2], dtype=torch.bool)
+        for blocks, total in zip(self.tables, self.totals):
+            for t in range(total):
+                seen[blocks[t // self.bs], t % self.bs] = True
+        self.kc[~seen], self.vc[~seen] = 0x7F, 0xFF
+
+    def reference(self, causal=True):
+        return omod.prefill_attention(as_np(self.q), self.cu_q.tolist(), self.cu_k.tolist(), self.scale,
+                                      k_cache=of8.dequantize(self.kc.numpy(), K_SCALE),
+                                      v_cache=of8.dequantize(self.vc.numpy(), V_SCALE), block_tables=self.table.numpy(),
+                                      causal=causal)
+
+    def call(self, causal=True, **kw):
+        return pkv.paged_varlen_prefill_attn_fp8(self.q.cuda(), self.kc.cuda(), self.vc.cuda(), self.table.cuda(),
+                                                 self.cu_q.cuda(), self.cu_k.cuda(), max(self.new), max(self.totals),
+                                                 self.scale, K_SCALE, V_SCALE, causal=causal, **kw)
+
+    def compare(self, causal=True, label="", **kw):
+        ref, dev = self.reference(causal)
+        self.poison()
+        out = self.call(causal, **kw)
+        torch.cuda.synchronize()
+        assert pkv.device_error() == 0
+        check(out, ref, dev, torch.float16, max(self.totals), label)
+        return out
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,hkv", [(1, 3), (2, 2), (4, 1), (8, 1)])
+@pytest.mark.parametrize("block_size", [16, 24, 256])
+def test_every_group_and_head_dim(d, group, hkv, block_size):
+    Case(group + d + block_size, CACHED, NEW, block_size=block_size, hq=group * hkv, hkv=hkv, d=d).compare()
+
+
+@pytest.mark.parametrize("block_size", [1, 4, 5, 8, 32, 64, 100, 128, 384])
+def test_block_sizes(block_size):
+    Case(block_size, CACHED, NEW, block_size=block_size, d=64 if block_size % 5 == 0 else 128).compare()
+
+
+def test_full_attention():
+    for d in (64, 128):
+        Case(d, CACHED, NEW, d=d).compare(causal=False)
+
+
+# q far outside f16's range either way: each row is scaled by a power of two, and a row of zeros stays one
+@pytest.mark.parametrize("q_scale", [0.0, 1e-30, 1e-6, 30.0, 3e4, 1e9])
+def test_q_magnitudes(q_scale):
+    c = Case(61, [40, 0], [130, 20], q_scale=q_scale)
+    c.q[5] = 0
+    c.scale = c.d ** -0.5 * (min(1.0, 3.0 / q_scale) if q_scale else 1.0)  # scores of a few units
+    c.compare(label=f"q x {q_scale}")
+
+
+def test_codes_of_every_value():
+    # every finite E4M3 code (subnormals among them) as K and as V
+    codes = torch.tensor([x for x in range(256) if x & 0x7F != 0x7F], dtype=torch.uint8)
+    c = Case(62, [0], [254], hkv=1, hq=2)
+    gen = torch.Generator().manual_seed(1)
+    for cache in (c.kc, c.vc):
+        cache.copy_(codes[torch.randint(0, 254, cache.shape, generator=gen)])
+    c.scale = 2e-4 / K_SCALE  # codes reach 448: scores of a few units
+    c.compare()
+
+
+def test_chunks_of_drafted_tokens():
+    # 1 to 8 drafted tokens per sequence after ragged histories
+    Case(63, [1000, 17, 0, 255, 511, 2000], [4, 1, 8, 3, 5, 2], hq=16, hkv=8, block_size=256).compare()
+
+
+def test_split_key_ranges():
+    c = Case(64, [6000, 3000], [70, 33], block_size=64, hq=4, hkv=2)
+    assert pkv.prefill_workspace_bytes(2, 4, 2, 128, 70) > 0
+    a = c.compare(label="split")
+    c.compare(workspace=False, label="not split")
+    ws = pkv.prefill_workspace(2, 4, 2, 128, 70)
+    for _ in range(3):
+        assert torch.equal(a, c.compare(workspace=ws))
+    assert int(ws[:65536].count_nonzero()) == 0
+
+
+def test_pool_past_32_bit_offsets():
+    bs, hkv, d, hq = 256, 8, 128, 16
+    blocks = (1 << 32) // (bs * hkv * d) + 40
+    gen = torch.Generator().manual_seed(3)
+    ids = [blocks - 1, 3, blocks - 17]
+    small = [_codes((3, bs, hkv, d), gen, s) for s in (K_SCALE, V_SCALE)]
+    pools = [torch.zeros(blocks, bs, hkv, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for pool, s in zip(pools, small):
+        pool[ids] = s.cuda()
+    q = torch.randn(40, hq, d, generator=gen).bfloat16()
+    out = pkv.paged_varlen_prefill_attn_fp8(q.cuda(), *pools, i32([ids]).cuda(), i32([0, 40]).cuda(), i32([0, 600]).cuda(),
+                                            40, 600, 0.1, K_SCALE, V_SCALE)
+    torch.cuda.synchronize()
+    assert pkv.device_error() == 0
+    ref, dev = omod.prefill_attention(as_np(q), [0, 40], [0, 600], 0.1, k_cache=of8.dequantize(small[0].numpy(), K_SCALE),
+                                      v_cache=of8.dequantize(small[1].numpy(), V_SCALE), block_tables=np.arange(3)[None])
+    check(out, ref, dev, torch.float16, 600)
+
+
+def test_bad_cu_seqlens_and_pages_raise_bits():
+    c = Case(65, [0, 16, 16], [20, 20, 20])
+    ref, dev = c.reference()
+
+    def call(cu_q, cu_k, max_q, table):
+        pkv.device_error(reset=True)
+        out = torch.full_like(c.q, 7.0).cuda()
+        pkv.paged_varlen_prefill_attn_fp8(c.q.cuda(), c.kc.cuda(), c.vc.cuda(), table.cuda(), i32(cu_q).cuda(),
+                                          i32(cu_k).cuda(), max_q, 64, c.scale, K_SCALE, V_SCALE, out=out)
+        return pkv.device_error(), out
+
+    for cu_q, cu_k, max_q in (([0, 20, 40, 61], [0, 20, 56, 92], 21), ([-1, 20, 40, 60], [0, 20, 56, 92], 21),
+                              ([0, 20, 40, 60], [0, 20, 56, 92], 19), ([0, 20, 40, 60], [0, 19, 56, 92], 20),
+                              ([0, 20, 40, 60], [0, 20, 56, 200], 20)):
+        assert call(cu_q, cu_k, max_q, c.table)[0] == _lib.DERR_LEN_RANGE, (cu_q, cu_k, max_q)
+    bad = c.table.clone()
+    bad[1, 0], bad[1, 2] = -1, c.kc.shape[0]
+    bits, out = call([0, 20, 40, 60], [0, 20, 56, 92], 20, bad)
+    assert bits == _lib.DERR_BLOCK_RANGE
+    check(out[:20], ref[:20], dev[:20], torch.float16, 36)
+    check(out[40:], ref[40:], dev[40:], torch.float16, 36)
+
+
+def test_binding_refusals():
+    c = Case(66, [0, 16], [8, 8])
+    q, kc, vc, table, cu_q, cu_k = [x.cuda() for x in (c.q, c.kc, c.vc, c.table, c.cu_q, c.cu_k)]
+
+    def call(q=q, kc=kc, vc=vc, table=table, ks=1.0, **kw):
+        return pkv.paged_varlen_prefill_attn_fp8(q, kc, vc, table, cu_q, cu_k, 8, 24, 0.1, ks, 1.0, **kw)
+
+    with pytest.raises(TypeError, match="E4M3"):
+        call(kc=kc.float(), vc=vc.float())
+    with pytest.raises(TypeError, match="E4M3"):
+        call(kc=kc.view(torch.float8_e5m2), vc=vc.view(torch.float8_e5m2))
+    with pytest.raises(TypeError, match="q must be"):
+        call(q=q.float())
+    with pytest.raises(ValueError, match="block_tables rows"):
+        call(table=table[:1].contiguous())
+    with pytest.raises(ValueError, match="head_dim differs"):
+        call(kc=kc[..., :64].contiguous(), vc=vc[..., :64].contiguous())
+    for ks in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(_lib.PagedKVError):
+            call(ks=ks)
+    with pytest.raises(_lib.PagedKVError):  # G = 3
+        call(q=torch.zeros(16, 6, 128, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(call(kc=kc.view(torch.float8_e4m3fn), vc=vc.view(torch.float8_e4m3fn)), call())
+    assert pkv.device_error() == 0
+
+
+def test_captured_and_on_another_stream():
+    c = Case(67, [900, 40], [60, 30], block_size=64, hq=4, hkv=2)
+    q, kc, vc, table, cu_q, cu_k = [x.cuda() for x in (c.q, c.kc, c.vc, c.table, c.cu_q, c.cu_k)]
+    out, ws = torch.empty_like(q), pkv.prefill_workspace(2, 4, 2, 128, 60)
+
+    def step(**kw):
+        return pkv.paged_varlen_prefill_attn_fp8(q, kc, vc, table, cu_q, cu_k, 60, 960, c.scale, K_SCALE, V_SCALE,
+                                                 **dict(dict(workspace=ws, out=out), **kw))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    side = torch.cuda.Stream()
+    gen = torch.Generator().manual_seed(9)
+    for _ in range(2):
+        c.q = torch.randn(c.q.shape, generator=gen).bfloat16()
+        q.copy_(c.q)
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        other = step(stream=side, workspace=None, out=None)
+        torch.cuda.synchronize()
+        assert pkv.device_error() == 0 and torch.equal(out, other)
+        ref, dev = c.reference()
+        check(out, ref, dev, torch.float16, 960)
+
+
+def test_quantizing_store_then_chunks_then_decode():
+    # a prompt in two chunks and a decoded token over one E4M3 cache, each against the oracle
+    bs, hq, hkv, d = 16, 8, 2, 128
+    gen = torch.Generator().manual_seed(50)
+    k, v = [torch.randn(150, hkv, d, generator=gen).bfloat16() for _ in range(2)]
+    q = torch.randn(150, hq, d, generator=gen).bfloat16()
+    table = [7, 2, 9, 0, 4, 8, 1, 3, 6, 5]
+    kc, vc = [torch.full((10, bs, hkv, d), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    kd, vd = of8.dequantize(of8.quantize(as_np(k), K_SCALE), K_SCALE), of8.dequantize(of8.quantize(as_np(v), V_SCALE), V_SCALE)
+    ref, dev = omod.prefill_attention(as_np(q), [0, 150], [0, 150], d ** -0.5, k=kd, v=vd)
+    done = 0
+    for n in (100, 49):
+        meta = md.prefill_metadata([table], [done], [n], bs, always_tables=True)
+        gm, rows = md.to_device(meta, "cuda"), slice(done, done + n)
+        pkv.kv_store_fp8(k[rows].cuda(), v[rows].cuda(), kc, vc, gm["slot_mapping"], K_SCALE, V_SCALE)
+        out = pkv.paged_varlen_prefill_attn_fp8(q[rows].cuda(), kc, vc, gm["block_tables"], gm["cu_seqlens_q"],
+                                                gm["cu_seqlens_k"], n, done + n, d ** -0.5, K_SCALE, V_SCALE)
+        check(out, ref[rows], dev[rows], torch.float16, 150, f"chunk at {done}")
+        done += n
+    meta = md.to_device(md.decode_metadata([table], [150], bs), "cuda")
+    pkv.kv_store_fp8(k[149:].cuda(), v[149:].cuda(), kc, vc, meta["slot_mapping"], K_SCALE, V_SCALE)
+    out = pkv.paged_decode_attn_fp8(q[149:].cuda(), kc, vc, meta["block_tables"], meta["context_lens"], d ** -0.5, K_SCALE,
+                                    V_SCALE)
+    check(out, ref[149:], dev[149:], torch.float16, 150, "decoded token")
+    assert pkv.device_error() == 0
