@@ -385,9 +385,10 @@ size_t pkv_paged_varlen_prefill_workspace_bytes(int32_t batch, int32_t num_q_hea
  * range makes the score an infinity, or undefined where both signs occur; a
  * cap takes an infinity to +-softcap).  In the bf16 calls the
  * weights enter the P V product as bf16 and the row sums add the same rounded
- * weights.  Values of keys that no row of the sequence sees are never used;
- * V of a key that some rows see must be finite, since a row that does not see
- * it weighs it by 0.
+ * weights.  Values of keys before the least first_keys of a tile's rows (a
+ * decode call's tile is the one row), or past the sequence's end, are never
+ * used; V of every other key must be finite, since a row that does not see it
+ * weighs it by 0.
  *
  * paged_decode_attn_mod: pkv_paged_decode_attn with these modifiers (the query
  * sits at position context_lens[b] - 1); every other argument, the workspace
@@ -407,6 +408,7 @@ int pkv_paged_decode_attn_mod(void* out, const void* q, const void* k_cache, con
  * paged_varlen_prefill_attn_mod: pkv_paged_varlen_prefill_attn with the score
  * modifiers above; every other argument, the range checks, the optional
  * workspace and its size function are pkv_paged_varlen_prefill_attn's.
+ *   scale           finite and > 0
  * Supported: BF16; head_dim 64 or 128; G in {1, 2, 4, 8}; every block size
  * (a tile is gathered in pieces of gcd(block_size, 128) rows, so sizes that
  * share few factors of 2 with 128 take more copies).
@@ -434,6 +436,7 @@ int pkv_paged_varlen_prefill_attn_mod(void* out, const void* q, const void* k, c
  *   q, out          device, bf16 [total_q, num_q_heads, head_dim]
  *   k_cache,v_cache device, E4M3 bytes [num_blocks, block_size, num_kv_heads, head_dim]
  *   k_scale,v_scale finite and > 0
+ *   scale           finite and > 0
  *   other arguments, range checks, workspace and its size function as for
  *   pkv_paged_varlen_prefill_attn
  * The weights enter the P V product as f16 (the row sums add the same rounded

@@ -42,6 +42,12 @@ struct PrefillArgs {
 // 128 of at least 8.
 bool prefill_tc_supported(const PrefillArgs& a);
 int prefill_tc_launch(const PrefillArgs& a, cudaStream_t stream);
+// The same kernel with score modifiers (every block size).
+int prefill_tc_mod_launch(const PrefillArgs& a, cudaStream_t stream);
+// Parts a long pair of query tiles may run as, and the bytes of each of the
+// split's two counter arrays.
+int prefill_tc_parts(int batch, int num_kv_heads, int group, int max_seqlen_q, int sms);
+size_t prefill_tc_flag_bytes(long long items);
 // Workspace bytes that let the tcgen05 path split long items (0: never splits).
 size_t prefill_tc_workspace_bytes(int batch, int num_kv_heads, int group, int head_dim, int max_seqlen_q);
 

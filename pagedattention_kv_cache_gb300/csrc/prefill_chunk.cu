@@ -118,6 +118,7 @@ int check_args(const PrefillArgs& a, int max_seqlen_k) {
   if (a.head_dim != 128 && a.head_dim != 64) return PKV_EUNSUPPORTED;
   if (a.group != 1 && a.group != 2 && a.group != 4 && a.group != 8) return PKV_EUNSUPPORTED;
   if (a.causal != 0 && a.causal != 1) return PKV_EINVAL;
+  if (!(a.scale > 0.f) || isinf(a.scale)) return PKV_EINVAL;
   if (a.batch == 0 || a.max_seqlen_q == 0 || a.total_q == 0) return 1;
   if (!a.out || !a.q || !a.cu_q || !a.cu_k) return PKV_EINVAL;
   if (a.block_tables) {
@@ -177,7 +178,7 @@ extern "C" int pkv_paged_varlen_prefill_attn_mod(
   int st = PKV_OK;
   a.err = pkv::device_error_word(&st);
   if (st != PKV_OK) return st;
-  return launch_rows(a, false, stream);
+  return pkv::prefill_tc_mod_launch(a, stream);
 }
 
 extern "C" int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,

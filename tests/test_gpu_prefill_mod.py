@@ -149,6 +149,14 @@ def test_prefix_longer_than_the_sequence_is_full_attention():
     assert torch.equal(big, full)
 
 
+def test_no_modifier_matches_the_plain_call():
+    c = Case(34, CACHED, NEW)
+    out = c.compare()
+    plain = pkv.paged_varlen_prefill_attn(c.q.cuda(), c.cu_q.cuda(), c.cu_k.cuda(), max(c.new), max(c.totals), c.scale,
+                                          k_cache=c.kc.cuda(), v_cache=c.vc.cuda(), block_tables=c.table.cuda())
+    assert torch.equal(out, plain)
+
+
 @pytest.mark.parametrize("q_scale,cap", [(40.0, 5.0), (8.0, 20.0)])
 def test_scores_around_and_far_beyond_the_cap(q_scale, cap):
     Case(35, [100, 0], [140, 60], q_scale=q_scale).compare(cap=cap)

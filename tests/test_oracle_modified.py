@@ -110,16 +110,17 @@ def test_decode_mod_refusals(change, status):
 def _prefill_mod(**kw):
     a = dict(out=P, q=P, k=None, v=None, kc=P, vc=P, cq=P, ck=P, mq=8, mk=8, bt=P, mb=4, batch=2, tq=9, tk=0, hq=4,
              hkv=2, d=128, bs=16, nb=8, causal=1, cap=0.0, slopes=None, first=None, prefix=None, ws=None, wsb=0,
-             dtype=_lib.BF16)
+             dtype=_lib.BF16, scale=0.1)
     a.update(kw)
     return _lib_built().pkv_paged_varlen_prefill_attn_mod(
         a["out"], a["q"], a["k"], a["v"], a["kc"], a["vc"], a["cq"], a["ck"], a["mq"], a["mk"], a["bt"], a["mb"],
-        a["batch"], a["tq"], a["tk"], a["hq"], a["hkv"], a["d"], a["bs"], a["nb"], ctypes.c_float(0.1), a["causal"],
+        a["batch"], a["tq"], a["tk"], a["hq"], a["hkv"], a["d"], a["bs"], a["nb"], ctypes.c_float(a["scale"]), a["causal"],
         ctypes.c_float(a["cap"]), a["slopes"], a["first"], a["prefix"], a["ws"], a["wsb"], a["dtype"], None)
 
 
 @pytest.mark.parametrize("change,status", [
     (dict(cap=-1.0), "EINVAL"), (dict(cap=float("nan")), "EINVAL"), (dict(prefix=P, causal=0), "EINVAL"),
+    (dict(scale=0.0), "EINVAL"), (dict(scale=-1.0), "EINVAL"), (dict(scale=float("nan")), "EINVAL"),
     (dict(causal=2), "EINVAL"), (dict(bt=None), "EINVAL"), (dict(bt=None, k=P, v=P, tk=0), "EINVAL"),
     (dict(bs=0), "EINVAL"), (dict(nb=0), "EINVAL"), (dict(nb=1 << 30, bs=16), "EINVAL"), (dict(cq=None), "EINVAL"),
     (dict(hq=12, hkv=2), "EUNSUPPORTED"), (dict(d=80), "EUNSUPPORTED"), (dict(dtype=_lib.F32), "EUNSUPPORTED"),
@@ -130,17 +131,17 @@ def test_prefill_mod_refusals(change, status):
 
 def _prefill_fp8(**kw):
     a = dict(out=P, q=P, kc=P, vc=P, cq=P, ck=P, mq=8, mk=8, bt=P, mb=4, batch=2, tq=9, hq=4, hkv=2, d=128, bs=16, nb=8,
-             ks=1.0, vs=1.0, causal=1, ws=None, wsb=0)
+             ks=1.0, vs=1.0, causal=1, ws=None, wsb=0, scale=0.1)
     a.update(kw)
     return _lib_built().pkv_paged_varlen_prefill_attn_fp8(
         a["out"], a["q"], a["kc"], a["vc"], a["cq"], a["ck"], a["mq"], a["mk"], a["bt"], a["mb"], a["batch"], a["tq"],
-        a["hq"], a["hkv"], a["d"], a["bs"], a["nb"], ctypes.c_float(0.1), ctypes.c_float(a["ks"]),
+        a["hq"], a["hkv"], a["d"], a["bs"], a["nb"], ctypes.c_float(a["scale"]), ctypes.c_float(a["ks"]),
         ctypes.c_float(a["vs"]), a["causal"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("change,status", [
     (dict(ks=0.0), "EINVAL"), (dict(vs=float("nan")), "EINVAL"), (dict(ks=float("inf")), "EINVAL"),
-    (dict(bt=None), "EINVAL"), (dict(kc=None), "EINVAL"), (dict(causal=-1), "EINVAL"), (dict(mk=-1), "EINVAL"),
+    (dict(scale=float("inf")), "EINVAL"), (dict(bt=None), "EINVAL"), (dict(kc=None), "EINVAL"), (dict(causal=-1), "EINVAL"), (dict(mk=-1), "EINVAL"),
     (dict(hq=10, hkv=2), "EUNSUPPORTED"), (dict(d=96), "EUNSUPPORTED"), (dict(q=P + 2), "EALIGN"),
     (dict(tq=0), "OK"), (dict(batch=0), "OK")])
 def test_prefill_fp8_refusals(change, status):
