@@ -64,18 +64,19 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 std::once_flag g_encode_once;
 EncodeTiledFn g_encode = nullptr;
+
+void find_encode() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q{};
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+}
 }  // namespace
 
 int encode_bf16_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1,
                    uint32_t b2) {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-  });
+  std::call_once(g_encode_once, find_encode);
   if (!g_encode) return PKV_ECUDA;
   const cuuint64_t dims[3] = {d0, d1, d2};
   const cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
@@ -88,16 +89,22 @@ int encode_bf16_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ECUDA;
 }
 
+int encode_u8_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b2) {
+  std::call_once(g_encode_once, find_encode);
+  if (!g_encode) return PKV_ECUDA;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {d0, d0 * d1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(d0), 1, b2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base),
+                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PKV_OK : PKV_ECUDA;
+}
+
 int encode_paged_kv(void* map, const void* base, uint32_t block_size, uint32_t hkv, uint64_t num_blocks,
                     int elem_bytes) {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-  });
+  std::call_once(g_encode_once, find_encode);
   if (!g_encode || (elem_bytes != 1 && elem_bytes != 2)) return PKV_ECUDA;
   // dims innermost first: head_dim, token in block, KV head, block; the
   // token stride (all heads of a token) is larger than the head stride

@@ -38,6 +38,10 @@ constexpr size_t kWorkspaceCounterBytes = 64 * 1024;
 int encode_bf16_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1,
                    uint32_t b2);
 
+// Encodes a 3-D tensor map of bytes (rows of d0 <= 256 of them) for unswizzled
+// tiled TMA loads of boxes of d0 x 1 x b2.
+int encode_u8_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b2);
+
 // Encodes the 4-D tensor map of one paged K or V pool [num_blocks,
 // block_size, hkv, 128] whose box is 16 tokens of every KV head and 128 bytes
 // of head_dim, ordered (head, token) in shared memory with 128-byte swizzle:
@@ -160,6 +164,13 @@ __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gmem_src, u
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+// L2 policy for data other CTAs read too.
+__device__ __forceinline__ uint64_t l2_normal_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 

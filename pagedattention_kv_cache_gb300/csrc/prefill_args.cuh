@@ -44,6 +44,8 @@ bool prefill_tc_supported(const PrefillArgs& a);
 int prefill_tc_launch(const PrefillArgs& a, cudaStream_t stream);
 // The same kernel with score modifiers (every block size).
 int prefill_tc_mod_launch(const PrefillArgs& a, cudaStream_t stream);
+// The same kernel over an FP8 E4M3 cache (every block size).
+int prefill_tc_fp8_launch(const PrefillArgs& a, cudaStream_t stream);
 // Parts a long pair of query tiles may run as, and the bytes of each of the
 // split's two counter arrays.
 int prefill_tc_parts(int batch, int num_kv_heads, int group, int max_seqlen_q, int sms);

@@ -55,7 +55,7 @@ bool prefill_tc_supported(const PrefillArgs& a) {
 }
 
 int prefill_tc_launch(const PrefillArgs& a, cudaStream_t stream) {
-  return a.head_dim == 64 ? launch_d<64, false>(a, stream) : launch_d<128, false>(a, stream);
+  return a.head_dim == 64 ? launch_d<64, false, false>(a, stream) : launch_d<128, false, false>(a, stream);
 }
 
 }  // namespace pkv

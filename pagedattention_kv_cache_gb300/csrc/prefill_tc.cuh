@@ -63,7 +63,12 @@ constexpr int kBM = 128;   // rows per query tile
 constexpr int kBN = 128;   // keys per tile
 constexpr int kStages = 2; // K ring and V ring depth
 constexpr int kSoftmaxWarps = 8;  // per query tile: two threads per row, one per half of the key tile
-constexpr int kThreads = 32 * (2 + 2 * kSoftmaxWarps);
+constexpr int kWidenWarps = 2;    // kFp8: warps that widen E4M3 codes to f16
+template <bool kFp8>
+constexpr int threads() {
+  return 32 * (2 + 2 * kSoftmaxWarps + (kFp8 ? kWidenWarps : 0));
+}
+constexpr int kRawRows = 64;  // kFp8: keys per slot of the raw-code ring (half a tile)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;    // S_A at 0, S_B at 128
 constexpr uint32_t kColO = 256;  // O_A at 256, O_B at 384
@@ -74,20 +79,25 @@ constexpr uint32_t kRedBytes = 2 * 2 * 2 * kBM * 4;  // row maxima / sums exchan
 // Sizes for head dimension D (64 or 128): a row of D bf16 is D / 64 slabs of
 // 128 bytes (one 128-byte swizzle atom each), and each slab of a tile is a
 // TMA box of its own.
-template <int D>
+template <int D, bool kFp8 = false>
 struct Geo {
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   static constexpr int kSlabs = D / 64;
   static constexpr uint32_t kTileQ = kSlabs * kSlabQ;
   static constexpr uint32_t kTileKV = kSlabs * kSlabKV;
-  static constexpr uint32_t kRedOffset = 2 * kTileQ + 2 * kStages * kTileKV;
+  // kFp8: slots of raw codes, as many as shared memory holds beside the f16 rings
+  static constexpr int kRawSlots = kFp8 ? (D == 128 ? 3 : 6) : 0;
+  static constexpr uint32_t kRawSlot = kRawRows * D;
+  static constexpr uint32_t kRawOffset = 2 * kTileQ + 2 * kStages * kTileKV;
+  static constexpr uint32_t kRedOffset = kRawOffset + kRawSlots * kRawSlot;
   static constexpr uint32_t kBarOffset = kRedOffset + kRedBytes;
   static constexpr uint32_t kSmemBytes = kBarOffset + 256 + 1024;  // barriers + 1 KB for alignment
   // one CTA per SM even when two would fit (each holds all 512 TMEM columns)
   static constexpr uint32_t kLaunchSmem = kSmemBytes > 120 * 1024 ? kSmemBytes : 120 * 1024;
   static constexpr size_t kRecordBytes = static_cast<size_t>(kBM) * D * 4 + static_cast<size_t>(kBM) * 8;
 };
-static_assert(Geo<128>::kSmemBytes <= 227 * 1024, "shared memory plan exceeds an SM");
+static_assert(Geo<128>::kSmemBytes <= 227 * 1024 && Geo<128, true>::kSmemBytes <= 227 * 1024,
+              "shared memory plan exceeds an SM");
 constexpr float kRescaleLog2 = 8.0f;
 
 // Key-range split of long work items, used only when the pairs do not fill
@@ -121,7 +131,10 @@ enum Bar {
   O_FINAL = P_FULL + 2,  // per query tile
   V_TAIL = O_FINAL + 2,
   V_HEAD,  // kMod: the first V tile, once its rows before the first visible key are zeroed
-  NUM_BARS
+  Q_READY,  // kFp8: Q rewritten as scaled f16
+  RAW_FULL,
+  RAW_EMPTY = RAW_FULL + 6,
+  NUM_BARS = RAW_EMPTY + 6
 };
 static_assert(NUM_BARS * 8 + 16 <= 256, "barrier area too small");
 
@@ -166,6 +179,9 @@ struct TcParams {
   unsigned char* records;  // [same][P][record bytes]: O rows (D fp32 each), then m[kBM], l[kBM]
   ScoreMod mod;            // kMod
   TanhPoly tanh_poly;      // kMod with a cap
+  const unsigned char* k_codes;  // kFp8: the pools, for block sizes whose pieces are single rows
+  const unsigned char* v_codes;
+  float v_scale;
 };
 
 }  // namespace
@@ -216,6 +232,29 @@ __device__ __forceinline__ uint32_t exp2_pair_bf16(uint32_t s0, uint32_t s1, flo
       "mov.b64 {sa, sb}, %1;\n\t"
       "fma.rn.f32.bf16 sa, pa, one, sa;\n\t"
       "fma.rn.f32.bf16 sb, pb, one, sb;\n\t"
+      "mov.b64 %1, {sa, sb};\n\t}"
+      : "=r"(out), "+l"(acc)
+      : "r"(s0), "r"(s1), "f"(scale), "f"(neg_m));
+  return out;
+}
+
+// The same with f16 weights (kFp8): at most 2^8 (the lazy rescale), far inside f16's range.
+__device__ __forceinline__ uint32_t exp2_pair_f16(uint32_t s0, uint32_t s1, float scale, float neg_m, uint64_t& acc) {
+  uint32_t out;
+  asm("{\n\t.reg .b64 x, c, m;\n\t.reg .f32 a, b, sa, sb;\n\t.reg .b16 pa, pb, one;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 c, {%4, %4};\n\t"
+      "mov.b64 m, {%5, %5};\n\t"
+      "fma.rn.f32x2 x, x, c, m;\n\t"
+      "mov.b64 {a, b}, x;\n\t"
+      "ex2.approx.ftz.f32 a, a;\n\t"
+      "ex2.approx.ftz.f32 b, b;\n\t"
+      "cvt.rn.f16x2.f32 %0, b, a;\n\t"
+      "mov.b32 {pa, pb}, %0;\n\t"
+      "mov.b16 one, 0x3c00;\n\t"
+      "mov.b64 {sa, sb}, %1;\n\t"
+      "fma.rn.f32.f16 sa, pa, one, sa;\n\t"
+      "fma.rn.f32.f16 sb, pb, one, sb;\n\t"
       "mov.b64 %1, {sa, sb};\n\t}"
       : "=r"(out), "+l"(acc)
       : "r"(s0), "r"(s1), "f"(scale), "f"(neg_m));
@@ -318,8 +357,8 @@ __device__ __forceinline__ void modify_scores(const TcParams& p, uint32_t* r, fl
   }
 }
 
-template <int G, int D, bool kMod>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int G, int D, bool kMod, bool kFp8>
+__global__ void __launch_bounds__(threads<kFp8>(), 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TcParams p) {
   pdl_enter();
@@ -329,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kTileQ = Geo<D>::kTileQ;
   constexpr uint32_t kTileKV = Geo<D>::kTileKV;
   constexpr size_t kRecordBytes = Geo<D>::kRecordBytes;
+  static_assert(!(kMod && kFp8), "modifiers over an FP8 cache are not built");
   // blocks launch in linear order: x runs over (sequence, KV head), y over
   // query-tile pairs from the last (most keys under the causal mask) to the
   // first, and, with a workspace, over the key-range parts of each pair
@@ -393,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_a = max(0, min(n_tiles, n_need[0] - j0));
   const int n_b = max(0, min(n_tiles, n_need[1] - j0));
   // the last tile holds keys past nk: its V rows there are zeroed first
-  const bool v_tail = kMod ? n_tiles > 0 && (j0 + n_tiles) * kBN > nk : (j0 + n_tiles) * kBN > nk;
+  // (kFp8: the widening warps write those rows as zeros)
+  const bool v_tail = kFp8 ? false : kMod ? n_tiles > 0 && (j0 + n_tiles) * kBN > nk : (j0 + n_tiles) * kBN > nk;
   // kMod: the first tile holds keys before lo_pair: its V rows there are zeroed too
   const bool v_head = kMod && n_tiles > 0 && j0 * kBN < lo_pair;
 
@@ -402,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* sq = smem;  // Q_A, then Q_B
   unsigned char* sk = sq + 2 * kTileQ;
   unsigned char* sv = sk + kStages * kTileKV;
-  float* red = reinterpret_cast<float*>(smem + Geo<D>::kRedOffset);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Geo<D>::kBarOffset);
+  float* red = reinterpret_cast<float*>(smem + Geo<D, kFp8>::kRedOffset);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Geo<D, kFp8>::kBarOffset);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_ticket = abort_flag + 1;  // split tiles' tickets, one per query tile
@@ -414,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     mbar_init(&bars[Q_FULL], 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars[K_FULL + s], 1);
-      mbar_init(&bars[V_FULL + s], 1);
+      mbar_init(&bars[K_FULL + s], kFp8 ? 2 * kWidenWarps : 1);  // kFp8: every widening warp, for both halves
+      mbar_init(&bars[V_FULL + s], kFp8 ? 2 * kWidenWarps : 1);
       mbar_init(&bars[K_EMPTY + s], 1);
       mbar_init(&bars[V_EMPTY + s], 1);
     }
@@ -427,6 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars[O_FINAL + 1], 1);
     mbar_init(&bars[V_TAIL], 1);
     mbar_init(&bars[V_HEAD], 1);
+    if constexpr (kFp8) {
+      mbar_init(&bars[Q_READY], 2 * kSoftmaxWarps);
+      for (int s = 0; s < Geo<D, kFp8>::kRawSlots; ++s) {
+        mbar_init(&bars[RAW_FULL + s], 1);
+        mbar_init(&bars[RAW_EMPTY + s], kWidenWarps);
+      }
+    }
     fence_mbar_init();
   }
   const Waiter wait{abort_flag, p.err};
@@ -491,6 +539,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_arrive(full);
   };
+  // kFp8: the codes of half tile n (K and V tiles alternate, two halves each) into
+  // slot n % kRawSlots of the raw ring, a piece per lane of the calling warp
+  auto load_raw = [&](int n) {
+    constexpr int kSlots = kFp8 ? Geo<D, kFp8>::kRawSlots : 1;
+    const int slot = n % kSlots;
+    const int use = n / kSlots;
+    const bool is_v = (n >> 1) & 1;
+    uint64_t* full = &bars[RAW_FULL + slot];
+    if (use > 0) wait(&bars[RAW_EMPTY + slot], (use - 1) & 1);
+    __syncwarp();
+    unsigned char* dst = smem + Geo<D, kFp8>::kRawOffset + slot * Geo<D, kFp8>::kRawSlot;
+    const int key0 = (j0 + (n >> 2)) * kBN + (n & 1) * kRawRows;
+    for (int r = lane * p.piece_rows; r < kRawRows; r += 32 * p.piece_rows) {
+      const int key = key0 + r;
+      if (key >= nk) continue;
+      const int blk = key / p.block_size;
+      const int phys = __ldg(table + blk);
+      if (phys < 0 || phys >= p.num_blocks) {
+        raise_error(p.err, PKV_DERR_BLOCK_RANGE);
+        continue;
+      }
+      const int row = phys * p.block_size + (key - blk * p.block_size);
+      mbar_expect_tx(full, p.piece_rows * D);
+      if (p.piece_rows > 1)
+        tc::tma_load_3d(dst + r * D, is_v ? &tm_v : &tm_k, 0, g, row, full);
+      else  // a tensor copy of one 64-byte row could start off its 128-byte boundary
+        bulk_g2s(dst + r * D, (is_v ? p.v_codes : p.k_codes) + (static_cast<size_t>(row) * p.hkv + g) * D, D, full,
+                 l2_normal_policy());
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full);
+  };
+  const int n_raw_early = kFp8 ? min(4 * n_tiles, Geo<D, kFp8>::kRawSlots) : 0;
   // the producer thread issues Q and the first K/V tiles (stages still free)
   // before the CTA-wide sync, so their latency overlaps the TMEM allocation
   const int n_early = min(n_tiles, kStages);
@@ -506,19 +587,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tma_load_3d(sq + x * kTileQ + kSlabQ, &tm_q, 64, g * G, q_begin + tok0 + x * TQ, &bars[Q_FULL]);
     }
     mbar_arrive(&bars[Q_FULL]);
-    if constexpr (!kMod) {
+    if constexpr (!kMod && !kFp8) {
       for (int j = 0; j < n_early; ++j) {
         load_tile(j, false);
         load_tile(j, true);
       }
     }
   }
-  if constexpr (kMod) {
+  if constexpr (kMod || kFp8) {
     if (warp == 0) {
       __syncwarp();  // the barriers are initialised
-      for (int j = 0; j < n_early; ++j) {
-        load_tile(j, false);
-        load_tile(j, true);
+      if constexpr (kFp8) {
+        for (int n = 0; n < n_raw_early; ++n) load_raw(n);
+      } else {
+        for (int j = 0; j < n_early; ++j) {
+          load_tile(j, false);
+          load_tile(j, true);
+        }
       }
     }
   }
@@ -547,7 +632,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     };
-    if constexpr (kMod) {
+    if constexpr (kFp8) {
+      for (int n = n_raw_early; n < 4 * n_tiles; ++n) load_raw(n);
+    } else if constexpr (kMod) {
       if (parts > 1) {
         // a split part streams a key range no other CTA reads: request it into
         // L2 first, a piece per lane
@@ -623,8 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one elected lane issues the MMAs and commits.
     {
       const bool leader = tc::elect_one();
-      constexpr uint32_t idesc_qk = tc::idesc_bf16(kBM, kBN, 0, 0);
-      constexpr uint32_t idesc_pv = tc::idesc_bf16(kBM, kD, 0, 1);
+      constexpr uint32_t idesc_qk = kFp8 ? tc::idesc_f16(kBM, kBN, 0, 0) : tc::idesc_bf16(kBM, kBN, 0, 0);
+      constexpr uint32_t idesc_pv = kFp8 ? tc::idesc_f16(kBM, kD, 0, 1) : tc::idesc_bf16(kBM, kD, 0, 1);
       // descriptors of the first Q, K and V slabs; later ones differ only in the
       // start-address field (address >> 4), so they are reached by adding offset >> 4
       const uint64_t q_desc = tc::smem_desc(smem_u32(sq), 16, 1024);
@@ -655,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mma_ts_k128(tmem + kColO + x * kD, tmem + kColS + x * kBN, v_desc + ((st * kTileKV) >> 4), idesc_pv,
                           j > 0 ? 1u : 0u);
       };
-      wait(&bars[Q_FULL], 0);
+      wait(&bars[kFp8 ? Q_READY : Q_FULL], 0);
       if (n_tiles > 0) {
         wait.ready(&bars[K_FULL], 0);
         tc::fence_after_sync();
@@ -696,6 +783,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A's, when B has none here) is the last MMA issued
       wait(&bars[O_FINAL + (n_b > 0 ? 1 : 0)], 0);
     }
+  } else if (kFp8 && warp >= 2 + 2 * kSoftmaxWarps) {
+    // ------------------------------------------------------------ kFp8: widen codes to f16
+    // Sixteen codes (one 16-byte chunk) become two chunks of the swizzled f16
+    // row.  The lanes whose two chunks share banks with those of another lane of
+    // their group of eight (the row's second slab) store them in the other order.
+    constexpr int kSlots = kFp8 ? Geo<D, kFp8>::kRawSlots : 1;
+    constexpr int kRowChunks = D / 16;
+    constexpr int kIter = kRawRows * kRowChunks / (32 * kWidenWarps);
+    const int me = (warp - 2 - 2 * kSoftmaxWarps) * 32 + lane;
+    const int c = me % kRowChunks;
+    const bool second = D == 128 && c >= 4;
+    for (int n = 0; n < 4 * n_tiles; ++n) {
+      const int slot = n % kSlots;
+      const int j = n >> 2;
+      const bool is_v = (n >> 1) & 1;
+      const int half = n & 1;
+      const int st = j % kStages;
+      wait(&bars[RAW_FULL + slot], (n / kSlots) & 1);
+      const unsigned char* raw = smem + Geo<D, kFp8>::kRawOffset + slot * Geo<D, kFp8>::kRawSlot;
+      uint4 codes[kIter];
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) codes[i] = lds128(raw + (i * 32 * kWidenWarps + me) * 16);
+      if (half == 0 && j >= kStages) wait(&bars[(is_v ? V_EMPTY : K_EMPTY) + st], (j / kStages - 1) & 1);
+      unsigned char* dst = (is_v ? sv : sk) + st * kTileKV + (D == 128 ? (c >> 2) * kSlabKV : 0);
+      const int rows = nk - (j0 + j) * kBN;  // rows of the tile that hold keys
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const int rr = half * kRawRows + (i * 32 * kWidenWarps + me) / kRowChunks;
+        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+        uint32_t f[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          f[2 * u] = e4m3x2_to_f16x2(w[u]);
+          f[2 * u + 1] = e4m3x2_to_f16x2(w[u] >> 16);
+        }
+        uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
+        if (rr >= rows) lo = hi = make_uint4(0, 0, 0, 0);  // past the last key: whatever the slot holds
+        const int ch = 2 * (c & 3);
+        unsigned char* row = dst + rr * 128;
+        *reinterpret_cast<uint4*>(row + (((ch + (second ? 1 : 0)) ^ (rr & 7)) << 4)) = second ? hi : lo;
+        *reinterpret_cast<uint4*>(row + (((ch + (second ? 0 : 1)) ^ (rr & 7)) << 4)) = second ? lo : hi;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars[RAW_EMPTY + slot]);
+        mbar_arrive(&bars[(is_v ? V_FULL : K_FULL) + st]);
+      }
+    }
   } else {
     // ------------------------------------------------------------ softmax + epilogue of tile X, one half of the keys
     const int x = (warp - 2) / kSoftmaxWarps;
@@ -725,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       lo_most = __reduce_max_sync(0xffffffffu, lo_row);
       if (p.mod.slopes) slope = __ldg(p.mod.slopes + g * G + row % G) * kLog2e;
     }
-    const float mul = kMod && (p.mod.cap_log2 > 0.f || p.mod.slopes) ? 1.f : p.scale_log2;
+    float mul = kMod && (p.mod.cap_log2 > 0.f || p.mod.slopes) ? 1.f : p.scale_log2;
     const int bar_id = 1 + x;                 // the tile's 8 softmax warps
     const int pair_id = 3 + x * 4 + quad;     // the tile's two warps (one per half) on these 32 rows
     constexpr int kGroup = 32 * kSoftmaxWarps;
@@ -733,6 +869,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m_run = -INFINITY;
     float l_run = 0.f;  // this half's keys only
     uint32_t r[64];
+    if constexpr (kFp8) {
+      // Q becomes f16 in place, each row scaled by the power of two that puts its
+      // largest element in [2^14, 2^15): exact but for elements 2^28 times
+      // smaller than that.  The power comes off with the softmax scale.
+      if (n_x > 0) {
+        wait(&bars[Q_FULL], 0);
+        constexpr int kChunksHalf = D / 16;  // this half's 16-byte chunks of the row
+        unsigned char* q_row = sq + x * kTileQ + (D == 128 ? half * kSlabQ : 0) + row * 128;
+        auto q_chunk = [&](int i) {
+          const int ch = D == 128 ? i : half * kChunksHalf + i;
+          return reinterpret_cast<uint4*>(q_row + ((ch ^ (row & 7)) << 4));
+        };
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kChunksHalf; ++i) {
+          float f[8];
+          Chunk<__nv_bfloat16>::unpack(*q_chunk(i), f);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(f[u]));
+        }
+        *red_at(0, half) = top;
+        named_barrier_sync(pair_id, 64);
+        top = fmaxf(*red_at(0, 0), *red_at(0, 1));
+        const int exponent = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127 for zero and subnormals
+        const int ex = min(max(14 - exponent, -100), 100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        mul *= __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+        for (int i = 0; i < kChunksHalf; ++i) {
+          float f[8];
+          Chunk<__nv_bfloat16>::unpack(*q_chunk(i), f);
+          *q_chunk(i) = make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
+                                   pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[Q_READY]);
+    }
 
     for (int j = 0; j < n_x; ++j) {
       const int key0 = (j0 + j) * kBN + half * 64;  // first key of this half
@@ -786,7 +961,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // so the adds do not form one long chain)
       uint64_t l_pair[2] = {0, 0};
 #pragma unroll
-      for (int e = 0; e < 32; ++e) r[e] = exp2_pair_bf16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2]);
+      for (int e = 0; e < 32; ++e)
+        r[e] = kFp8 ? exp2_pair_f16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2])
+                    : exp2_pair_bf16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2]);
       tc::tmem_st32(s_addr + half * 32, r);
       float l_tile = 0.f;
 #pragma unroll
@@ -837,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // chunks per row) so the eight rows of a quarter-warp hit distinct banks;
       // then copied out 512 contiguous bytes (when G > 1) per warp instruction
       constexpr int kChunks = kD / 8;  // 16-byte chunks per row
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float inv = l_run > 0.f ? (kFp8 ? p.v_scale : 1.f) / l_run : 0.f;
       unsigned char* stage = sq + x * kTileQ;
 #pragma unroll
       for (int c = 0; c < kD / 64; ++c) {
@@ -942,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mq[q] = lq[q] > 0.f ? exp2f(mq[q] - mm) : 0.f;  // now the part's weight
             total += mq[q] * lq[q];
           }
-          const float inv = total > 0.f ? 1.f / total : 0.f;
+          const float inv = total > 0.f ? (kFp8 ? p.v_scale : 1.f) / total : 0.f;
 #pragma unroll
           for (int c = 0; c < kD / 64; ++c) {
             uint32_t o[32];
@@ -994,8 +1171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Rows per K/V copy of a paged tile: no piece crosses a block or a tile.
-inline int piece_rows(const PrefillArgs& a) {
-  int x = a.block_size, y = kBN;
+inline int piece_rows(const PrefillArgs& a, int tile) {
+  int x = a.block_size, y = tile;
   while (y) {
     const int r = x % y;
     x = y;
@@ -1004,19 +1181,24 @@ inline int piece_rows(const PrefillArgs& a) {
   return x;
 }
 
-template <int G, int D, bool kMod>
+template <int G, int D, bool kMod, bool kFp8>
 int launch(const PrefillArgs& a, cudaStream_t stream) {
   constexpr int TQ = kBM / G;
   constexpr int kD = D;
   alignas(64) CUtensorMap tm_q, tm_k, tm_v;
   if (encode_bf16_3d(&tm_q, a.q, kD, a.hq, a.total_q, 64, G, TQ) != PKV_OK) return PKV_ECUDA;
   const bool paged = a.block_tables != nullptr;
-  const int piece = paged ? piece_rows(a) : kBN;
+  const int piece = paged ? piece_rows(a, kFp8 ? kRawRows : kBN) : kBN;
   const void* kb = paged ? a.k_cache : a.k;
   const void* vb = paged ? a.v_cache : a.v;
   const uint64_t rows = paged ? static_cast<uint64_t>(a.num_blocks) * a.block_size : a.total_k;
-  if (encode_bf16_3d(&tm_k, kb, kD, a.hkv, rows, 64, 1, piece) != PKV_OK) return PKV_ECUDA;
-  if (encode_bf16_3d(&tm_v, vb, kD, a.hkv, rows, 64, 1, piece) != PKV_OK) return PKV_ECUDA;
+  if constexpr (kFp8) {
+    if (encode_u8_3d(&tm_k, kb, kD, a.hkv, rows, piece) != PKV_OK) return PKV_ECUDA;
+    if (encode_u8_3d(&tm_v, vb, kD, a.hkv, rows, piece) != PKV_OK) return PKV_ECUDA;
+  } else {
+    if (encode_bf16_3d(&tm_k, kb, kD, a.hkv, rows, 64, 1, piece) != PKV_OK) return PKV_ECUDA;
+    if (encode_bf16_3d(&tm_v, vb, kD, a.hkv, rows, 64, 1, piece) != PKV_OK) return PKV_ECUDA;
+  }
   TcParams p{};
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.cu_q = a.cu_q;
@@ -1036,6 +1218,12 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
   p.paged = paged ? 1 : 0;
   p.mod = a.mod;
   if constexpr (kMod) p.tanh_poly = make_tanh_poly(a.mod.cap_log2);
+  if constexpr (kFp8) {
+    p.scale_log2 *= a.k_scale;
+    p.v_scale = a.v_scale;
+    p.k_codes = static_cast<const unsigned char*>(a.k_cache);
+    p.v_codes = static_cast<const unsigned char*>(a.v_cache);
+  }
   p.piece_rows = piece;
   const int pairs = (a.max_seqlen_q + 2 * TQ - 1) / (2 * TQ);
   p.q_tiles = 2 * pairs;
@@ -1052,23 +1240,23 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
     p.ready = reinterpret_cast<int*>(ws + flags);
     p.records = ws + 2 * flags;
   }
-  auto kernel = prefill_tc_kernel<G, D, kMod>;
-  constexpr uint32_t kSmemBytes = Geo<D>::kLaunchSmem;
+  auto kernel = prefill_tc_kernel<G, D, kMod, kFp8>;
+  constexpr uint32_t kSmemBytes = Geo<D, kFp8>::kLaunchSmem;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
       cudaSuccess)
     return PKV_ECUDA;
   dim3 grid(a.batch * a.hkv, pairs * p.parts_max);
-  return launch_pdl(kernel, grid, dim3(kThreads), kSmemBytes, stream, tm_q, tm_k, tm_v, p) == cudaSuccess ? PKV_OK
+  return launch_pdl(kernel, grid, dim3(threads<kFp8>()), kSmemBytes, stream, tm_q, tm_k, tm_v, p) == cudaSuccess ? PKV_OK
                                                                                                   : PKV_ECUDA;
 }
 
-template <int D, bool kMod>
+template <int D, bool kMod, bool kFp8>
 int launch_d(const PrefillArgs& a, cudaStream_t stream) {
   switch (a.group) {
-    case 1: return launch<1, D, kMod>(a, stream);
-    case 2: return launch<2, D, kMod>(a, stream);
-    case 4: return launch<4, D, kMod>(a, stream);
-    default: return launch<8, D, kMod>(a, stream);
+    case 1: return launch<1, D, kMod, kFp8>(a, stream);
+    case 2: return launch<2, D, kMod, kFp8>(a, stream);
+    case 4: return launch<4, D, kMod, kFp8>(a, stream);
+    default: return launch<8, D, kMod, kFp8>(a, stream);
   }
 }
 

@@ -4,7 +4,7 @@
 namespace pkv {
 
 int prefill_tc_mod_launch(const PrefillArgs& a, cudaStream_t stream) {
-  return a.head_dim == 64 ? launch_d<64, true>(a, stream) : launch_d<128, true>(a, stream);
+  return a.head_dim == 64 ? launch_d<64, true, false>(a, stream) : launch_d<128, true, false>(a, stream);
 }
 
 }  // namespace pkv
