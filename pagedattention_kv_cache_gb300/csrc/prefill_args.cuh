@@ -42,9 +42,12 @@ struct PrefillArgs {
 // 128 of at least 8.
 bool prefill_tc_supported(const PrefillArgs& a);
 int prefill_tc_launch(const PrefillArgs& a, cudaStream_t stream);
-// The same kernel with score modifiers (every block size).
-int prefill_tc_mod_launch(const PrefillArgs& a, cudaStream_t stream);
-// The same kernel over an FP8 E4M3 cache (every block size).
+// The same kernel with score modifiers (masks; a cap; a distance bias; both),
+// and over an FP8 E4M3 cache; every block size.
+int prefill_tc_masked_launch(const PrefillArgs& a, cudaStream_t stream);
+int prefill_tc_capped_launch(const PrefillArgs& a, cudaStream_t stream);
+int prefill_tc_biased_launch(const PrefillArgs& a, cudaStream_t stream);
+int prefill_tc_capped_biased_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_fp8_launch(const PrefillArgs& a, cudaStream_t stream);
 // Parts a long pair of query tiles may run as, and the bytes of each of the
 // split's two counter arrays.

@@ -85,7 +85,9 @@ extern "C" int pkv_paged_varlen_prefill_attn_mod(
   int st = PKV_OK;
   a.err = pkv::device_error_word(&st);
   if (st != PKV_OK) return st;
-  return pkv::prefill_tc_mod_launch(a, stream);
+  if (a.mod.slopes)
+    return softcap > 0.f ? pkv::prefill_tc_capped_biased_launch(a, stream) : pkv::prefill_tc_biased_launch(a, stream);
+  return softcap > 0.f ? pkv::prefill_tc_capped_launch(a, stream) : pkv::prefill_tc_masked_launch(a, stream);
 }
 
 extern "C" int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,

@@ -54,8 +54,6 @@ bool prefill_tc_supported(const PrefillArgs& a) {
   return true;
 }
 
-int prefill_tc_launch(const PrefillArgs& a, cudaStream_t stream) {
-  return a.head_dim == 64 ? launch_d<64, false, false>(a, stream) : launch_d<128, false, false>(a, stream);
-}
+int prefill_tc_launch(const PrefillArgs& a, cudaStream_t stream) { return launch_form<kPlain>(a, stream); }
 
 }  // namespace pkv

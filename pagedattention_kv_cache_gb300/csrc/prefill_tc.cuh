@@ -40,12 +40,15 @@
 // Every wait is bounded; on a timeout the CTA records an error, skips the
 // remaining waits and still frees its TMEM.
 //
-// Two further forms of the kernel share this file (instantiated in
-// prefill_tc_mod.cu and prefill_tc_fp8.cu):
+// Further forms of the kernel share this file (Form below; each is instantiated
+// in a file of its own):
 //   kMod   score modifiers.  The key tiles of a pair start at its rows' least
 //          first key and end at its largest visible key (a prefix may reach past
-//          the causal end).  The softmax warps turn raw scores into modified
-//          ones in registers before the row maximum.
+//          the causal end).  Masks alone (kMasked), with a cap (kCapped), with a
+//          distance bias (kBiased) or both are separate instantiations: a thread
+//          holds its 64 scores in registers at a cap of 96, and one kernel that
+//          branched on the modifiers at run time spilled (a batch of 16 chunks,
+//          56 GFLOP, no modifier given: 70.7 us against the plain kernel's 62.6).
 //   kFp8   an E4M3 cache: raw codes arrive in a ring of 64-key half tiles, and
 //          two more warps widen them to f16 in the K and V rings.
 #pragma once
@@ -138,19 +141,37 @@ enum Bar {
 };
 static_assert(NUM_BARS * 8 + 16 <= 256, "barrier area too small");
 
-// c log2e tanh(x) on |x| <= 1 as x P(x^2), P of degree 4: the coefficients (each
-// twice, for two-lane arithmetic) minimise the largest error of x P(x^2), found
-// by a reweighted least-squares fit; it is 2.8e-6, 1.4e-4 in a score capped at 50,
-// which changes a weight by less than a thirtieth of its bf16 rounding.
+enum Form { kPlain, kMasked, kCapped, kBiased, kCappedBiased, kE4m3 };
+
+// c log2e tanh(k s) of a raw score s as s P(s^2), k = raw_to_x: P of degree 2
+// for |k s| <= 1/2 and of degree 4 for |k s| <= 1.  The coefficients of tanh
+// minimise the largest error of x P(x^2) (a reweighted least-squares fit); it is
+// 5.3e-6 and 2.8e-6, 2.7e-4 in a score capped at 50, which changes a weight by
+// less than a tenth of its bf16 rounding.  They are held twice each for
+// two-lane arithmetic, with c log2e and the powers of k folded in (k within
+// 2^+-12 keeps k^9 far inside fp32; other k take the exponentials).
 struct TanhPoly {
-  float2 c[5];
+  float2 near[3];
+  float2 wide[5];
+  float near_limit;  // raw scores up to here take `near`, up to wide_limit `wide`
+  float wide_limit;
 };
 
-inline TanhPoly make_tanh_poly(float cap_log2) {
-  constexpr double a[5] = {0.9999684691429138, -0.33265823125839233, 0.12922066450119019, -0.04329986125230789,
-                           0.008365885354578495};
-  TanhPoly p;
-  for (int i = 0; i < 5; ++i) p.c[i].x = p.c[i].y = static_cast<float>(a[i] * cap_log2);
+inline TanhPoly make_tanh_poly(float cap_log2, float k) {
+  constexpr double near[3] = {0.9999248302164969, -0.3308550498666596, 0.11254137113152551};
+  constexpr double wide[5] = {0.9999684694472680, -0.33265823169460657, 0.12922066707514057, -0.0432998613731271,
+                              0.008365885392756466};
+  TanhPoly p{};
+  p.near_limit = p.wide_limit = -1.f;
+  if (!(k >= 0x1p-12f && k <= 0x1p12f)) return p;
+  double power = static_cast<double>(cap_log2) * k;
+  for (int i = 0; i < 5; ++i) {
+    if (i < 3) p.near[i].x = p.near[i].y = static_cast<float>(near[i] * power);
+    p.wide[i].x = p.wide[i].y = static_cast<float>(wide[i] * power);
+    power *= static_cast<double>(k) * k;
+  }
+  p.near_limit = 0.5f / k;
+  p.wide_limit = 1.0f / k;
   return p;
 }
 
@@ -261,6 +282,25 @@ __device__ __forceinline__ uint32_t exp2_pair_f16(uint32_t s0, uint32_t s1, floa
   return out;
 }
 
+// exp2 of an exponent pair, rounded to bf16 and summed as in exp2_pair_bf16.
+__device__ __forceinline__ uint32_t exp2_of_pair_bf16(uint64_t x, uint64_t& acc) {
+  uint32_t out;
+  asm("{\n\t.reg .f32 a, b, sa, sb;\n\t.reg .b16 pa, pb, one;\n\t"
+      "mov.b64 {a, b}, %2;\n\t"
+      "ex2.approx.ftz.f32 a, a;\n\t"
+      "ex2.approx.ftz.f32 b, b;\n\t"
+      "cvt.rn.bf16x2.f32 %0, b, a;\n\t"
+      "mov.b32 {pa, pb}, %0;\n\t"
+      "mov.b16 one, 0x3f80;\n\t"
+      "mov.b64 {sa, sb}, %1;\n\t"
+      "fma.rn.f32.bf16 sa, pa, one, sa;\n\t"
+      "fma.rn.f32.bf16 sb, pb, one, sb;\n\t"
+      "mov.b64 %1, {sa, sb};\n\t}"
+      : "=r"(out), "+l"(acc)
+      : "l"(x));
+  return out;
+}
+
 // Maximum of three floats in one instruction.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -298,14 +338,26 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Raw scores of one row and 64 consecutive keys (r) to modified ones in the
-// exp2 domain, in place: cap, then distance bias.  dist0 = first key - the row's
-// position; `ahead`: some key may lie past the position (a prefix, or full
-// attention), so the distance's absolute value is taken.  Without a cap and
-// without slopes the scores stay raw (the caller scales them).
-__device__ __forceinline__ void modify_scores(const TcParams& p, uint32_t* r, float slope, int dist0, bool ahead) {
-  if (p.mod.cap_log2 > 0.f) {
-    // the polynomial holds while every |s / c| of the warp is at most 1; beyond, tanh by exponentials
+// s P(s^2) + c for two raw scores.
+template <int N>
+__device__ __forceinline__ uint64_t capped_pair(uint32_t s0, uint32_t s1, const float2 (&poly)[N], uint64_t c) {
+  const uint64_t s = pack2u(s0, s1);
+  const uint64_t y = mul2(s, s);
+  uint64_t t = pack2(poly[N - 1].x, poly[N - 1].y);
+#pragma unroll
+  for (int i = N - 2; i >= 0; --i) t = fma2(t, y, pack2(poly[i].x, poly[i].y));
+  return fma2(s, t, c);
+}
+
+// Raw scores of one row and 64 consecutive keys (r) to biased ones in the exp2
+// domain, in place: cap (kCap) or scale, then - slope |distance|.  dist0 = first
+// key - the row's position; `ahead`: some key may lie past the position (a
+// prefix, or full attention), so the distance's absolute value is taken.
+template <bool kCap>
+__device__ __forceinline__ void bias_scores(const TcParams& p, uint32_t* r, float slope, int dist0, bool ahead) {
+  const float d0 = static_cast<float>(dist0);
+  int tier = 0;  // of the cap: 0 exponentials, 1 wide, 2 near polynomial; 3 no cap
+  if constexpr (kCap) {
     float mx[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 64; e += 8) {
@@ -313,52 +365,45 @@ __device__ __forceinline__ void modify_scores(const TcParams& p, uint32_t* r, fl
       for (int u = 0; u < 4; ++u)
         mx[u] = max3(mx[u], fabsf(__uint_as_float(r[e + 2 * u])), fabsf(__uint_as_float(r[e + 2 * u + 1])));
     }
-    const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.mod.raw_to_x;
-    if (__any_sync(0xffffffffu, top > 1.f)) {
-#pragma unroll
-      for (int e = 0; e < 64; ++e)
-        r[e] = __float_as_uint(p.mod.cap_log2 * tanh_by_exp(__uint_as_float(r[e]) * p.mod.raw_to_x));
-    } else {
-      const uint64_t k2 = pack2(p.mod.raw_to_x, p.mod.raw_to_x);
-      uint64_t c[5];
-#pragma unroll
-      for (int i = 0; i < 5; ++i) c[i] = pack2(p.tanh_poly.c[i].x, p.tanh_poly.c[i].y);
-#pragma unroll
-      for (int e = 0; e < 64; e += 2) {
-        const uint64_t x = mul2(pack2u(r[e], r[e + 1]), k2);
-        const uint64_t y = mul2(x, x);
-        uint64_t t = fma2(c[4], y, c[3]);
-        t = fma2(t, y, c[2]);
-        t = fma2(t, y, c[1]);
-        t = fma2(t, y, c[0]);
-        unpack2u(mul2(x, t), r[e], r[e + 1]);
-      }
-    }
+    const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+    tier = !__any_sync(0xffffffffu, top > p.tanh_poly.near_limit)   ? 2
+           : !__any_sync(0xffffffffu, top > p.tanh_poly.wide_limit) ? 1
+                                                                     : 0;
+  } else {
+    tier = 3;
   }
-  if (p.mod.slopes) {
-    const float mul = p.mod.cap_log2 > 0.f ? 1.f : p.scale_log2;
-    const float d0 = static_cast<float>(dist0);
-    if (ahead) {
+  if (ahead || tier == 0) {
 #pragma unroll
-      for (int e = 0; e < 64; ++e)
-        r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), mul, -slope * fabsf(d0 + static_cast<float>(e))));
-    } else {
-      const uint64_t mul_2 = pack2(mul, mul), s2 = pack2(slope, slope), step = pack2(4.f, 4.f);
-      uint64_t d[2] = {pack2(d0, d0 + 1.f), pack2(d0 + 2.f, d0 + 3.f)};  // whole numbers: exact
-#pragma unroll
-      for (int e = 0; e < 64; e += 4) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          unpack2u(fma2(pack2u(r[e + 2 * u], r[e + 2 * u + 1]), mul_2, mul2(s2, d[u])), r[e + 2 * u], r[e + 2 * u + 1]);
-          d[u] = add2(d[u], step);
-        }
-      }
+    for (int e = 0; e < 64; ++e) {
+      const float s = __uint_as_float(r[e]);
+      const float x = kCap ? p.mod.cap_log2 * tanh_by_exp(s * p.mod.raw_to_x) : s * p.scale_log2;
+      r[e] = __float_as_uint(fmaf(-slope, fabsf(d0 + static_cast<float>(e)), x));
     }
+    return;
+  }
+  // keys up to the position: the bias is slope * (key - position), the distances whole numbers (exact)
+  const uint64_t s2 = pack2(slope, slope), step = pack2(4.f, 4.f);
+  auto run = [&](auto&& value) {
+    uint64_t d[2] = {pack2(d0, d0 + 1.f), pack2(d0 + 2.f, d0 + 3.f)};
+#pragma unroll
+    for (int e = 0; e < 64; e += 2) {
+      unpack2u(value(r[e], r[e + 1], mul2(s2, d[(e / 2) % 2])), r[e], r[e + 1]);
+      d[(e / 2) % 2] = add2(d[(e / 2) % 2], step);
+    }
+  };
+  if constexpr (kCap) {
+    if (tier == 2)
+      run([&](uint32_t a, uint32_t b, uint64_t bias) { return capped_pair(a, b, p.tanh_poly.near, bias); });
+    else
+      run([&](uint32_t a, uint32_t b, uint64_t bias) { return capped_pair(a, b, p.tanh_poly.wide, bias); });
+  } else {
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+    run([&](uint32_t a, uint32_t b, uint64_t bias) { return fma2(pack2u(a, b), scale2, bias); });
   }
 }
 
-template <int G, int D, bool kMod, bool kFp8>
-__global__ void __launch_bounds__(threads<kFp8>(), 1)
+template <int G, int D, Form kForm>
+__global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TcParams p) {
   pdl_enter();
@@ -368,7 +413,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
   constexpr uint32_t kTileQ = Geo<D>::kTileQ;
   constexpr uint32_t kTileKV = Geo<D>::kTileKV;
   constexpr size_t kRecordBytes = Geo<D>::kRecordBytes;
-  static_assert(!(kMod && kFp8), "modifiers over an FP8 cache are not built");
+  constexpr bool kFp8 = kForm == kE4m3;
+  constexpr bool kMod = kForm != kPlain && kForm != kE4m3;
+  constexpr bool kCap = kForm == kCapped || kForm == kCappedBiased;
+  constexpr bool kBias = kForm == kBiased || kForm == kCappedBiased;
   // blocks launch in linear order: x runs over (sequence, KV head), y over
   // query-tile pairs from the last (most keys under the causal mask) to the
   // first, and, with a workspace, over the key-range parts of each pair
@@ -393,9 +441,6 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
   const int tok0 = pt * 2 * TQ;  // first token of tile A; tile B starts TQ later
   if (tok0 >= nq) return;
   const int cached = nk - nq;
-  const int tid = threadIdx.x;
-  const int warp = tid / 32;
-  const int lane = tid % 32;
   // kMod: keys below prefix_end are visible to every row besides the causal ones;
   // no row of the pair sees a key before lo_pair
   int prefix_end = 0;
@@ -404,7 +449,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     if (p.mod.prefix_lens) prefix_end = min(max(__ldg(p.mod.prefix_lens + seq), 0), nk);
     if (p.mod.first_keys) {
       int least = INT32_MAX;
-      for (int t = tok0 + lane; t < min(nq, tok0 + 2 * TQ); t += 32)
+      for (int t = tok0 + static_cast<int>(threadIdx.x % 32); t < min(nq, tok0 + 2 * TQ); t += 32)
         least = min(least, __ldg(p.mod.first_keys + q_begin + t));
       lo_pair = max(__reduce_min_sync(0xffffffffu, least), 0);
     }
@@ -434,7 +479,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
   const int n_b = max(0, min(n_tiles, n_need[1] - j0));
   // the last tile holds keys past nk: its V rows there are zeroed first
   // (kFp8: the widening warps write those rows as zeros)
-  const bool v_tail = kFp8 ? false : kMod ? n_tiles > 0 && (j0 + n_tiles) * kBN > nk : (j0 + n_tiles) * kBN > nk;
+  const bool v_tail = !kFp8 && (!kMod || n_tiles > 0) && (j0 + n_tiles) * kBN > nk;
   // kMod: the first tile holds keys before lo_pair: its V rows there are zeroed too
   const bool v_head = kMod && n_tiles > 0 && j0 * kBN < lo_pair;
 
@@ -449,6 +494,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_ticket = abort_flag + 1;  // split tiles' tickets, one per query tile
 
+  const int tid = threadIdx.x;
+  const int warp = tid / 32;
+  const int lane = tid % 32;
   const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
 
   if (tid == 0) {
@@ -467,7 +515,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     mbar_init(&bars[O_FINAL], 1);
     mbar_init(&bars[O_FINAL + 1], 1);
     mbar_init(&bars[V_TAIL], 1);
-    mbar_init(&bars[V_HEAD], 1);
+    if constexpr (kMod) mbar_init(&bars[V_HEAD], 1);
     if constexpr (kFp8) {
       mbar_init(&bars[Q_READY], 2 * kSoftmaxWarps);
       for (int s = 0; s < Geo<D, kFp8>::kRawSlots; ++s) {
@@ -633,6 +681,18 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
       __syncwarp();
     };
     if constexpr (kFp8) {
+      if (parts > 1 && p.piece_rows > 1) {  // as below
+        for (int key = j0 * kBN + n_raw_early / 4 * kRawRows + lane * p.piece_rows; key < min((j0 + n_tiles) * kBN, nk);
+             key += 32 * p.piece_rows) {
+          const int blk = key / p.block_size;
+          const int phys = __ldg(table + blk);
+          if (phys < 0 || phys >= p.num_blocks) continue;  // raised by the load
+          const int row = phys * p.block_size + (key - blk * p.block_size);
+          tc::tma_prefetch_3d(&tm_k, 0, g, row);
+          tc::tma_prefetch_3d(&tm_v, 0, g, row);
+        }
+        __syncwarp();
+      }
       for (int n = n_raw_early; n < 4 * n_tiles; ++n) load_raw(n);
     } else if constexpr (kMod) {
       if (parts > 1) {
@@ -754,7 +814,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         if (leader && (n_x[x] == 0)) tc::commit(&bars[O_FINAL + x]);  // a tile with no key tile here: nothing to wait for
       for (int j = 0; j < n_tiles; ++j) {
         const int st = j % kStages;
-        if (v_head && j == 0) wait(&bars[V_HEAD], 0);
+        if constexpr (kMod) {
+          if (v_head && j == 0) wait(&bars[V_HEAD], 0);
+        }
         if (v_tail && j == n_tiles - 1)
           wait(&bars[V_TAIL], 0);
         else
@@ -785,15 +847,17 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     }
   } else if (kFp8 && warp >= 2 + 2 * kSoftmaxWarps) {
     // ------------------------------------------------------------ kFp8: widen codes to f16
-    // Sixteen codes (one 16-byte chunk) become two chunks of the swizzled f16
-    // row.  The lanes whose two chunks share banks with those of another lane of
-    // their group of eight (the row's second slab) store them in the other order.
+    // Each warp takes 32 rows of every half tile.  Sixteen codes (one 16-byte
+    // chunk) become two chunks of the swizzled f16 row.  A group of eight lanes
+    // takes two neighbouring rows, at head_dim 128 from opposite slabs: its loads
+    // cover 128 distinct bytes modulo 128, and its stores the even chunk positions
+    // of one row and the odd ones of the other, so neither has bank conflicts.
     constexpr int kSlots = kFp8 ? Geo<D, kFp8>::kRawSlots : 1;
-    constexpr int kRowChunks = D / 16;
-    constexpr int kIter = kRawRows * kRowChunks / (32 * kWidenWarps);
-    const int me = (warp - 2 - 2 * kSoftmaxWarps) * 32 + lane;
-    const int c = me % kRowChunks;
-    const bool second = D == 128 && c >= 4;
+    constexpr int kIter = D / 16;
+    const int me = warp - 2 - 2 * kSoftmaxWarps;
+    const int odd = (lane >> 2) & 1;
+    const int row0 = me * 32 + 2 * (lane >> 3) + odd;  // + 8 per two (head_dim 128) or one iterations
+    const uint32_t at0 = ((2 * (lane & 3)) ^ (row0 & 7)) << 4;
     for (int n = 0; n < 4 * n_tiles; ++n) {
       const int slot = n % kSlots;
       const int j = n >> 2;
@@ -801,30 +865,40 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
       const int half = n & 1;
       const int st = j % kStages;
       wait(&bars[RAW_FULL + slot], (n / kSlots) & 1);
-      const unsigned char* raw = smem + Geo<D, kFp8>::kRawOffset + slot * Geo<D, kFp8>::kRawSlot;
+      const unsigned char* raw =
+          smem + Geo<D, kFp8>::kRawOffset + slot * Geo<D, kFp8>::kRawSlot + row0 * D + (lane & 3) * 16;
       uint4 codes[kIter];
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) codes[i] = lds128(raw + (i * 32 * kWidenWarps + me) * 16);
-      if (half == 0 && j >= kStages) wait(&bars[(is_v ? V_EMPTY : K_EMPTY) + st], (j / kStages - 1) & 1);
-      unsigned char* dst = (is_v ? sv : sk) + st * kTileKV + (D == 128 ? (c >> 2) * kSlabKV : 0);
-      const int rows = nk - (j0 + j) * kBN;  // rows of the tile that hold keys
-#pragma unroll
       for (int i = 0; i < kIter; ++i) {
-        const int rr = half * kRawRows + (i * 32 * kWidenWarps + me) / kRowChunks;
-        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-        uint32_t f[8];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          f[2 * u] = e4m3x2_to_f16x2(w[u]);
-          f[2 * u + 1] = e4m3x2_to_f16x2(w[u] >> 16);
-        }
-        uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
-        if (rr >= rows) lo = hi = make_uint4(0, 0, 0, 0);  // past the last key: whatever the slot holds
-        const int ch = 2 * (c & 3);
-        unsigned char* row = dst + rr * 128;
-        *reinterpret_cast<uint4*>(row + (((ch + (second ? 1 : 0)) ^ (rr & 7)) << 4)) = second ? hi : lo;
-        *reinterpret_cast<uint4*>(row + (((ch + (second ? 0 : 1)) ^ (rr & 7)) << 4)) = second ? lo : hi;
+        if constexpr (D == 128)
+          codes[i] = lds128(raw + (i >> 1) * 8 * D + ((i & 1) ^ odd) * 64);
+        else
+          codes[i] = lds128(raw + i * 8 * D);
       }
+      if (half == 0 && j >= kStages) wait(&bars[(is_v ? V_EMPTY : K_EMPTY) + st], (j / kStages - 1) & 1);
+      unsigned char* dst = (is_v ? sv : sk) + st * kTileKV + (half * kRawRows + row0) * 128 + at0;
+      const int rows = nk - (j0 + j) * kBN - half * kRawRows - row0;  // row0 + i of the half tile holds a key: i < rows
+      auto widen = [&](bool partial) {
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+          uint32_t f[8];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) e4m3x4_to_f16x4(w[u], f[2 * u], f[2 * u + 1]);
+          const int step = D == 128 ? (i >> 1) * 8 : i * 8;
+          if (partial && step >= rows) {  // past the last key: whatever the slot holds
+#pragma unroll
+            for (int u = 0; u < 8; ++u) f[u] = 0u;
+          }
+          unsigned char* to = dst + step * 128 + (D == 128 ? ((i & 1) ^ odd) * kSlabKV : 0);
+          *reinterpret_cast<uint4*>(to) = make_uint4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<uint4*>(to + (at0 & 16 ? -16 : 16)) = make_uint4(f[4], f[5], f[6], f[7]);
+        }
+      };
+      if (nk >= (j0 + j) * kBN + (half + 1) * kRawRows)
+        widen(false);
+      else
+        widen(true);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
@@ -859,9 +933,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         lim = lo_row;
       }
       lo_most = __reduce_max_sync(0xffffffffu, lo_row);
-      if (p.mod.slopes) slope = __ldg(p.mod.slopes + g * G + row % G) * kLog2e;
+      if constexpr (kBias) slope = __ldg(p.mod.slopes + g * G + row % G) * kLog2e;
     }
-    float mul = kMod && (p.mod.cap_log2 > 0.f || p.mod.slopes) ? 1.f : p.scale_log2;
+    float mul = kBias ? 1.f : p.scale_log2;  // registers (raw, or biased scores) to exponents
     const int bar_id = 1 + x;                 // the tile's 8 softmax warps
     const int pair_id = 3 + x * 4 + quad;     // the tile's two warps (one per half) on these 32 rows
     constexpr int kGroup = 32 * kSoftmaxWarps;
@@ -909,6 +983,16 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
       if (lane == 0) mbar_arrive(&bars[Q_READY]);
     }
 
+    // kMod: keys the row does not see get -infinity; lo_row <= key <= lim in one unsigned comparison
+    bool masked = false;
+    auto hide = [&](int key0) {
+      const uint32_t span = static_cast<uint32_t>(lim - lo_row);
+      const uint32_t off = static_cast<uint32_t>(key0 - lo_row);
+#pragma unroll
+      for (int e = 0; e < 64; ++e)
+        if (off + e > span) r[e] = __float_as_uint(-INFINITY);
+    };
+
     for (int j = 0; j < n_x; ++j) {
       const int key0 = (j0 + j) * kBN + half * 64;  // first key of this half
       wait(&bars[S_FULL + x], j & 1);
@@ -919,16 +1003,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
       tc::tmem_ld32(s_addr + half * 64 + 32, r + 32);
       tc::tmem_wait_ld();
       if constexpr (kMod) {
+        if constexpr (kBias) bias_scores<kCap>(p, r, slope, key0 - pos, key0 + 63 > cached + tok_first);
         const int seen_by_all = p.causal ? max(cached + tok_first, prefix_end - 1) : nk - 1;
-        modify_scores(p, r, slope, key0 - pos, key0 + 63 > cached + tok_first);
-        if (key0 + 63 > seen_by_all || key0 < lo_most) {
-          // lo_row <= key <= lim in one unsigned comparison
-          const uint32_t span = static_cast<uint32_t>(lim - lo_row);
-          const uint32_t off = static_cast<uint32_t>(key0 - lo_row);
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (off + e > span) r[e] = __float_as_uint(-INFINITY);
-        }
+        masked = key0 + 63 > seen_by_all || key0 < lo_most;
+        if (masked) hide(key0);
       } else if (key0 + 63 > (p.causal ? cached + tok_first : nk - 1)) {
 #pragma unroll
         for (int e = 0; e < 64; ++e)
@@ -946,7 +1024,13 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
       *red_at(j & 1, half) = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
       named_barrier_sync(pair_id, 64);
       const float mt = fmaxf(*red_at(j & 1, 0), *red_at(j & 1, 1));
-      const float m_new = fmaxf(m_run, mt * mul);
+      float m_tile = mt * mul;
+      if constexpr (kCap && !kBias) {
+        // (a score that overflowed to -infinity is seen all the same, as - c)
+        const bool sees = lim >= (j0 + j) * kBN && lo_row < (j0 + j + 1) * kBN;
+        m_tile = sees ? p.mod.cap_log2 * tanh_by_exp(mt * p.mod.raw_to_x) : -INFINITY;
+      }
+      const float m_new = fmaxf(m_run, m_tile);
       const bool grow = m_new > m_run + kRescaleLog2 || (m_run == -INFINITY && m_new != -INFINITY);
       const bool rescale = __any_sync(0xffffffffu, grow);  // the same in both halves' warps
       float factor = 1.f;
@@ -960,10 +1044,37 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
       // row sum adds the same rounded values (two accumulators of two lanes,
       // so the adds do not form one long chain)
       uint64_t l_pair[2] = {0, 0};
+      if constexpr (kCap && !kBias) {
+        // tanh is monotone, so the maximum was taken on raw scores.  Below the
+        // polynomials' range s P(s^2) keeps falling, past c log2e tanh(-1/2) or
+        // tanh(-1); such keys' weights are below e^-20 either way when m is that far
+        // above, so only the largest score is compared with the range.
+        const bool none = m_run == -INFINITY;
+        const bool near = none || (mt <= p.tanh_poly.near_limit && m_run + 0.462f * p.mod.cap_log2 >= 20.f * kLog2e);
+        const bool wide = none || (mt <= p.tanh_poly.wide_limit && m_run + 0.761f * p.mod.cap_log2 >= 20.f * kLog2e);
+        const uint64_t neg_m = pack2(-m_use, -m_use);
+        if (__all_sync(0xffffffffu, near)) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        r[e] = kFp8 ? exp2_pair_f16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2])
-                    : exp2_pair_bf16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2]);
+          for (int e = 0; e < 32; ++e)
+            r[e] = exp2_of_pair_bf16(capped_pair(r[2 * e], r[2 * e + 1], p.tanh_poly.near, neg_m), l_pair[e % 2]);
+        } else if (__all_sync(0xffffffffu, wide)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            r[e] = exp2_of_pair_bf16(capped_pair(r[2 * e], r[2 * e + 1], p.tanh_poly.wide, neg_m), l_pair[e % 2]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            r[e] = __float_as_uint(p.mod.cap_log2 * tanh_by_exp(__uint_as_float(r[e]) * p.mod.raw_to_x));
+          if (masked) hide(key0);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = exp2_pair_bf16(r[2 * e], r[2 * e + 1], 1.f, -m_use, l_pair[e % 2]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          r[e] = kFp8 ? exp2_pair_f16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2])
+                      : exp2_pair_bf16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2]);
+      }
       tc::tmem_st32(s_addr + half * 32, r);
       float l_tile = 0.f;
 #pragma unroll
@@ -1181,8 +1292,9 @@ inline int piece_rows(const PrefillArgs& a, int tile) {
   return x;
 }
 
-template <int G, int D, bool kMod, bool kFp8>
+template <int G, int D, Form kForm>
 int launch(const PrefillArgs& a, cudaStream_t stream) {
+  constexpr bool kFp8 = kForm == kE4m3;
   constexpr int TQ = kBM / G;
   constexpr int kD = D;
   alignas(64) CUtensorMap tm_q, tm_k, tm_v;
@@ -1217,7 +1329,8 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
   p.causal = a.causal;
   p.paged = paged ? 1 : 0;
   p.mod = a.mod;
-  if constexpr (kMod) p.tanh_poly = make_tanh_poly(a.mod.cap_log2);
+  if constexpr (kForm == kCapped || kForm == kCappedBiased)
+    p.tanh_poly = make_tanh_poly(a.mod.cap_log2, a.mod.raw_to_x);
   if constexpr (kFp8) {
     p.scale_log2 *= a.k_scale;
     p.v_scale = a.v_scale;
@@ -1240,7 +1353,7 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
     p.ready = reinterpret_cast<int*>(ws + flags);
     p.records = ws + 2 * flags;
   }
-  auto kernel = prefill_tc_kernel<G, D, kMod, kFp8>;
+  auto kernel = prefill_tc_kernel<G, D, kForm>;
   constexpr uint32_t kSmemBytes = Geo<D, kFp8>::kLaunchSmem;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
       cudaSuccess)
@@ -1250,14 +1363,19 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
                                                                                                   : PKV_ECUDA;
 }
 
-template <int D, bool kMod, bool kFp8>
+template <int D, Form kForm>
 int launch_d(const PrefillArgs& a, cudaStream_t stream) {
   switch (a.group) {
-    case 1: return launch<1, D, kMod, kFp8>(a, stream);
-    case 2: return launch<2, D, kMod, kFp8>(a, stream);
-    case 4: return launch<4, D, kMod, kFp8>(a, stream);
-    default: return launch<8, D, kMod, kFp8>(a, stream);
+    case 1: return launch<1, D, kForm>(a, stream);
+    case 2: return launch<2, D, kForm>(a, stream);
+    case 4: return launch<4, D, kForm>(a, stream);
+    default: return launch<8, D, kForm>(a, stream);
   }
+}
+
+template <Form kForm>
+int launch_form(const PrefillArgs& a, cudaStream_t stream) {
+  return a.head_dim == 64 ? launch_d<64, kForm>(a, stream) : launch_d<128, kForm>(a, stream);
 }
 
 }  // namespace

@@ -3,8 +3,6 @@
 
 namespace pkv {
 
-int prefill_tc_fp8_launch(const PrefillArgs& a, cudaStream_t stream) {
-  return a.head_dim == 64 ? launch_d<64, false, true>(a, stream) : launch_d<128, false, true>(a, stream);
-}
+int prefill_tc_fp8_launch(const PrefillArgs& a, cudaStream_t stream) { return launch_form<kE4m3>(a, stream); }
 
 }  // namespace pkv
