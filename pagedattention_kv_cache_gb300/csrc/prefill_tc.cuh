@@ -200,6 +200,7 @@ struct TcParams {
   unsigned char* records;  // [same][P][record bytes]: O rows (D fp32 each), then m[kBM], l[kBM]
   ScoreMod mod;            // kMod
   TanhPoly tanh_poly;      // kMod with a cap
+  float bias_mul;          // slopes to the units of bias_scores
   const unsigned char* k_codes;  // kFp8: the pools, for block sizes whose pieces are single rows
   const unsigned char* v_codes;
   float v_scale;
@@ -349,14 +350,16 @@ __device__ __forceinline__ uint64_t capped_pair(uint32_t s0, uint32_t s1, const 
   return fma2(s, t, c);
 }
 
-// Raw scores of one row and 64 consecutive keys (r) to biased ones in the exp2
-// domain, in place: cap (kCap) or scale, then - slope |distance|.  dist0 = first
-// key - the row's position; `ahead`: some key may lie past the position (a
-// prefix, or full attention), so the distance's absolute value is taken.
+// Adds the distance bias to the scores of one row and 64 consecutive keys (r),
+// in place.  Without a cap the scores stay raw and `slope` is the bias per key in
+// raw units (slope / scale), so one fma per score suffices; with one (kCap) they
+// are capped too and end in the exp2 domain.  dist0 = first key - the row's
+// position; `ahead`: some key may lie past the position (a prefix, or full
+// attention), so the distance's absolute value is taken.
 template <bool kCap>
 __device__ __forceinline__ void bias_scores(const TcParams& p, uint32_t* r, float slope, int dist0, bool ahead) {
   const float d0 = static_cast<float>(dist0);
-  int tier = 0;  // of the cap: 0 exponentials, 1 wide, 2 near polynomial; 3 no cap
+  int tier = 2;  // of the cap: 0 exponentials, 1 wide, 2 near polynomial
   if constexpr (kCap) {
     float mx[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -369,14 +372,12 @@ __device__ __forceinline__ void bias_scores(const TcParams& p, uint32_t* r, floa
     tier = !__any_sync(0xffffffffu, top > p.tanh_poly.near_limit)   ? 2
            : !__any_sync(0xffffffffu, top > p.tanh_poly.wide_limit) ? 1
                                                                      : 0;
-  } else {
-    tier = 3;
   }
   if (ahead || tier == 0) {
 #pragma unroll
     for (int e = 0; e < 64; ++e) {
       const float s = __uint_as_float(r[e]);
-      const float x = kCap ? p.mod.cap_log2 * tanh_by_exp(s * p.mod.raw_to_x) : s * p.scale_log2;
+      const float x = kCap ? p.mod.cap_log2 * tanh_by_exp(s * p.mod.raw_to_x) : s;
       r[e] = __float_as_uint(fmaf(-slope, fabsf(d0 + static_cast<float>(e)), x));
     }
     return;
@@ -387,18 +388,17 @@ __device__ __forceinline__ void bias_scores(const TcParams& p, uint32_t* r, floa
     uint64_t d[2] = {pack2(d0, d0 + 1.f), pack2(d0 + 2.f, d0 + 3.f)};
 #pragma unroll
     for (int e = 0; e < 64; e += 2) {
-      unpack2u(value(r[e], r[e + 1], mul2(s2, d[(e / 2) % 2])), r[e], r[e + 1]);
+      unpack2u(value(r[e], r[e + 1], d[(e / 2) % 2]), r[e], r[e + 1]);
       d[(e / 2) % 2] = add2(d[(e / 2) % 2], step);
     }
   };
   if constexpr (kCap) {
     if (tier == 2)
-      run([&](uint32_t a, uint32_t b, uint64_t bias) { return capped_pair(a, b, p.tanh_poly.near, bias); });
+      run([&](uint32_t a, uint32_t b, uint64_t d) { return capped_pair(a, b, p.tanh_poly.near, mul2(s2, d)); });
     else
-      run([&](uint32_t a, uint32_t b, uint64_t bias) { return capped_pair(a, b, p.tanh_poly.wide, bias); });
+      run([&](uint32_t a, uint32_t b, uint64_t d) { return capped_pair(a, b, p.tanh_poly.wide, mul2(s2, d)); });
   } else {
-    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    run([&](uint32_t a, uint32_t b, uint64_t bias) { return fma2(pack2u(a, b), scale2, bias); });
+    run([&](uint32_t a, uint32_t b, uint64_t d) { return fma2(s2, d, pack2u(a, b)); });
   }
 }
 
@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     // kMod: the row sees keys lo_row .. lim; a row that sees none gets a range no key is in
     int lo_row = 0;
     int lo_most = 0;     // the largest lo_row of the warp
-    float slope = 0.f;   // per key of distance, exp2 domain
+    float slope = 0.f;   // per key of distance, in the units of bias_scores
     if constexpr (kMod) {
       lim = max(lim, prefix_end - 1);
       if (p.mod.first_keys && tok < nq) lo_row = max(__ldg(p.mod.first_keys + q_begin + tok), 0);
@@ -933,9 +933,9 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         lim = lo_row;
       }
       lo_most = __reduce_max_sync(0xffffffffu, lo_row);
-      if constexpr (kBias) slope = __ldg(p.mod.slopes + g * G + row % G) * kLog2e;
+      if constexpr (kBias) slope = __ldg(p.mod.slopes + g * G + row % G) * p.bias_mul;
     }
-    float mul = kBias ? 1.f : p.scale_log2;  // registers (raw, or biased scores) to exponents
+    float mul = kBias && kCap ? 1.f : p.scale_log2;  // scores as held in registers to exponents
     const int bar_id = 1 + x;                 // the tile's 8 softmax warps
     const int pair_id = 3 + x * 4 + quad;     // the tile's two warps (one per half) on these 32 rows
     constexpr int kGroup = 32 * kSoftmaxWarps;
@@ -1331,6 +1331,7 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
   p.mod = a.mod;
   if constexpr (kForm == kCapped || kForm == kCappedBiased)
     p.tanh_poly = make_tanh_poly(a.mod.cap_log2, a.mod.raw_to_x);
+  p.bias_mul = kForm == kBiased ? 1.f / a.scale : kLog2e;
   if constexpr (kFp8) {
     p.scale_log2 *= a.k_scale;
     p.v_scale = a.v_scale;
