@@ -54,6 +54,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cfloat>
 
 #include "prefill_args.cuh"
 #include "tcgen05.cuh"
@@ -147,12 +148,12 @@ enum Form { kPlain, kMasked, kCapped, kBiased, kCappedBiased, kE4m3 };
 // for |k s| <= 1/2 and of degree 4 for |k s| <= 1.  The coefficients of tanh
 // minimise the largest error of x P(x^2) (a reweighted least-squares fit); it is
 // 5.3e-6 and 2.8e-6, 2.7e-4 in a score capped at 50, which changes a weight by
-// less than a tenth of its bf16 rounding.  They are held twice each for
-// two-lane arithmetic, with c log2e and the powers of k folded in (k within
-// 2^+-12 keeps k^9 far inside fp32; other k take the exponentials).
+// less than a tenth of its bf16 rounding.  c log2e and the powers of k are
+// folded in (k within 2^+-12 keeps k^9 far inside fp32; other k take the
+// exponentials).
 struct TanhPoly {
-  float2 near[3];
-  float2 wide[5];
+  float near[3];
+  float wide[5];
   float near_limit;  // raw scores up to here take `near`, up to wide_limit `wide`
   float wide_limit;
 };
@@ -166,8 +167,8 @@ inline TanhPoly make_tanh_poly(float cap_log2, float k) {
   if (!(k >= 0x1p-12f && k <= 0x1p12f)) return p;
   double power = static_cast<double>(cap_log2) * k;
   for (int i = 0; i < 5; ++i) {
-    if (i < 3) p.near[i].x = p.near[i].y = static_cast<float>(near[i] * power);
-    p.wide[i].x = p.wide[i].y = static_cast<float>(wide[i] * power);
+    if (i < 3) p.near[i] = static_cast<float>(near[i] * power);
+    p.wide[i] = static_cast<float>(wide[i] * power);
     power *= static_cast<double>(k) * k;
   }
   p.near_limit = 0.5f / k;
@@ -341,12 +342,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // s P(s^2) + c for two raw scores.
 template <int N>
-__device__ __forceinline__ uint64_t capped_pair(uint32_t s0, uint32_t s1, const float2 (&poly)[N], uint64_t c) {
+__device__ __forceinline__ uint64_t capped_pair(uint32_t s0, uint32_t s1, const float (&poly)[N], uint64_t c) {
   const uint64_t s = pack2u(s0, s1);
   const uint64_t y = mul2(s, s);
-  uint64_t t = pack2(poly[N - 1].x, poly[N - 1].y);
+  uint64_t t = pack2(poly[N - 1], poly[N - 1]);
 #pragma unroll
-  for (int i = N - 2; i >= 0; --i) t = fma2(t, y, pack2(poly[i].x, poly[i].y));
+  for (int i = N - 2; i >= 0; --i) t = fma2(t, y, pack2(poly[i], poly[i]));
   return fma2(s, t, c);
 }
 
@@ -402,6 +403,14 @@ __device__ __forceinline__ void bias_scores(const TcParams& p, uint32_t* r, floa
   }
 }
 
+// kForm other than kPlain: a value the warp's lanes agree on, told to the compiler as
+// such (it can then live in a uniform register and leaves the 96 per thread alone).
+template <Form kForm>
+__device__ __forceinline__ int warp_uniform(int v) {
+  if constexpr (kForm == kPlain) return v;
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 template <int G, int D, Form kForm>
 __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -425,10 +434,10 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   const int pairs = p.q_tiles / 2;
   const int pt = pairs - 1 - static_cast<int>(blockIdx.y) / p.parts_max;
   const int part = static_cast<int>(blockIdx.y) % p.parts_max;
-  const int q_begin = __ldg(p.cu_q + seq);
-  const int nq = __ldg(p.cu_q + seq + 1) - q_begin;
-  const int k_begin = __ldg(p.cu_k + seq);
-  const int nk = __ldg(p.cu_k + seq + 1) - k_begin;
+  const int q_begin = warp_uniform<kForm>(__ldg(p.cu_q + seq));
+  const int nq = warp_uniform<kForm>(__ldg(p.cu_q + seq + 1)) - q_begin;
+  const int k_begin = warp_uniform<kForm>(__ldg(p.cu_k + seq));
+  const int nk = warp_uniform<kForm>(__ldg(p.cu_k + seq + 1)) - k_begin;
   // cu_seqlens must describe rows inside q / out (and the packed k / v), and no
   // sequence may have more rows than max_seqlen_q, which sized the grid: such a
   // sequence is skipped whole and raises the range bit
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   int prefix_end = 0;
   int lo_pair = 0;
   if constexpr (kMod) {
-    if (p.mod.prefix_lens) prefix_end = min(max(__ldg(p.mod.prefix_lens + seq), 0), nk);
+    if (p.mod.prefix_lens) prefix_end = warp_uniform<kForm>(min(max(__ldg(p.mod.prefix_lens + seq), 0), nk));
     if (p.mod.first_keys) {
       int least = INT32_MAX;
       for (int t = tok0 + static_cast<int>(threadIdx.x % 32); t < min(nq, tok0 + 2 * TQ); t += 32)
@@ -495,7 +504,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   volatile int* s_ticket = abort_flag + 1;  // split tiles' tickets, one per query tile
 
   const int tid = threadIdx.x;
-  const int warp = tid / 32;
+  const int warp = warp_uniform<kForm>(tid / 32);
   const int lane = tid % 32;
   const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
 
@@ -989,8 +998,11 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       const uint32_t span = static_cast<uint32_t>(lim - lo_row);
       const uint32_t off = static_cast<uint32_t>(key0 - lo_row);
 #pragma unroll
-      for (int e = 0; e < 64; ++e)
+      for (int e = 0; e < 64; ++e) {
+        // (a cap tells a key not seen, -infinity, from a score that overflowed)
+        if constexpr (kCap && !kBias) r[e] = __float_as_uint(fmaxf(__uint_as_float(r[e]), -FLT_MAX));
         if (off + e > span) r[e] = __float_as_uint(-INFINITY);
+      }
     };
 
     for (int j = 0; j < n_x; ++j) {
@@ -1021,14 +1033,16 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         for (int u = 0; u < 4; ++u)
           mx[u] = max3(mx[u], __uint_as_float(r[e + 2 * u]), __uint_as_float(r[e + 2 * u + 1]));
       }
-      *red_at(j & 1, half) = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+      float mx_half = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+      if constexpr (kCap && !kBias) {
+        if (!masked) mx_half = fmaxf(mx_half, -FLT_MAX);  // -infinity stands for "sees no key"
+      }
+      *red_at(j & 1, half) = mx_half;
       named_barrier_sync(pair_id, 64);
       const float mt = fmaxf(*red_at(j & 1, 0), *red_at(j & 1, 1));
       float m_tile = mt * mul;
       if constexpr (kCap && !kBias) {
-        // (a score that overflowed to -infinity is seen all the same, as - c)
-        const bool sees = lim >= (j0 + j) * kBN && lo_row < (j0 + j + 1) * kBN;
-        m_tile = sees ? p.mod.cap_log2 * tanh_by_exp(mt * p.mod.raw_to_x) : -INFINITY;
+        m_tile = mt == -INFINITY ? mt : p.mod.cap_log2 * tanh_by_exp(mt * p.mod.raw_to_x);
       }
       const float m_new = fmaxf(m_run, m_tile);
       const bool grow = m_new > m_run + kRescaleLog2 || (m_run == -INFINITY && m_new != -INFINITY);
@@ -1063,9 +1077,11 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
             r[e] = exp2_of_pair_bf16(capped_pair(r[2 * e], r[2 * e + 1], p.tanh_poly.wide, neg_m), l_pair[e % 2]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            r[e] = __float_as_uint(p.mod.cap_log2 * tanh_by_exp(__uint_as_float(r[e]) * p.mod.raw_to_x));
-          if (masked) hide(key0);
+          for (int e = 0; e < 64; ++e) {
+            const float s = __uint_as_float(r[e]);
+            const float z = p.mod.cap_log2 * tanh_by_exp(s * p.mod.raw_to_x);
+            r[e] = __float_as_uint(masked && s == -INFINITY ? s : z);
+          }
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = exp2_pair_bf16(r[2 * e], r[2 * e + 1], 1.f, -m_use, l_pair[e % 2]);
         }
