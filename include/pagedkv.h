@@ -407,7 +407,8 @@ int pkv_paged_decode_attn_mod(void* out, const void* q, const void* k_cache, con
 /*
  * paged_varlen_prefill_attn_mod: pkv_paged_varlen_prefill_attn with the score
  * modifiers above; every other argument, the range checks, the optional
- * workspace and its size function are pkv_paged_varlen_prefill_attn's.
+ * workspace and its size function are pkv_paged_varlen_prefill_attn's (short
+ * chunks: pkv_paged_short_chunk_workspace_bytes).
  *   scale           finite and > 0
  * Supported: BF16; head_dim 64 or 128; G in {1, 2, 4, 8}; every block size
  * (a tile is gathered in pieces of gcd(block_size, 128) rows, so sizes that
@@ -427,6 +428,18 @@ int pkv_paged_varlen_prefill_attn_mod(void* out, const void* q, const void* k, c
                                       pkv_stream_t stream);
 
 /*
+ * Bytes of workspace with which paged_varlen_prefill_attn_mod and
+ * paged_varlen_prefill_attn_fp8 run short chunks, max_seqlen_q * G <= 8 rows
+ * per KV head over a paged cache (drafted tokens of a verify pass, a prompt's
+ * last tokens), on the decode kernel, which divides the batch's keys evenly
+ * over the SMs; given less they run on the prefill kernel.  0 when the sizes
+ * are no short chunk (head_dim 128, num_kv_heads <= 8).  Zero-filled once; the
+ * same counter area as every split workspace.
+ */
+size_t pkv_paged_short_chunk_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                             int32_t head_dim, int32_t max_seqlen_q);
+
+/*
  * paged_varlen_prefill_attn_fp8: a chunk of new tokens per sequence over an
  * FP8 E4M3 cache (chunked prefill, or the drafted tokens of a verify pass):
  * the same result as pkv_paged_varlen_prefill_attn on the dequantized cache
@@ -438,7 +451,8 @@ int pkv_paged_varlen_prefill_attn_mod(void* out, const void* q, const void* k, c
  *   k_scale,v_scale finite and > 0
  *   scale           finite and > 0
  *   other arguments, range checks, workspace and its size function as for
- *   pkv_paged_varlen_prefill_attn
+ *   pkv_paged_varlen_prefill_attn (short chunks:
+ *   pkv_paged_short_chunk_workspace_bytes)
  * The weights enter the P V product as f16 (the row sums add the same rounded
  * weights), q as f16 after a power-of-two scaling of each row.
  * Supported: head_dim 64 or 128; G in {1, 2, 4, 8}; every block size.

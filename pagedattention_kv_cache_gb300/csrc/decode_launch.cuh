@@ -111,7 +111,7 @@ int launch(Params& p, int sms, cudaStream_t stream) {
                                                                                                        : PKV_ECUDA;
 }
 
-template <int G, int QL, typename TC = __nv_bfloat16, bool kMod = false>
+template <int G, int QL, typename TC = __nv_bfloat16, bool kMod = false, bool kVar = false>
 int launch_mma(Params& p, int sms, cudaStream_t stream) {
   constexpr int ES = static_cast<int>(sizeof(TC));
   constexpr int R = G * QL;
@@ -146,7 +146,7 @@ int launch_mma(Params& p, int sms, cudaStream_t stream) {
   p.t_stage = ls.t_stage;
   p.stages = ls.stages;
   p.stage_bytes = ls.stage_bytes;
-  auto kernel = paged_decode_mma_kernel<G, QL, TC, kMod>;
+  auto kernel = paged_decode_mma_kernel<G, QL, TC, kMod, kVar>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ls.smem)) !=
       cudaSuccess)
     return PKV_ECUDA;

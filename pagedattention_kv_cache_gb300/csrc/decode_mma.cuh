@@ -65,7 +65,9 @@ __host__ __device__ constexpr int mma_chunks_per_warp() {
   return std::is_same<TC, __nv_fp8_e4m3>::value ? 2 : 1;
 }
 
-template <int G, int QL, typename TC = __nv_bfloat16, bool kMod = false>
+// kVar: chunks of 1 to QL new tokens per sequence (cu_q / cu_k), R = G QL rows
+// of which a sequence uses its first G nq.
+template <int G, int QL, typename TC = __nv_bfloat16, bool kMod = false, bool kVar = false>
 __global__ void __launch_bounds__(288, 1)
     paged_decode_mma_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
@@ -121,7 +123,14 @@ __global__ void __launch_bounds__(288, 1)
     pkv::fence_mbar_init();
   }
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-    if (covered_len<kMod>(p, b) != 0) continue;
+    if (covered_len<kMod, kVar>(p, b) != 0) continue;
+    if constexpr (kVar) {
+      if (seq_len<kVar>(p, b) == 0) continue;  // no rows, or skipped
+      const int q0 = __ldg(p.cu_q + b), nq = __ldg(p.cu_q + b + 1) - q0;
+      T* o = static_cast<T*>(p.out) + static_cast<size_t>(q0) * p.hq * D;
+      for (int i = tid; i < nq * p.hq * D; i += blockDim.x) o[i] = static_cast<T>(0.0f);
+      continue;
+    }
     T* o = static_cast<T*>(p.out) + static_cast<size_t>(b) * rows_per_seq * D;
     for (int i = tid; i < rows_per_seq * D; i += blockDim.x) o[i] = static_cast<T>(0.0f);
   }
@@ -130,7 +139,7 @@ __global__ void __launch_bounds__(288, 1)
     plan_fixed<kMod>(p, plan);
     __syncthreads();
   } else {
-    plan_auto<kMod>(p, plan, sh);
+    plan_auto<kMod, kVar>(p, plan, sh);
   }
 
   if (warp == nw) {
@@ -147,7 +156,7 @@ __global__ void __launch_bounds__(288, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
       }
-      for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
+      for_each_segment<kMod, kVar>(p, plan, [&](const Segment& seg) -> bool {
         const int32_t* table = p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks;
         for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
           const int s = it % p.stages;
@@ -180,7 +189,7 @@ __global__ void __launch_bounds__(288, 1)
       });
       return;
     }
-    for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
+    for_each_segment<kMod, kVar>(p, plan, [&](const Segment& seg) -> bool {
       const int32_t* table = p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks;
       for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
         const int s = it % p.stages;
@@ -248,7 +257,7 @@ __global__ void __launch_bounds__(288, 1)
   const uint32_t v8b = cbase + (2 * c + 1) * rs + ((vq ^ (p.tma ? 2u * c + 1u : 0u)) << 4);
   int it = 0;
 
-  for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
+  for_each_segment<kMod, kVar>(p, plan, [&](const Segment& seg) -> bool {
     // Q as the A operand: rows r0 / r0 + 8, columns 16 kk + 2c (+1) and + 8
     // (bf16), or 16 kk + 4c (+1) and 16 kk + 4c + 2 (+3) as scaled f16 (FP8)
     uint32_t qf[8][4];
@@ -261,6 +270,11 @@ __global__ void __launch_bounds__(288, 1)
                                                       ((static_cast<size_t>(seg.b) * QL + rho / G) * p.hq + g * G +
                                                        rho % G) * D)
                   : nullptr;
+      if constexpr (kVar)
+        qrow = rho / G < seg.nq ? reinterpret_cast<const uint32_t*>(
+                                      static_cast<const T*>(p.q) +
+                                      ((static_cast<size_t>(seg.q0) + rho / G) * p.hq + g * G + rho % G) * D)
+                                : nullptr;
       if constexpr (kFp8) {
         float amax = 0.f;
 #pragma unroll
@@ -306,7 +320,17 @@ __global__ void __launch_bounds__(288, 1)
       f.r[3] = kT ? 0u : qf[kk][3];
       return f;
     };
-    const int lim0 = seg.ctx - QL + (r0 < R ? r0 / G : 0);
+    int lim0 = seg.ctx - QL + (r0 < R ? r0 / G : 0);
+    int lo0 = seg.lo;  // kMod: the row's own first visible key
+    if constexpr (kVar) {
+      lim0 = seg.ctx - 1;
+      if (p.causal) {
+        lim0 = seg.ctx - seg.nq + r0 / G;
+        if (kMod && p.mod.prefix_lens) lim0 = max(lim0, min(__ldg(p.mod.prefix_lens + seg.b), seg.ctx) - 1);
+      }
+      if (kMod && p.mod.first_keys && r0 / G < seg.nq) lo0 = max(__ldg(p.mod.first_keys + seg.q0 + r0 / G), 0);
+    }
+    const int pos0 = kVar ? seg.ctx - seg.nq + r0 / G : seg.ctx - 1;  // the row's position
     const int lim1 = seg.ctx - QL + (r0 + 8 < R ? (r0 + 8) / G : 0);
     float o[NO][4];
 #pragma unroll
@@ -316,10 +340,11 @@ __global__ void __launch_bounds__(288, 1)
     float m[2] = {-INFINITY, -INFINITY};
     float l[2] = {0.f, 0.f};
     // distance bias of the fragment rows' heads, per key of distance, in the exp2 domain
-    static_assert(!kMod || (QL == 1 && kT), "score modifiers: decode only");
+    static_assert(!kMod || ((QL == 1 || kVar) && kT), "score modifiers: decode and chunks of at most 8 rows");
+    static_assert(!kVar || kT, "chunks of at most 8 rows");
     float slope = 0.f;
     if constexpr (kMod) {
-      if (p.mod.slopes && r0 < R) slope = __ldg(p.mod.slopes + g * G + r0) * pkv::kLog2e;
+      if (p.mod.slopes && r0 < R) slope = __ldg(p.mod.slopes + g * G + r0 % G) * pkv::kLog2e;
     }
 
     for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
@@ -400,13 +425,12 @@ __global__ void __launch_bounds__(288, 1)
             for (int e = 0; e < 2 * HH; ++e) {
               const int key = nb * 8 + 2 * c + (e & 1);
               float x = sacc[sub][nb][e] * qmul[e >> 1];
-              bool visible = key < nv && (QL == 1 || t + tt0 + key <= ((e < 2) ? lim0 : lim1));
+              bool visible = key < nv && ((QL == 1 && !kVar) || t + tt0 + key <= ((e < 2) ? lim0 : lim1));
               if constexpr (kMod) {
                 if (p.mod.cap_log2 > 0.f)
                   x = p.mod.cap_log2 * pkv::tanh_by_exp(sacc[sub][nb][e] * p.mod.raw_to_x);
-                // the query sits at ctx - 1, so the distance is ctx - 1 - t >= 0
-                x = fmaf(slope, static_cast<float>(t + tt0 + key - (seg.ctx - 1)), x);
-                visible = visible && t + tt0 + key >= seg.lo;
+                x = fmaf(-slope, fabsf(static_cast<float>(t + tt0 + key - pos0)), x);
+                visible = visible && t + tt0 + key >= lo0;
               }
               x = visible ? x : -INFINITY;
               sacc[sub][nb][e] = x;
@@ -605,12 +629,13 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int row = 2 * c + i;
-          if (row >= R) continue;
+          if (row >= R || (kVar && row / G >= seg.nq)) continue;
           const int head = (row / G) * p.hq + g * G + row % G;
           const float vs = kFp8 ? p.v_scale : 1.f;
           if (seg.nparts == 1) {
-            const float ws = vs / lr[i];
-            T* orow = static_cast<T*>(p.out) + (static_cast<size_t>(seg.b) * rows_per_seq + head) * D;
+            const float ws = kVar && lr[i] == 0.f ? 0.f : vs / lr[i];  // kVar: a row may see nothing
+            T* orow = static_cast<T*>(p.out) + ((kVar ? static_cast<size_t>(seg.q0) * p.hq
+                                                      : static_cast<size_t>(seg.b) * rows_per_seq) + head) * D;
             if constexpr (kFp8) {
               // this lane's 16 outputs are contiguous: head_dim 16 q4 .. 16 q4 + 15
               uint32_t w[8];
@@ -726,7 +751,7 @@ __global__ void __launch_bounds__(288, 1)
         }
       }
     }
-    if (seg.nparts > 1) combine_if_last<T, D>(p, seg, rows_per_seq, sh_flag, nthreads_c);
+    if (seg.nparts > 1) combine_if_last<T, D, kVar>(p, seg, rows_per_seq, sh_flag, nthreads_c);
     return true;
   });
 }

@@ -84,6 +84,13 @@ struct Params {
   int align;  // split points fall on multiples of this many tokens of a sequence (0 or 1: anywhere)
   int tma;    // mma kernel: stages filled by 4-D tensor copies of 16-token boxes (block_size % 16 == 0)
   pkv::ScoreMod mod;  // score modifiers (kernels instantiated with kMod)
+  // chunks of new tokens (kernels instantiated with kVar): sequence b has the
+  // query rows cu_q[b] .. cu_q[b + 1] - 1, at most QL tokens, and cu_k's keys
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int total_q;
+  int max_seqlen_q;
+  int causal;
 };
 
 // One contiguous piece of work: tokens [t0, t1) of sequence b.
@@ -94,7 +101,8 @@ struct Segment {
   int nparts;      // CTAs sharing sequence b
   int first_slot;  // workspace slot of the sequence's first part
   int slot;        // this part's slot
-  int lo;          // first visible key (0 without modifiers)
+  int lo;          // first visible key of any row (0 without modifiers)
+  int q0, nq;      // kVar: the sequence's first query token, and how many there are
 };
 
 // Bounded pipeline wait.  On a timeout the CTA raises PKV_DERR_WAIT_TIMEOUT,
@@ -123,12 +131,36 @@ __device__ __forceinline__ int context_len(const Params& p, int b) {
   return n;
 }
 
-// First visible key of sequence b of length n (kMod with first_keys; else 0), in [0, n].
-template <bool kMod>
+// Keys of sequence b: its context length; for chunks the keys that cu_k gives
+// it, 0 where it has no query rows or where cu_q / cu_k do not describe rows
+// inside q and keys inside its table row (then skipped, and the range bit set).
+template <bool kVar>
+__device__ __forceinline__ int seq_len(const Params& p, int b) {
+  if constexpr (!kVar) return context_len(p, b);
+  const int q0 = __ldg(p.cu_q + b), nq = __ldg(p.cu_q + b + 1) - q0;
+  const int nk = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+  if (q0 < 0 || nq < 0 || nk < nq || static_cast<long long>(q0) + nq > p.total_q || nq > p.max_seqlen_q ||
+      static_cast<long long>(nk) > static_cast<long long>(p.max_blocks) * p.block_size) {
+    pkv::raise_error(p.err, PKV_DERR_LEN_RANGE);
+    return 0;
+  }
+  return nq == 0 ? 0 : nk;
+}
+
+// First visible key of sequence b of length n (kMod with first_keys: the least
+// of its rows'; else 0), in [0, n].
+template <bool kMod, bool kVar>
 __device__ __forceinline__ int first_key(const Params& p, int b, int n) {
   if constexpr (!kMod) return 0;
-  if (!p.mod.first_keys) return 0;
-  return min(max(__ldg(p.mod.first_keys + b), 0), n);
+  if (!p.mod.first_keys || n == 0) return 0;
+  int least;
+  if constexpr (kVar) {
+    least = n;
+    for (int r = __ldg(p.cu_q + b); r < __ldg(p.cu_q + b + 1); ++r) least = min(least, __ldg(p.mod.first_keys + r));
+  } else {
+    least = __ldg(p.mod.first_keys + b);
+  }
+  return min(max(least, 0), n);
 }
 
 // Where the tokens a CTA plan covers begin: the first visible key, down to the
@@ -137,11 +169,11 @@ __device__ __forceinline__ int first_key(const Params& p, int b, int n) {
 __device__ __forceinline__ int cover_start(const Params& p, int lo) { return lo - lo % align_tokens(p); }
 
 // Tokens of sequence b that the plan covers: its context, from cover_start on; 0 when it sees no key.
-template <bool kMod>
+template <bool kMod, bool kVar = false>
 __device__ __forceinline__ int covered_len(const Params& p, int b) {
-  const int n = context_len(p, b);
+  const int n = seq_len<kVar>(p, b);
   if constexpr (!kMod) return n;
-  const int lo = first_key<kMod>(p, b, n);
+  const int lo = first_key<kMod, kVar>(p, b, n);
   return lo >= n ? 0 : n - cover_start(p, lo);
 }
 
@@ -158,7 +190,7 @@ struct Plan {
 
 // Block-wide sum over context lengths and search for the first sequence
 // overlapping this CTA's token range (automatic mode).
-template <bool kMod>
+template <bool kMod, bool kVar = false>
 __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
   const int tid = threadIdx.x;
   const int nthreads = blockDim.x;
@@ -167,7 +199,7 @@ __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
   if (p.batch <= nthreads) {
     // one pass when the batch fits the block: each thread loads one length,
     // one block-wide scan gives the total and the prefix that holds `start`
-    const long long n = tid < p.batch ? round_up(covered_len<kMod>(p, tid), A) : 0;
+    const long long n = tid < p.batch ? round_up(covered_len<kMod, kVar>(p, tid), A) : 0;
     long long incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -200,7 +232,7 @@ __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
     return;
   }
   long long local = 0;
-  for (int b = tid; b < p.batch; b += nthreads) local += round_up(covered_len<kMod>(p, b), A);
+  for (int b = tid; b < p.batch; b += nthreads) local += round_up(covered_len<kMod, kVar>(p, b), A);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) local += __shfl_xor_sync(0xffffffffu, local, off);
   if (tid % 32 == 0) sh[tid / 32] = local;
@@ -221,7 +253,7 @@ __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
   long long running = 0;
   for (int base = 0; base < p.batch; base += nthreads) {
     const int b = base + tid;
-    const long long n = b < p.batch ? round_up(covered_len<kMod>(p, b), A) : 0;
+    const long long n = b < p.batch ? round_up(covered_len<kMod, kVar>(p, b), A) : 0;
     long long incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -258,7 +290,7 @@ __device__ void plan_fixed(const Params& p, Plan& plan) {
   plan.fixed_valid = false;
   if (b >= p.batch) return;
   const int ctx = context_len(p, b);
-  const int lo = first_key<kMod>(p, b, ctx);
+  const int lo = first_key<kMod, false>(p, b, ctx);
   if (lo >= ctx) return;
   const int start = kMod ? cover_start(p, lo) : 0;
   const int n = ctx - start;
@@ -266,12 +298,12 @@ __device__ void plan_fixed(const Params& p, Plan& plan) {
   const int t0 = j * chunk;
   if (t0 >= n) return;
   const int t1 = t0 + chunk < n ? t0 + chunk : n;
-  plan.fixed = Segment{b, ctx, start + t0, start + t1, (n + chunk - 1) / chunk, b * S, b * S + j, lo};
+  plan.fixed = Segment{b, ctx, start + t0, start + t1, (n + chunk - 1) / chunk, b * S, b * S + j, lo, 0, 0};
   plan.fixed_valid = true;
 }
 
 // Calls fn(segment) for every segment of this CTA, in order.
-template <bool kMod, typename Fn>
+template <bool kMod, bool kVar, typename Fn>
 __device__ __forceinline__ bool for_each_segment(const Params& p, const Plan& plan, Fn&& fn) {
   if (p.num_splits > 0) {
     if (plan.fixed_valid) return fn(plan.fixed);
@@ -283,8 +315,8 @@ __device__ __forceinline__ bool for_each_segment(const Params& p, const Plan& pl
   const int A = align_tokens(p);
   long long cu = plan.cu_first;
   for (int b = plan.b_first; b < p.batch && cu < plan.end; ++b) {
-    const int ctx = context_len(p, b);
-    const int lo = first_key<kMod>(p, b, ctx);
+    const int ctx = seq_len<kVar>(p, b);
+    const int lo = first_key<kMod, kVar>(p, b, ctx);
     const int start = kMod ? cover_start(p, lo) : 0;
     const int n = lo < ctx ? ctx - start : 0;
     const long long np = round_up(n, A);
@@ -294,7 +326,11 @@ __device__ __forceinline__ bool for_each_segment(const Params& p, const Plan& pl
       const int c0 = static_cast<int>(cu / plan.per);
       const int c1 = static_cast<int>((cu + np - 1) / plan.per);
       Segment seg{b, ctx, start + static_cast<int>(s0 - cu), start + static_cast<int>(s1 - cu < n ? s1 - cu : n),
-                  c1 - c0 + 1, c0 + b, static_cast<int>(blockIdx.x) + b, lo};
+                  c1 - c0 + 1, c0 + b, static_cast<int>(blockIdx.x) + b, lo, 0, 0};
+      if constexpr (kVar) {
+        seg.q0 = __ldg(p.cu_q + b);
+        seg.nq = __ldg(p.cu_q + b + 1) - seg.q0;
+      }
       if (!fn(seg)) return false;
     }
     cu += np;
@@ -312,7 +348,7 @@ __device__ __forceinline__ bool for_each_segment(const Params& p, const Plan& pl
 // rescaled whenever a part raises m (every lane keeps the same m and l).
 // Parts are loaded kJ at a time, every load of a batch issued before the
 // first is used, so a batch costs one round trip to L2.
-template <typename T, int D>
+template <typename T, int D, bool kVar>
 __device__ __forceinline__ void merge_parts(const Params& p, const Segment& seg, int rows_per_seq, int first,
                                             int step, int count, bool final, int nthreads_c) {
   constexpr int RW = 2;  // rows a warp merges together
@@ -322,12 +358,15 @@ __device__ __forceinline__ void merge_parts(const Params& p, const Segment& seg,
   const int warp = tid / 32;
   const int lane = tid % 32;
   const int nwarps = nthreads_c / 32;
-  T* out = static_cast<T*>(p.out) + static_cast<size_t>(seg.b) * rows_per_seq * D;
+  // a chunk's rows are its own nq tokens' (records are rows_per_seq apart all the same)
+  T* out = static_cast<T*>(p.out) +
+           (kVar ? static_cast<size_t>(seg.q0) * p.hq : static_cast<size_t>(seg.b) * rows_per_seq) * D;
+  const int rows = kVar ? seg.nq * p.hq : rows_per_seq;
   const size_t ml_stride = static_cast<size_t>(step) * rows_per_seq * 2;
   const size_t o_stride = static_cast<size_t>(step) * rows_per_seq * D;
   float* ml_base = p.part_ml + static_cast<size_t>(first) * rows_per_seq * 2;
   float* o_base = p.part_o + static_cast<size_t>(first) * rows_per_seq * D + lane * PER;
-  for (int row0 = warp * RW; row0 < rows_per_seq; row0 += nwarps * RW) {
+  for (int row0 = warp * RW; row0 < rows; row0 += nwarps * RW) {
     float mm[RW], ll[RW], acc[RW][PER];
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
@@ -346,7 +385,7 @@ __device__ __forceinline__ void merge_parts(const Params& p, const Segment& seg,
           ml[jj][r] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int e = 0; e < PER; ++e) v[jj][r][e] = 0.f;
-          if (j0 + jj >= count || row0 + r >= rows_per_seq) continue;
+          if (j0 + jj >= count || row0 + r >= rows) continue;
           const size_t j = j0 + jj;
           ml[jj][r] = __ldcg(reinterpret_cast<const float2*>(ml_base + j * ml_stride + (row0 + r) * 2));
           const float* src = o_base + j * o_stride + static_cast<size_t>(row0 + r) * D;
@@ -383,9 +422,9 @@ __device__ __forceinline__ void merge_parts(const Params& p, const Segment& seg,
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
-      if (row0 + r >= rows_per_seq) continue;
+      if (row0 + r >= rows) continue;
       if (final) {
-        const float inv = 1.f / ll[r];
+        const float inv = kVar && ll[r] == 0.f ? 0.f : 1.f / ll[r];  // kVar: a row may see nothing
 #pragma unroll
         for (int e = 0; e < PER; ++e)
           out[static_cast<size_t>(row0 + r) * D + lane * PER + e] = static_cast<T>(acc[r][e] * inv);
@@ -410,7 +449,7 @@ constexpr int kMergeGroup = 8;
 // kMergeGroup parts is merged straight to the output).  A long context split
 // over ~150 parts thus merges in two short steps spread over ~20 CTAs instead
 // of one CTA reading every part.
-template <typename T, int D>
+template <typename T, int D, bool kVar = false>
 __device__ __forceinline__ void combine_if_last(const Params& p, const Segment& seg, int rows_per_seq, int* sh_flag,
                                                 int nthreads_c) {
   const int tid = threadIdx.x;
@@ -429,10 +468,10 @@ __device__ __forceinline__ void combine_if_last(const Params& p, const Segment& 
   if (sh_flag[0]) {
     __threadfence();
     if (ng == 1) {
-      merge_parts<T, D>(p, seg, rows_per_seq, seg.first_slot, 1, np, true, nthreads_c);
+      merge_parts<T, D, kVar>(p, seg, rows_per_seq, seg.first_slot, 1, np, true, nthreads_c);
       if (tid == 0) *gcount = 0;
     } else {
-      merge_parts<T, D>(p, seg, rows_per_seq, seg.first_slot + gfirst, 1, gsize, false, nthreads_c);
+      merge_parts<T, D, kVar>(p, seg, rows_per_seq, seg.first_slot + gfirst, 1, gsize, false, nthreads_c);
       pkv::named_barrier_sync(1, nthreads_c);
       if (tid == 0) {
         *gcount = 0;
@@ -442,7 +481,7 @@ __device__ __forceinline__ void combine_if_last(const Params& p, const Segment& 
       pkv::named_barrier_sync(1, nthreads_c);
       if (sh_flag[0]) {
         __threadfence();
-        merge_parts<T, D>(p, seg, rows_per_seq, seg.first_slot, kMergeGroup, ng, true, nthreads_c);
+        merge_parts<T, D, kVar>(p, seg, rows_per_seq, seg.first_slot, kMergeGroup, ng, true, nthreads_c);
         if (tid == 0) p.counters[seg.b] = 0;
       }
     }

@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
     const uint64_t policy = pkv::l2_evict_first_policy();
     const size_t head_row = static_cast<size_t>(p.hkv) * S::ROW_BYTES;  // bytes per token, all heads
     int it = 0;
-    for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
+    for_each_segment<kMod, false>(p, plan, [&](const Segment& seg) -> bool {
       const int32_t* table = p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks;
       for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
         const int s = it % p.stages;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
   const int nthreads_c = nw * 32;
   int it = 0;
 
-  for_each_segment<kMod>(p, plan, [&](const Segment& seg) -> bool {
+  for_each_segment<kMod, false>(p, plan, [&](const Segment& seg) -> bool {
     // q of the R rows sharing KV head g, pre-scaled into the exp2 domain
     float qr[R][S::EPL];
 #pragma unroll

@@ -49,6 +49,10 @@ int prefill_tc_capped_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_biased_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_capped_biased_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_fp8_launch(const PrefillArgs& a, cudaStream_t stream);
+// Chunks of at most 8 rows per KV head (max_seqlen_q * G <= 8) on the decode
+// kernel; workspace bytes it needs on the current device (0: an error).
+int chunk_decode_launch(const PrefillArgs& a, bool fp8, cudaStream_t stream);
+size_t chunk_decode_workspace_bytes(int batch, int num_kv_heads, int head_dim);
 // Parts a long pair of query tiles may run as, and the bytes of each of the
 // split's two counter arrays.
 int prefill_tc_parts(int batch, int num_kv_heads, int group, int max_seqlen_q, int sms);

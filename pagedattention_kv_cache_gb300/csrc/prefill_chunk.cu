@@ -43,7 +43,32 @@ int check_args(const PrefillArgs& a, int max_seqlen_k) {
   return PKV_OK;
 }
 
+// Chunks of at most 8 rows per KV head that the decode kernel takes (its own
+// limits are head_dim 128 and 8 KV heads).
+bool short_chunk(int group, int num_kv_heads, int head_dim, int max_seqlen_q) {
+  return head_dim == 128 && num_kv_heads <= 8 && static_cast<long long>(max_seqlen_q) * group <= 8;
+}
+
+// The decode kernel runs a short chunk when its workspace is there, else the
+// tcgen05 kernel does.
+bool on_decode_kernel(const PrefillArgs& a) {
+  if (!a.block_tables || !short_chunk(a.group, a.hkv, a.head_dim, a.max_seqlen_q)) return false;
+  const size_t need = pkv::chunk_decode_workspace_bytes(a.batch, a.hkv, a.head_dim);
+  return need > 0 && a.workspace && a.workspace_bytes >= need;
+}
+
 }  // namespace
+
+extern "C" size_t pkv_paged_short_chunk_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                        int32_t head_dim, int32_t max_seqlen_q) {
+  if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_seqlen_q <= 0)
+    return 0;
+  const int group = num_q_heads / num_kv_heads;
+  if ((group != 1 && group != 2 && group != 4 && group != 8) ||
+      !short_chunk(group, num_kv_heads, head_dim, max_seqlen_q))
+    return 0;
+  return pkv::chunk_decode_workspace_bytes(batch, num_kv_heads, head_dim);
+}
 
 extern "C" int pkv_paged_varlen_prefill_attn_mod(
     void* out, const void* q, const void* k, const void* v, const void* k_cache, const void* v_cache,
@@ -85,6 +110,7 @@ extern "C" int pkv_paged_varlen_prefill_attn_mod(
   int st = PKV_OK;
   a.err = pkv::device_error_word(&st);
   if (st != PKV_OK) return st;
+  if (on_decode_kernel(a)) return pkv::chunk_decode_launch(a, false, stream);
   if (a.mod.slopes)
     return softcap > 0.f ? pkv::prefill_tc_capped_biased_launch(a, stream) : pkv::prefill_tc_biased_launch(a, stream);
   return softcap > 0.f ? pkv::prefill_tc_capped_launch(a, stream) : pkv::prefill_tc_masked_launch(a, stream);
@@ -130,5 +156,6 @@ extern "C" int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const
   int st = PKV_OK;
   a.err = pkv::device_error_word(&st);
   if (st != PKV_OK) return st;
+  if (on_decode_kernel(a)) return pkv::chunk_decode_launch(a, true, stream);
   return pkv::prefill_tc_fp8_launch(a, stream);
 }

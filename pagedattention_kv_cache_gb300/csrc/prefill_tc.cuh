@@ -351,55 +351,50 @@ __device__ __forceinline__ uint64_t capped_pair(uint32_t s0, uint32_t s1, const 
   return fma2(s, t, c);
 }
 
+// Caps the raw scores of one row and 64 consecutive keys (r) in place, into the
+// exp2 domain.  The polynomials hold for the whole warp's scores or not at all.
+__device__ __forceinline__ void cap_scores(const TcParams& p, uint32_t* r) {
+  float mx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 64; e += 8) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      mx[u] = max3(mx[u], fabsf(__uint_as_float(r[e + 2 * u])), fabsf(__uint_as_float(r[e + 2 * u + 1])));
+  }
+  const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+  if (!__any_sync(0xffffffffu, top > p.tanh_poly.near_limit)) {
+#pragma unroll
+    for (int e = 0; e < 64; e += 2) unpack2u(capped_pair(r[e], r[e + 1], p.tanh_poly.near, 0ull), r[e], r[e + 1]);
+  } else if (!__any_sync(0xffffffffu, top > p.tanh_poly.wide_limit)) {
+#pragma unroll
+    for (int e = 0; e < 64; e += 2) unpack2u(capped_pair(r[e], r[e + 1], p.tanh_poly.wide, 0ull), r[e], r[e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 64; ++e)
+      r[e] = __float_as_uint(p.mod.cap_log2 * tanh_by_exp(__uint_as_float(r[e]) * p.mod.raw_to_x));
+  }
+}
+
 // Adds the distance bias to the scores of one row and 64 consecutive keys (r),
-// in place.  Without a cap the scores stay raw and `slope` is the bias per key in
-// raw units (slope / scale), so one fma per score suffices; with one (kCap) they
-// are capped too and end in the exp2 domain.  dist0 = first key - the row's
-// position; `ahead`: some key may lie past the position (a prefix, or full
-// attention), so the distance's absolute value is taken.
-template <bool kCap>
-__device__ __forceinline__ void bias_scores(const TcParams& p, uint32_t* r, float slope, int dist0, bool ahead) {
+// in place, one fma per score: `slope` is the bias per key in the scores' units
+// (raw, slope / scale, or the exp2 domain after a cap).  dist0 = first key - the
+// row's position (distances are whole numbers, so exact); `ahead`: some key may
+// lie past the position (a prefix, or full attention), so the distance's absolute
+// value is taken.
+__device__ __forceinline__ void bias_scores(uint32_t* r, float slope, int dist0, bool ahead) {
   const float d0 = static_cast<float>(dist0);
-  int tier = 2;  // of the cap: 0 exponentials, 1 wide, 2 near polynomial
-  if constexpr (kCap) {
-    float mx[4] = {0.f, 0.f, 0.f, 0.f};
+  if (ahead) {
 #pragma unroll
-    for (int e = 0; e < 64; e += 8) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        mx[u] = max3(mx[u], fabsf(__uint_as_float(r[e + 2 * u])), fabsf(__uint_as_float(r[e + 2 * u + 1])));
-    }
-    const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-    tier = !__any_sync(0xffffffffu, top > p.tanh_poly.near_limit)   ? 2
-           : !__any_sync(0xffffffffu, top > p.tanh_poly.wide_limit) ? 1
-                                                                     : 0;
-  }
-  if (ahead || tier == 0) {
-#pragma unroll
-    for (int e = 0; e < 64; ++e) {
-      const float s = __uint_as_float(r[e]);
-      const float x = kCap ? p.mod.cap_log2 * tanh_by_exp(s * p.mod.raw_to_x) : s;
-      r[e] = __float_as_uint(fmaf(-slope, fabsf(d0 + static_cast<float>(e)), x));
-    }
-    return;
-  }
-  // keys up to the position: the bias is slope * (key - position), the distances whole numbers (exact)
-  const uint64_t s2 = pack2(slope, slope), step = pack2(4.f, 4.f);
-  auto run = [&](auto&& value) {
-    uint64_t d[2] = {pack2(d0, d0 + 1.f), pack2(d0 + 2.f, d0 + 3.f)};
+    for (int e = 0; e < 64; ++e)
+      r[e] = __float_as_uint(fmaf(-slope, fabsf(d0 + static_cast<float>(e)), __uint_as_float(r[e])));
+  } else {
+    const uint64_t s2 = pack2(slope, slope), step = pack2(2.f, 2.f);
+    uint64_t d = pack2(d0, d0 + 1.f);
 #pragma unroll
     for (int e = 0; e < 64; e += 2) {
-      unpack2u(value(r[e], r[e + 1], d[(e / 2) % 2]), r[e], r[e + 1]);
-      d[(e / 2) % 2] = add2(d[(e / 2) % 2], step);
+      unpack2u(fma2(s2, d, pack2u(r[e], r[e + 1])), r[e], r[e + 1]);
+      d = add2(d, step);
     }
-  };
-  if constexpr (kCap) {
-    if (tier == 2)
-      run([&](uint32_t a, uint32_t b, uint64_t d) { return capped_pair(a, b, p.tanh_poly.near, mul2(s2, d)); });
-    else
-      run([&](uint32_t a, uint32_t b, uint64_t d) { return capped_pair(a, b, p.tanh_poly.wide, mul2(s2, d)); });
-  } else {
-    run([&](uint32_t a, uint32_t b, uint64_t d) { return fma2(s2, d, pack2u(a, b)); });
   }
 }
 
@@ -929,19 +924,21 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t s_addr = lane_addr + kColS + x * kBN;
     const uint32_t o_addr = lane_addr + kColO + x * kD + half * (kD / 2);  // this half's D / 2 output columns
-    int lim = p.causal ? min(pos, nk - 1) : nk - 1;
-    // kMod: the row sees keys lo_row .. lim; a row that sees none gets a range no key is in
-    int lo_row = 0;
-    int lo_most = 0;     // the largest lo_row of the warp
+    const int lim = p.causal ? min(pos, nk - 1) : nk - 1;
+    // kMod: the row sees keys lo .. hi; a row that sees none gets a range no key is
+    // in.  Taken anew for each tile that needs it: held through the loop, the two
+    // would cost registers.
+    auto seen_range = [&](int& lo, int& hi) {
+      hi = max(lim, prefix_end - 1);
+      lo = p.mod.first_keys && tok < nq ? max(__ldg(p.mod.first_keys + q_begin + tok), 0) : 0;
+      if (lo > hi) lo = hi = INT32_MAX;
+    };
+    int lo_most = 0;     // the largest lo of the warp
     float slope = 0.f;   // per key of distance, in the units of bias_scores
     if constexpr (kMod) {
-      lim = max(lim, prefix_end - 1);
-      if (p.mod.first_keys && tok < nq) lo_row = max(__ldg(p.mod.first_keys + q_begin + tok), 0);
-      if (lo_row > lim) {
-        lo_row = INT32_MAX;
-        lim = lo_row;
-      }
-      lo_most = __reduce_max_sync(0xffffffffu, lo_row);
+      int hi;
+      seen_range(lo_most, hi);
+      lo_most = __reduce_max_sync(0xffffffffu, lo_most);
       if constexpr (kBias) slope = __ldg(p.mod.slopes + g * G + row % G) * p.bias_mul;
     }
     float mul = kBias && kCap ? 1.f : p.scale_log2;  // scores as held in registers to exponents
@@ -992,11 +989,13 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       if (lane == 0) mbar_arrive(&bars[Q_READY]);
     }
 
-    // kMod: keys the row does not see get -infinity; lo_row <= key <= lim in one unsigned comparison
+    // kMod: keys the row does not see get -infinity; lo <= key <= hi in one unsigned comparison
     bool masked = false;
     auto hide = [&](int key0) {
-      const uint32_t span = static_cast<uint32_t>(lim - lo_row);
-      const uint32_t off = static_cast<uint32_t>(key0 - lo_row);
+      int lo, hi;
+      seen_range(lo, hi);
+      const uint32_t span = static_cast<uint32_t>(hi - lo);
+      const uint32_t off = static_cast<uint32_t>(key0 - lo);
 #pragma unroll
       for (int e = 0; e < 64; ++e) {
         // (a cap tells a key not seen, -infinity, from a score that overflowed)
@@ -1015,7 +1014,8 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       tc::tmem_ld32(s_addr + half * 64 + 32, r + 32);
       tc::tmem_wait_ld();
       if constexpr (kMod) {
-        if constexpr (kBias) bias_scores<kCap>(p, r, slope, key0 - pos, key0 + 63 > cached + tok_first);
+        if constexpr (kBias && kCap) cap_scores(p, r);
+        if constexpr (kBias) bias_scores(r, slope, key0 - pos, key0 + 63 > cached + tok_first);
         const int seen_by_all = p.causal ? max(cached + tok_first, prefix_end - 1) : nk - 1;
         masked = key0 + 63 > seen_by_all || key0 < lo_most;
         if (masked) hide(key0);

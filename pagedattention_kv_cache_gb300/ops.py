@@ -385,6 +385,33 @@ def _workspace_args(workspace, nbytes: int, device: torch.device):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def chunk_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int) -> int:
+    """Bytes of the workspace with which paged_varlen_prefill_attn_mod and _fp8 split these sizes (0: never)."""
+    short = int(_lib.load().pkv_paged_short_chunk_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim,
+                                                                  max_seqlen_q))
+    return max(short, prefill_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q))
+
+
+def chunk_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int,
+                    device=None) -> torch.Tensor | None:
+    """A zero-filled workspace (uint8) for paged_varlen_prefill_attn_mod and _fp8, or None when none is needed."""
+    n = chunk_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q)
+    if n == 0:
+        return None
+    return torch.zeros(n, dtype=torch.uint8, device=device or torch.cuda.current_device())
+
+
+def _chunk_workspace_args(workspace, batch: int, hq: int, hkv: int, d: int, max_q: int, paged: bool, device):
+    """The workspace of a chunk call: the caller's if it is large enough for a short chunk, else one for this call."""
+    short = 0
+    if paged and d == 128 and hkv <= 8 and max_q * hq <= 8 * hkv and batch > 0 and max_q > 0:
+        short = int(_lib.load().pkv_paged_short_chunk_workspace_bytes(batch, hq, hkv, d, max_q))
+    if short > 0 and (workspace is None or workspace is False or workspace.numel() * workspace.element_size() < short):
+        return _workspace_args(None, short, device)
+    return _workspace_args(workspace, prefill_workspace_bytes(batch, hq, hkv, d, max_q) if workspace is None else 0,
+                           device)
+
+
 def _need_modifiers(device, num_q_heads: int, alibi_slopes, first_keys, rows: int, prefix_lens=None, batch: int = 0):
     if alibi_slopes is not None:
         _need(alibi_slopes, "alibi_slopes", dtype=torch.float32, device=device, shape=(num_q_heads,))
@@ -447,8 +474,9 @@ def paged_varlen_prefill_attn_mod(q: torch.Tensor, cu_seqlens_q: torch.Tensor, c
     softcap, alibi_slopes: as for paged_decode_attn_mod.
     first_keys: int32 [total_q]; the row does not see keys before it (document or window mask).
     prefix_lens: int32 [B]; every row of the sequence sees keys below it besides the causal ones.
-    workspace: None = a zero-filled one for this call where a split needs it; False = never
-    split long query tiles; or a tensor from prefill_workspace().
+    workspace: a tensor from chunk_workspace() (or prefill_workspace()); None = a zero-filled one
+    for this call where a split needs it; False = never split long query tiles.  Short chunks
+    (max_seqlen_q * Hq / Hkv <= 8 over a cache) take one for the call where the given one is too small.
     """
     dev = _device(q, "q")
     _need(q, "q", ndim=3)
@@ -481,8 +509,8 @@ def paged_varlen_prefill_attn_mod(q: torch.Tensor, cu_seqlens_q: torch.Tensor, c
         if out is None:
             out = torch.empty_like(q)
         _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
-        workspace, ws_ptr, ws_bytes = _workspace_args(
-            workspace, prefill_workspace_bytes(B, hq, hkv, d, int(max_seqlen_q)) if workspace is None else 0, dev)
+        workspace, ws_ptr, ws_bytes = _chunk_workspace_args(workspace, B, hq, hkv, d, int(max_seqlen_q),
+                                                            block_tables is not None, dev)
     st = _lib.load().pkv_paged_varlen_prefill_attn_mod(
         _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q),
         _ptr(cu_seqlens_k), int(max_seqlen_q), int(max_seqlen_k), _ptr(block_tables), mb, B, total_q,
@@ -522,8 +550,7 @@ def paged_varlen_prefill_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cach
         if out is None:
             out = torch.empty_like(q)
         _need(out, "out", dtype=torch.bfloat16, device=dev, shape=q.shape)
-        workspace, ws_ptr, ws_bytes = _workspace_args(
-            workspace, prefill_workspace_bytes(B, hq, hkv, d, int(max_seqlen_q)) if workspace is None else 0, dev)
+        workspace, ws_ptr, ws_bytes = _chunk_workspace_args(workspace, B, hq, hkv, d, int(max_seqlen_q), True, dev)
     st = _lib.load().pkv_paged_varlen_prefill_attn_fp8(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(max_seqlen_q),
         int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], B, total_q, hq, hkv, d, bs, nb,

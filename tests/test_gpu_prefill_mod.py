@@ -85,6 +85,14 @@ class Case:
 CACHED, NEW = [0, 16, 0, 130, 300, 5], [1, 40, 129, 0, 260, 3]
 
 
+def _call_args(case, kw):
+    """Arguments of Case.compare as those of Case.call."""
+    kw = dict(kw)
+    if kw.pop("alibi", False):
+        kw["slopes"] = slopes_of(case.hq)
+    return {n: i32(np.asarray(x).tolist()) if n in ("first", "prefix") else x for n, x in kw.items()}
+
+
 def _documents(case, seed, least=1):
     """First key of each row from random document starts of each sequence."""
     rng, out = np.random.default_rng(seed), []
@@ -120,6 +128,32 @@ def test_packed_keys_and_full_attention(d, group):
     c.compare(causal=False, first=c.positions() - 50, label="packed, full, first keys")
     c = Case(80 + d, CACHED, NEW, hq=2 * group, hkv=2, d=d)
     c.compare(causal=False, cap=40.0, alibi=True, first=np.minimum(_documents(c, 6), 60), hide=True, label="paged, full")
+
+
+@pytest.mark.parametrize("block_size", [16, 24, 256])
+@pytest.mark.parametrize("group,hkv,new", [(1, 8, [4, 1, 8, 3, 0, 2]), (2, 3, [4, 1, 2, 3, 0, 4]), (4, 2, [2, 1, 2, 0, 1, 2]),
+                                           (8, 1, [1, 1, 1, 0, 1, 1])])
+@pytest.mark.parametrize("mods", ["cap", "alibi", "documents", "window", "prefix", "all", "nothing", "full"])
+def test_short_chunks_on_the_decode_kernel(block_size, group, hkv, new, mods):
+    c = Case(90 + group, [1000, 17, 0, 255, 511, 2000], new, hq=group * hkv, hkv=hkv, block_size=block_size)
+    assert pkv.chunk_workspace_bytes(6, c.hq, hkv, 128, max(new)) > 0
+    kw = {"cap": dict(cap=50.0), "alibi": dict(alibi=True), "documents": dict(first=_documents(c, group)),
+          "window": dict(first=c.positions() - 99), "prefix": dict(prefix=[0, 18, 200, 257, 301, -4], alibi=True),
+          "all": dict(cap=20.0, alibi=True, first=_documents(c, group + 1), prefix=[1003, 56, 64, 7, 400, 0]),
+          "nothing": dict(cap=50.0, first=c.positions() + np.arange(sum(new)) % 3 - 1),
+          "full": dict(causal=False, alibi=True, cap=30.0, first=c.positions() - 40)}[mods]
+    c.compare(label=mods, **kw)
+    ws = pkv.chunk_workspace(6, c.hq, hkv, 128, max(new))
+    a = c.compare(workspace=ws, hide=True, **kw)
+    assert torch.equal(a, c.call(workspace=ws, **_call_args(c, kw)))
+    assert int(ws[:65536].count_nonzero()) == 0
+
+
+def test_short_chunk_of_sequences_without_a_key():
+    c = Case(99, [40, 30, 0], [2, 3, 1], hq=4, hkv=2)
+    first = np.array([1 << 30, 1 << 30, 0, 5, 1 << 30, 1 << 30])
+    out = c.compare(first=first)
+    assert not out[:2].any() and not out[4:].any() and out[2:4].any()
 
 
 def test_rows_that_see_nothing():
