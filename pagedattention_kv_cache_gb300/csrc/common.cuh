@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/pagedkv.h"
@@ -68,6 +69,22 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Raises kernel's dynamic shared memory limit to `bytes`, once per device and
+// kernel (a launch with the same kernel needs no second call; `done` is the
+// kernel's own word, one bit per device).
+template <typename F>
+inline cudaError_t allow_smem(F* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  const cudaError_t st = cudaGetDevice(&dev);
+  if (st != cudaSuccess) return st;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

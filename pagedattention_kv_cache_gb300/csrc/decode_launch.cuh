@@ -98,9 +98,8 @@ int launch(Params& p, int sms, cudaStream_t stream) {
   p.stages = ls.stages;
   p.stage_bytes = ls.stage_bytes;
   auto kernel = paged_decode_kernel<T, TC, D, G, QL, kMod>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ls.smem)) !=
-      cudaSuccess)
-    return PKV_ECUDA;
+  static std::atomic<uint64_t> smem_allowed{0};  // the limit for every number of KV heads
+  if (pkv::allow_smem(kernel, kSmemBudget + 1024, smem_allowed) != cudaSuccess) return PKV_ECUDA;
   unsigned grid;
   if (p.num_splits > 0)
     grid = static_cast<unsigned>(static_cast<long long>(p.batch) * p.num_splits);
@@ -147,9 +146,8 @@ int launch_mma(Params& p, int sms, cudaStream_t stream) {
   p.stages = ls.stages;
   p.stage_bytes = ls.stage_bytes;
   auto kernel = paged_decode_mma_kernel<G, QL, TC, kMod, kVar>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(ls.smem)) !=
-      cudaSuccess)
-    return PKV_ECUDA;
+  static std::atomic<uint64_t> smem_allowed{0};  // the limit for every number of KV heads
+  if (pkv::allow_smem(kernel, kSmemBudget + 1024, smem_allowed) != cudaSuccess) return PKV_ECUDA;
   unsigned grid;
   if (p.num_splits > 0)
     grid = static_cast<unsigned>(static_cast<long long>(p.batch) * p.num_splits);

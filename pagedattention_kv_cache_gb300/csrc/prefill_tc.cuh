@@ -1372,9 +1372,8 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
   }
   auto kernel = prefill_tc_kernel<G, D, kForm>;
   constexpr uint32_t kSmemBytes = Geo<D, kFp8>::kLaunchSmem;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
-      cudaSuccess)
-    return PKV_ECUDA;
+  static std::atomic<uint64_t> smem_allowed{0};
+  if (allow_smem(kernel, kSmemBytes, smem_allowed) != cudaSuccess) return PKV_ECUDA;
   dim3 grid(a.batch * a.hkv, pairs * p.parts_max);
   return launch_pdl(kernel, grid, dim3(threads<kFp8>()), kSmemBytes, stream, tm_q, tm_k, tm_v, p) == cudaSuccess ? PKV_OK
                                                                                                   : PKV_ECUDA;

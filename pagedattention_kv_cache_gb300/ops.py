@@ -10,7 +10,6 @@ in the library's CUDA kernels; nothing here computes.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -44,7 +43,7 @@ def _need(t: torch.Tensor, name: str, dtype=None, ndim=None, device=None, shape=
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -58,9 +57,14 @@ def _device(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
+# the current stream's handle without building a Stream object (2 us of a call's host time)
+_current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                 lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(stream, device: torch.device) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream_handle(device.index)
     if stream.device != device:
         raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
     return stream.cuda_stream
@@ -370,19 +374,35 @@ def paged_varlen_prefill_attn(q: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_se
     return out
 
 
-def _on_stream(stream):
-    """Allocations of a call belong to the stream it runs on (its pool, and the zero fill in its order)."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _buffers(stream, q: torch.Tensor, out, workspace_args, *args):
+    """out (allocated when None) and the workspace_args(*args) of a call, allocated on the stream the call
+    runs on (its pool, and the zero fill in its order)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _buffers(None, q, out, workspace_args, *args)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", dtype=q.dtype, device=q.device, shape=q.shape)
+    return out, *workspace_args(*args)
 
 
-def _workspace_args(workspace, nbytes: int, device: torch.device):
-    """(tensor, pointer, bytes) of a split workspace: the caller's, none (False), or a zero-filled one for this call."""
+def _workspace_args(workspace, nbytes: int, batch: int, device: torch.device):
+    """(tensor, pointer, bytes) of a split workspace: the caller's, none (False), or one for this call."""
     if workspace is False or (workspace is None and nbytes == 0):
         return None, None, 0
     if workspace is None:
-        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    _need(workspace, "workspace", device=device)
+        # only the counter area must be zero; past 4096 sequences it may be longer than 64 KiB
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        (workspace if batch > 4096 else workspace.narrow(0, 0, min(nbytes, 65536))).zero_()
+    else:
+        _need(workspace, "workspace", device=device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _decode_workspace_args(workspace, batch: int, hq: int, d: int, num_splits: int, device):
+    return _workspace_args(workspace, decode_workspace_bytes(batch, hq, d, num_splits) if workspace is None else 0,
+                           batch * max(num_splits, 1), device)
 
 
 def chunk_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int) -> int:
@@ -407,9 +427,9 @@ def _chunk_workspace_args(workspace, batch: int, hq: int, hkv: int, d: int, max_
     if paged and d == 128 and hkv <= 8 and max_q * hq <= 8 * hkv and batch > 0 and max_q > 0:
         short = int(_lib.load().pkv_paged_short_chunk_workspace_bytes(batch, hq, hkv, d, max_q))
     if short > 0 and (workspace is None or workspace is False or workspace.numel() * workspace.element_size() < short):
-        return _workspace_args(None, short, device)
+        return _workspace_args(None, short, batch, device)
     return _workspace_args(workspace, prefill_workspace_bytes(batch, hq, hkv, d, max_q) if workspace is None else 0,
-                           device)
+                           batch, device)
 
 
 def _need_modifiers(device, num_q_heads: int, alibi_slopes, first_keys, rows: int, prefix_lens=None, batch: int = 0):
@@ -446,12 +466,8 @@ def paged_decode_attn_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
         raise ValueError("inconsistent shapes between q, caches, block_tables and context_lens")
     _need_modifiers(dev, hq, alibi_slopes, first_keys, B)
     handle = _stream(stream, dev)
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
-        workspace, ws_ptr, ws_bytes = _workspace_args(
-            workspace, decode_workspace_bytes(B, hq, d, num_splits) if workspace is None else 0, dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _decode_workspace_args, workspace, B, hq, d, num_splits,
+                                                dev)
     st = _lib.load().pkv_paged_decode_attn_mod(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
         _ptr(context_lens), B, hq, hkv, d, bs, nb, ctypes.c_float(scale), ctypes.c_float(softcap), _ptr(alibi_slopes),
@@ -505,12 +521,8 @@ def paged_varlen_prefill_attn_mod(q: torch.Tensor, cu_seqlens_q: torch.Tensor, c
         raise ValueError("the keys' head_dim differs from q's")
     _need_modifiers(dev, hq, alibi_slopes, first_keys, total_q, prefix_lens, B)
     handle = _stream(stream, dev)
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
-        workspace, ws_ptr, ws_bytes = _chunk_workspace_args(workspace, B, hq, hkv, d, int(max_seqlen_q),
-                                                            block_tables is not None, dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _chunk_workspace_args, workspace, B, hq, hkv, d,
+                                                int(max_seqlen_q), block_tables is not None, dev)
     st = _lib.load().pkv_paged_varlen_prefill_attn_mod(
         _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q),
         _ptr(cu_seqlens_k), int(max_seqlen_q), int(max_seqlen_k), _ptr(block_tables), mb, B, total_q,
@@ -546,11 +558,8 @@ def paged_varlen_prefill_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     if block_tables.shape[0] != B:
         raise ValueError("block_tables rows must equal the batch")
     handle = _stream(stream, dev)
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        _need(out, "out", dtype=torch.bfloat16, device=dev, shape=q.shape)
-        workspace, ws_ptr, ws_bytes = _chunk_workspace_args(workspace, B, hq, hkv, d, int(max_seqlen_q), True, dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _chunk_workspace_args, workspace, B, hq, hkv, d,
+                                                int(max_seqlen_q), True, dev)
     st = _lib.load().pkv_paged_varlen_prefill_attn_fp8(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(max_seqlen_q),
         int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], B, total_q, hq, hkv, d, bs, nb,
