@@ -433,11 +433,14 @@ int pkv_paged_varlen_prefill_attn_mod(void* out, const void* q, const void* k, c
  * per KV head over a paged cache (drafted tokens of a verify pass, a prompt's
  * last tokens), on the decode kernel, which divides the batch's keys evenly
  * over the SMs; given less they run on the prefill kernel.  0 when the sizes
- * are no short chunk (head_dim 128, num_kv_heads <= 8).  Zero-filled once; the
- * same counter area as every split workspace.
+ * are no short chunk (it needs head_dim 128, num_kv_heads <= 8, and more than
+ * 128 keys per row, max_seqlen_k > 128 * max_seqlen_q * G, or a batch that
+ * fills the SMs).  Zero-filled once; the same counter area as every split
+ * workspace.
  */
 size_t pkv_paged_short_chunk_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
-                                             int32_t head_dim, int32_t max_seqlen_q);
+                                             int32_t head_dim, int32_t max_seqlen_q,
+                                             int32_t max_seqlen_k);
 
 /*
  * paged_varlen_prefill_attn_fp8: a chunk of new tokens per sequence over an

@@ -58,7 +58,7 @@ SIGNATURES = [
      [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _S,
       ctypes.c_int, _P]),
     ("pkv_paged_varlen_prefill_workspace_bytes", _S, [_I, _I, _I, _I, _I]),
-    ("pkv_paged_short_chunk_workspace_bytes", _S, [_I, _I, _I, _I, _I]),
+    ("pkv_paged_short_chunk_workspace_bytes", _S, [_I, _I, _I, _I, _I, _I]),
     ("pkv_paged_decode_attn_mod", ctypes.c_int,
      [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _F, _P, _P, _I, _P, _S, ctypes.c_int, _P]),
     ("pkv_paged_varlen_prefill_attn_mod", ctypes.c_int,

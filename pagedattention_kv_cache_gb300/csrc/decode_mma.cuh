@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(288, 1)
         }
       }
     }
-    if (seg.nparts > 1) combine_if_last<T, D, kVar>(p, seg, rows_per_seq, sh_flag, nthreads_c);
+    if (seg.nparts > 1) combine_if_last<T, D, kMod, kVar>(p, seg, rows_per_seq, sh_flag, nthreads_c);
     return true;
   });
 }

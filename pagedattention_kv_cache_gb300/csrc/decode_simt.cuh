@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
       }
     }
 
-    if (seg.nparts > 1) combine_if_last<T, D>(p, seg, rows_per_seq, sh_flag, nthreads_c);
+    if (seg.nparts > 1) combine_if_last<T, D, kMod>(p, seg, rows_per_seq, sh_flag, nthreads_c);
     return true;
   });
 }

@@ -43,16 +43,28 @@ int check_args(const PrefillArgs& a, int max_seqlen_k) {
   return PKV_OK;
 }
 
-// Chunks of at most 8 rows per KV head that the decode kernel takes (its own
-// limits are head_dim 128 and 8 KV heads).
-bool short_chunk(int group, int num_kv_heads, int head_dim, int max_seqlen_q) {
-  return head_dim == 128 && num_kv_heads <= 8 && static_cast<long long>(max_seqlen_q) * group <= 8;
+// Whether the decode kernel takes a chunk: at most 8 rows per KV head (its own
+// limits are head_dim 128 and 8 KV heads), and work enough.  The tcgen05 kernel
+// needs about 6 us and 1 us per 128 keys for each wave of one (sequence, KV head)
+// per SM; the decode kernel 8 us, the time of the bytes, and up to 17 us of
+// merging, more with more rows.  Measured with 8 KV heads, G = 2, E4M3 (us,
+// decode / tcgen05): 4 tokens x 1 sequence after 512 keys 16.9 / 13.8, after
+// 2048 21.0 / 25.2; x 16 sequences 27.6 / 14.5 and 30.2 / 35.6; 1 token x 1
+// sequence after 128 keys 8.3 / 8.9, after 512 10.2 / 13.8; two waves (64
+// sequences) 16.9 / 28.3 after 32 keys.
+bool short_chunk(int batch, int group, int num_kv_heads, int head_dim, int max_seqlen_q, int max_seqlen_k) {
+  const long long rows = static_cast<long long>(max_seqlen_q) * group;
+  if (head_dim != 128 || num_kv_heads > 8 || rows > 8) return false;
+  pkv::DeviceInfo info;
+  if (pkv::device_info(&info) != PKV_OK) return false;
+  const bool one_wave = static_cast<long long>(batch) * num_kv_heads <= info.sms;
+  return !one_wave || max_seqlen_k > 128 * rows;
 }
 
 // The decode kernel runs a short chunk when its workspace is there, else the
 // tcgen05 kernel does.
-bool on_decode_kernel(const PrefillArgs& a) {
-  if (!a.block_tables || !short_chunk(a.group, a.hkv, a.head_dim, a.max_seqlen_q)) return false;
+bool on_decode_kernel(const PrefillArgs& a, int max_seqlen_k) {
+  if (!a.block_tables || !short_chunk(a.batch, a.group, a.hkv, a.head_dim, a.max_seqlen_q, max_seqlen_k)) return false;
   const size_t need = pkv::chunk_decode_workspace_bytes(a.batch, a.hkv, a.head_dim);
   return need > 0 && a.workspace && a.workspace_bytes >= need;
 }
@@ -60,12 +72,13 @@ bool on_decode_kernel(const PrefillArgs& a) {
 }  // namespace
 
 extern "C" size_t pkv_paged_short_chunk_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
-                                                        int32_t head_dim, int32_t max_seqlen_q) {
+                                                        int32_t head_dim, int32_t max_seqlen_q,
+                                                        int32_t max_seqlen_k) {
   if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_seqlen_q <= 0)
     return 0;
   const int group = num_q_heads / num_kv_heads;
   if ((group != 1 && group != 2 && group != 4 && group != 8) ||
-      !short_chunk(group, num_kv_heads, head_dim, max_seqlen_q))
+      !short_chunk(batch, group, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k))
     return 0;
   return pkv::chunk_decode_workspace_bytes(batch, num_kv_heads, head_dim);
 }
@@ -110,7 +123,7 @@ extern "C" int pkv_paged_varlen_prefill_attn_mod(
   int st = PKV_OK;
   a.err = pkv::device_error_word(&st);
   if (st != PKV_OK) return st;
-  if (on_decode_kernel(a)) return pkv::chunk_decode_launch(a, false, stream);
+  if (on_decode_kernel(a, max_seqlen_k)) return pkv::chunk_decode_launch(a, false, stream);
   if (a.mod.slopes)
     return softcap > 0.f ? pkv::prefill_tc_capped_biased_launch(a, stream) : pkv::prefill_tc_biased_launch(a, stream);
   return softcap > 0.f ? pkv::prefill_tc_capped_launch(a, stream) : pkv::prefill_tc_masked_launch(a, stream);
@@ -156,6 +169,6 @@ extern "C" int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const
   int st = PKV_OK;
   a.err = pkv::device_error_word(&st);
   if (st != PKV_OK) return st;
-  if (on_decode_kernel(a)) return pkv::chunk_decode_launch(a, true, stream);
+  if (on_decode_kernel(a, max_seqlen_k)) return pkv::chunk_decode_launch(a, true, stream);
   return pkv::prefill_tc_fp8_launch(a, stream);
 }

@@ -405,27 +405,28 @@ def _decode_workspace_args(workspace, batch: int, hq: int, d: int, num_splits: i
                            batch * max(num_splits, 1), device)
 
 
-def chunk_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int) -> int:
+def chunk_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int,
+                          max_seqlen_k: int) -> int:
     """Bytes of the workspace with which paged_varlen_prefill_attn_mod and _fp8 split these sizes (0: never)."""
     short = int(_lib.load().pkv_paged_short_chunk_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim,
-                                                                  max_seqlen_q))
+                                                                  max_seqlen_q, max_seqlen_k))
     return max(short, prefill_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q))
 
 
 def chunk_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int,
-                    device=None) -> torch.Tensor | None:
+                    max_seqlen_k: int, device=None) -> torch.Tensor | None:
     """A zero-filled workspace (uint8) for paged_varlen_prefill_attn_mod and _fp8, or None when none is needed."""
-    n = chunk_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q)
+    n = chunk_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k)
     if n == 0:
         return None
     return torch.zeros(n, dtype=torch.uint8, device=device or torch.cuda.current_device())
 
 
-def _chunk_workspace_args(workspace, batch: int, hq: int, hkv: int, d: int, max_q: int, paged: bool, device):
+def _chunk_workspace_args(workspace, batch: int, hq: int, hkv: int, d: int, max_q: int, max_k: int, paged: bool, device):
     """The workspace of a chunk call: the caller's if it is large enough for a short chunk, else one for this call."""
     short = 0
-    if paged and d == 128 and hkv <= 8 and max_q * hq <= 8 * hkv and batch > 0 and max_q > 0:
-        short = int(_lib.load().pkv_paged_short_chunk_workspace_bytes(batch, hq, hkv, d, max_q))
+    if paged and max_q * hq <= 8 * hkv:
+        short = int(_lib.load().pkv_paged_short_chunk_workspace_bytes(batch, hq, hkv, d, max_q, max_k))
     if short > 0 and (workspace is None or workspace is False or workspace.numel() * workspace.element_size() < short):
         return _workspace_args(None, short, batch, device)
     return _workspace_args(workspace, prefill_workspace_bytes(batch, hq, hkv, d, max_q) if workspace is None else 0,
@@ -492,7 +493,7 @@ def paged_varlen_prefill_attn_mod(q: torch.Tensor, cu_seqlens_q: torch.Tensor, c
     prefix_lens: int32 [B]; every row of the sequence sees keys below it besides the causal ones.
     workspace: a tensor from chunk_workspace() (or prefill_workspace()); None = a zero-filled one
     for this call where a split needs it; False = never split long query tiles.  Short chunks
-    (max_seqlen_q * Hq / Hkv <= 8 over a cache) take one for the call where the given one is too small.
+    (max_seqlen_q * Hq / Hkv <= 8 over a long cache) take one for the call where the given one is too small.
     """
     dev = _device(q, "q")
     _need(q, "q", ndim=3)
@@ -522,7 +523,7 @@ def paged_varlen_prefill_attn_mod(q: torch.Tensor, cu_seqlens_q: torch.Tensor, c
     _need_modifiers(dev, hq, alibi_slopes, first_keys, total_q, prefix_lens, B)
     handle = _stream(stream, dev)
     out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _chunk_workspace_args, workspace, B, hq, hkv, d,
-                                                int(max_seqlen_q), block_tables is not None, dev)
+                                                int(max_seqlen_q), int(max_seqlen_k), block_tables is not None, dev)
     st = _lib.load().pkv_paged_varlen_prefill_attn_mod(
         _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q),
         _ptr(cu_seqlens_k), int(max_seqlen_q), int(max_seqlen_k), _ptr(block_tables), mb, B, total_q,
@@ -559,7 +560,7 @@ def paged_varlen_prefill_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cach
         raise ValueError("block_tables rows must equal the batch")
     handle = _stream(stream, dev)
     out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _chunk_workspace_args, workspace, B, hq, hkv, d,
-                                                int(max_seqlen_q), True, dev)
+                                                int(max_seqlen_q), int(max_seqlen_k), True, dev)
     st = _lib.load().pkv_paged_varlen_prefill_attn_fp8(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(max_seqlen_q),
         int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], B, total_q, hq, hkv, d, bs, nb,

@@ -109,29 +109,29 @@ def test_codes_of_every_value():
 def test_short_chunks_on_the_decode_kernel(block_size, group, hkv, new):
     # drafted tokens after ragged histories, split over the SMs and merged
     c = Case(63, [1000, 17, 0, 255, 511, 2000], new, hq=group * hkv, hkv=hkv, block_size=block_size)
-    assert pkv.chunk_workspace_bytes(6, c.hq, hkv, 128, max(new)) > 0
+    assert pkv.chunk_workspace_bytes(6, c.hq, hkv, 128, max(new), 2004) > 0
     c.compare(label="causal")
     c.compare(causal=False, label="full")
-    ws = pkv.chunk_workspace(6, c.hq, hkv, 128, max(new))
+    ws = pkv.chunk_workspace(6, c.hq, hkv, 128, max(new), 2004)
     a = c.compare(workspace=ws)
     assert torch.equal(a, c.compare(workspace=ws)) and int(ws[:65536].count_nonzero()) == 0
 
 
 def test_short_chunk_through_the_c_abi_without_its_workspace():
     # with no workspace, or one that is too small, the prefill kernel runs it
-    c = Case(68, [300, 17], [4, 2], hq=4, hkv=2)
+    c = Case(68, [1300, 17], [4, 2], hq=4, hkv=2)
     ref, dev = c.reference()
     q, kc, vc, table, cu_q, cu_k = [x.cuda() for x in (c.q, c.kc, c.vc, c.table, c.cu_q, c.cu_k)]
     small = torch.zeros(65536, dtype=torch.uint8, device="cuda")
     for ws, n in ((None, 0), (small.data_ptr(), small.numel())):
         out = torch.empty_like(q)
         st = _lib.load().pkv_paged_varlen_prefill_attn_fp8(
-            out.data_ptr(), q.data_ptr(), kc.data_ptr(), vc.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), 4, 304,
+            out.data_ptr(), q.data_ptr(), kc.data_ptr(), vc.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), 4, 1304,
             table.data_ptr(), table.shape[1], 2, 6, 4, 2, 128, 16, kc.shape[0], c.scale, K_SCALE, V_SCALE, 1, ws, n,
             torch.cuda.current_stream().cuda_stream)
         assert st == _lib.OK
         torch.cuda.synchronize()
-        check(out, ref, dev, torch.float16, 304)
+        check(out, ref, dev, torch.float16, 1304)
     assert pkv.device_error() == 0
 
 
@@ -191,7 +191,7 @@ def test_bad_cu_seqlens_and_pages_raise_bits():
                               ([0, 2, 4, 6], [0, 2, 20, 100], 2)):
         out = torch.full_like(short.q, 7.0).cuda()
         pkv.paged_varlen_prefill_attn_fp8(short.q.cuda(), short.kc.cuda(), short.vc.cuda(), short.table.cuda(),
-                                          i32(cu_q).cuda(), i32(cu_k).cuda(), max_q, 64, c.scale, K_SCALE, V_SCALE, out=out)
+                                          i32(cu_q).cuda(), i32(cu_k).cuda(), max_q, 2000, c.scale, K_SCALE, V_SCALE, out=out)
         assert pkv.device_error() == _lib.DERR_LEN_RANGE, (cu_q, cu_k, max_q)
         assert cu_k[-1] < 100 or torch.all(out[4:] == 7.0)  # a skipped sequence's rows are left alone
     bad = c.table.clone()

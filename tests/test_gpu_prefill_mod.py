@@ -136,21 +136,21 @@ def test_packed_keys_and_full_attention(d, group):
 @pytest.mark.parametrize("mods", ["cap", "alibi", "documents", "window", "prefix", "all", "nothing", "full"])
 def test_short_chunks_on_the_decode_kernel(block_size, group, hkv, new, mods):
     c = Case(90 + group, [1000, 17, 0, 255, 511, 2000], new, hq=group * hkv, hkv=hkv, block_size=block_size)
-    assert pkv.chunk_workspace_bytes(6, c.hq, hkv, 128, max(new)) > 0
+    assert pkv.chunk_workspace_bytes(6, c.hq, hkv, 128, max(new), 2004) > 0
     kw = {"cap": dict(cap=50.0), "alibi": dict(alibi=True), "documents": dict(first=_documents(c, group)),
           "window": dict(first=c.positions() - 99), "prefix": dict(prefix=[0, 18, 200, 257, 301, -4], alibi=True),
           "all": dict(cap=20.0, alibi=True, first=_documents(c, group + 1), prefix=[1003, 56, 64, 7, 400, 0]),
           "nothing": dict(cap=50.0, first=c.positions() + np.arange(sum(new)) % 3 - 1),
           "full": dict(causal=False, alibi=True, cap=30.0, first=c.positions() - 40)}[mods]
     c.compare(label=mods, **kw)
-    ws = pkv.chunk_workspace(6, c.hq, hkv, 128, max(new))
+    ws = pkv.chunk_workspace(6, c.hq, hkv, 128, max(new), 2004)
     a = c.compare(workspace=ws, hide=True, **kw)
     assert torch.equal(a, c.call(workspace=ws, **_call_args(c, kw)))
     assert int(ws[:65536].count_nonzero()) == 0
 
 
 def test_short_chunk_of_sequences_without_a_key():
-    c = Case(99, [40, 30, 0], [2, 3, 1], hq=4, hkv=2)
+    c = Case(99, [2000, 30, 0], [2, 3, 1], hq=4, hkv=2)
     first = np.array([1 << 30, 1 << 30, 0, 5, 1 << 30, 1 << 30])
     out = c.compare(first=first)
     assert not out[:2].any() and not out[4:].any() and out[2:4].any()
