@@ -198,7 +198,7 @@ struct TcParams {
   int parts_max;   // P: the most parts a long pair runs as (1: no split)
   int* tickets;    // [sequences x KV heads x q_tiles]: finish order of a split tile's parts, reset by the last
   int* ready;      // [same]: records published so far, reset by the last
-  unsigned char* records;  // [same][P][record bytes]: O rows (D fp32 each), then m[kBM], l[kBM]
+  unsigned char* records;  // [same][P][record bytes]: O (D / 4 chunks of 4 fp32 columns x kBM rows), then m[kBM], l[kBM]
   ScoreMod mod;            // kMod
   TanhPoly tanh_poly;      // kMod with a cap
   float bias_mul;          // slopes to the units of bias_scores
@@ -1183,6 +1183,10 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       auto record = [&](int q) {
         return reinterpret_cast<float*>(p.records + (static_cast<size_t>(item) * p.parts_max + q) * kRecordBytes);
       };
+      // 16-byte chunk of this half's column d (a multiple of 4) of the thread's row:
+      // the rows of a chunk are consecutive, so a warp's accesses are 512 contiguous
+      // bytes
+      auto record_chunk = [&](int d) { return (half * (kD / 2) + d) / 4 * kBM + row; };
       named_barrier_sync(bar_id, kGroup);
       if (threadIdx.x == leader) s_ticket[x] = atomicAdd(p.tickets + item, 1);
       named_barrier_sync(bar_id, kGroup);
@@ -1194,8 +1198,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
           load_o(c, o);
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            reinterpret_cast<uint4*>(rec + row * kD + half * (kD / 2) + c * 32 + e)[0] =
-                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            reinterpret_cast<uint4*>(rec)[record_chunk(c * 32 + e)] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
         if (half == 0) {
           rec[kBM * kD + row] = m_run;
@@ -1256,22 +1259,29 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
               for (int e = 0; e < 32; e += 8) {
                 float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int q = 0; q < kMaxParts; ++q) {
-                  if (q >= parts) break;
-                  if (mq[q] == 0.f) continue;  // saw no key of this row: weight 0, record not read
-                  float v8[8];
-                  if (q == part) {
+                for (int q0 = 0; q0 < kMaxParts; q0 += 2) {
+                  if (q0 >= parts) break;
+                  // two parts' loads go out before the first is used
+                  float4 v[2][2];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) v8[u] = __uint_as_float(o[e + u]);
-                  } else {
-                    const float* src = record(q) + row * kD + half * (kD / 2) + c * 32 + e;
-                    const float4 r0 = __ldcg(reinterpret_cast<const float4*>(src));
-                    const float4 r1 = __ldcg(reinterpret_cast<const float4*>(src + 4));
-                    v8[0] = r0.x, v8[1] = r0.y, v8[2] = r0.z, v8[3] = r0.w;
-                    v8[4] = r1.x, v8[5] = r1.y, v8[6] = r1.z, v8[7] = r1.w;
+                  for (int u = 0; u < 2; ++u) {
+                    if (q0 + u >= parts || q0 + u == part) continue;
+                    const float4* src = reinterpret_cast<const float4*>(record(q0 + u));
+                    v[u][0] = __ldcg(src + record_chunk(c * 32 + e));
+                    v[u][1] = __ldcg(src + record_chunk(c * 32 + e + 4));
                   }
 #pragma unroll
-                  for (int u = 0; u < 8; ++u) f[u] += mq[q] * v8[u];
+                  for (int u = 0; u < 2; ++u) {
+                    const int q = q0 + u;
+                    if (q >= parts || mq[q] == 0.f) continue;  // saw no key of this row: weight 0
+                    float v8[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+                    if (q == part) {
+#pragma unroll
+                      for (int i = 0; i < 8; ++i) v8[i] = __uint_as_float(o[e + i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] += mq[q] * v8[i];
+                  }
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) f[u] *= inv;

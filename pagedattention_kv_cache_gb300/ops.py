@@ -35,7 +35,7 @@ def _need(t: torch.Tensor, name: str, dtype=None, ndim=None, device=None, shape=
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
+    if device is not None and t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -471,7 +471,7 @@ def paged_decode_attn_mod(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                                                 dev)
     st = _lib.load().pkv_paged_decode_attn_mod(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
-        _ptr(context_lens), B, hq, hkv, d, bs, nb, ctypes.c_float(scale), ctypes.c_float(softcap), _ptr(alibi_slopes),
+        _ptr(context_lens), B, hq, hkv, d, bs, nb, scale, softcap, _ptr(alibi_slopes),
         _ptr(first_keys), num_splits, ws_ptr, ws_bytes, _dtype_code(q), handle)
     _lib.check("pkv_paged_decode_attn_mod", st)
     return out
@@ -527,7 +527,7 @@ def paged_varlen_prefill_attn_mod(q: torch.Tensor, cu_seqlens_q: torch.Tensor, c
     st = _lib.load().pkv_paged_varlen_prefill_attn_mod(
         _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q),
         _ptr(cu_seqlens_k), int(max_seqlen_q), int(max_seqlen_k), _ptr(block_tables), mb, B, total_q,
-        total_k, hq, hkv, d, bs, nb, ctypes.c_float(scale), 1 if causal else 0, ctypes.c_float(softcap),
+        total_k, hq, hkv, d, bs, nb, scale, 1 if causal else 0, softcap,
         _ptr(alibi_slopes), _ptr(first_keys), _ptr(prefix_lens), ws_ptr, ws_bytes, _dtype_code(q), handle)
     _lib.check("pkv_paged_varlen_prefill_attn_mod", st)
     return out
@@ -564,7 +564,7 @@ def paged_varlen_prefill_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     st = _lib.load().pkv_paged_varlen_prefill_attn_fp8(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(max_seqlen_q),
         int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], B, total_q, hq, hkv, d, bs, nb,
-        ctypes.c_float(scale), ctypes.c_float(k_scale), ctypes.c_float(v_scale), 1 if causal else 0, ws_ptr, ws_bytes,
+        scale, k_scale, v_scale, 1 if causal else 0, ws_ptr, ws_bytes,
         handle)
     _lib.check("pkv_paged_varlen_prefill_attn_fp8", st)
     return out
