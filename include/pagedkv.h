@@ -376,7 +376,7 @@ size_t pkv_paged_varlen_prefill_workspace_bytes(int32_t batch, int32_t num_q_hea
  * key before every first_keys value of a tile of rows is not read, and neither
  * is the table entry of a block that holds only such keys.
  *
- * softcap         0 = none, else finite and > 0
+ * softcap         0 = none, else in [1e-30, 1e30]
  * alibi_slopes    device, float32 [num_q_heads], or NULL
  * first_keys      device, int32, or NULL: [batch] for decode, [total_q] for the prefill call
  * prefix_lens     device, int32 [batch], or NULL: any value (clamped to [0, nk]); needs causal = 1
@@ -409,7 +409,7 @@ int pkv_paged_decode_attn_mod(void* out, const void* q, const void* k_cache, con
  * modifiers above; every other argument, the range checks, the optional
  * workspace and its size function are pkv_paged_varlen_prefill_attn's (short
  * chunks: pkv_paged_short_chunk_workspace_bytes).
- *   scale           finite and > 0
+ *   scale           finite and > 0 (not subnormal)
  * Supported: BF16; head_dim 64 or 128; G in {1, 2, 4, 8}; every block size
  * (a tile is gathered in pieces of gcd(block_size, 128) rows, so sizes that
  * share few factors of 2 with 128 take more copies).
@@ -452,7 +452,7 @@ size_t pkv_paged_short_chunk_workspace_bytes(int32_t batch, int32_t num_q_heads,
  *   q, out          device, bf16 [total_q, num_q_heads, head_dim]
  *   k_cache,v_cache device, E4M3 bytes [num_blocks, block_size, num_kv_heads, head_dim]
  *   k_scale,v_scale finite and > 0
- *   scale           finite and > 0
+ *   scale           finite and > 0 (not subnormal)
  *   other arguments, range checks, workspace and its size function as for
  *   pkv_paged_varlen_prefill_attn (short chunks:
  *   pkv_paged_short_chunk_workspace_bytes)

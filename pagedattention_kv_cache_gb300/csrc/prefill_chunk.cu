@@ -8,6 +8,8 @@
 //     out = sum_t softmax(s)_t V_t,
 // zeros when it sees none.  The row sees first_keys[row] <= t < nk with t <= p
 // (causal) or t < prefix_lens[i].
+#include <cfloat>
+
 #include "prefill_args.cuh"
 #include "score_mod.cuh"
 
@@ -25,7 +27,7 @@ int check_args(const PrefillArgs& a, int max_seqlen_k) {
   if (a.head_dim != 128 && a.head_dim != 64) return PKV_EUNSUPPORTED;
   if (a.group != 1 && a.group != 2 && a.group != 4 && a.group != 8) return PKV_EUNSUPPORTED;
   if (a.causal != 0 && a.causal != 1) return PKV_EINVAL;
-  if (!(a.scale > 0.f) || isinf(a.scale)) return PKV_EINVAL;
+  if (!(a.scale >= FLT_MIN) || isinf(a.scale)) return PKV_EINVAL;
   if (a.batch == 0 || a.max_seqlen_q == 0 || a.total_q == 0) return 1;
   if (!a.out || !a.q || !a.cu_q || !a.cu_k) return PKV_EINVAL;
   if (a.block_tables) {

@@ -145,34 +145,42 @@ static_assert(NUM_BARS * 8 + 16 <= 256, "barrier area too small");
 enum Form { kPlain, kMasked, kCapped, kBiased, kCappedBiased, kE4m3 };
 
 // c log2e tanh(k s) of a raw score s as s P(s^2), k = raw_to_x: P of degree 2
-// for |k s| <= 1/2 and of degree 4 for |k s| <= 1.  The coefficients of tanh
-// minimise the largest error of x P(x^2) (a reweighted least-squares fit); it is
-// 5.3e-6 and 2.8e-6, 2.7e-4 in a score capped at 50, which changes a weight by
-// less than a tenth of its bf16 rounding.  c log2e and the powers of k are
-// folded in (k within 2^+-12 keeps k^9 far inside fp32; other k take the
-// exponentials).
+// for |k s| <= 0.4 and of degree 4 for |k s| <= 1.  The coefficients of tanh(x) / x
+// minimise its largest relative error (a reweighted least-squares fit), 6.2e-6
+// and 6.9e-6: a score of 20 is off by 1.2e-4 or less, which changes a weight by a
+// thirtieth of its bf16 rounding.  c log2e and the powers of k are folded in; a
+// tier whose coefficients leave fp32's normal range is not used.
 struct TanhPoly {
   float near[3];
   float wide[5];
-  float near_limit;  // raw scores up to here take `near`, up to wide_limit `wide`
+  float near_limit;  // raw scores up to here take `near`, up to wide_limit `wide` (-infinity: tier not used)
   float wide_limit;
 };
 
 inline TanhPoly make_tanh_poly(float cap_log2, float k) {
-  constexpr double near[3] = {0.9999248302164969, -0.3308550498666596, 0.11254137113152551};
-  constexpr double wide[5] = {0.9999684694472680, -0.33265823169460657, 0.12922066707514057, -0.0432998613731271,
-                              0.008365885392756466};
+  constexpr double near[3] = {0.9999937531147292, -0.3326257940886756, 0.12127786248978804};
+  constexpr double wide[5] = {0.9999930893432413, -0.3329806519023404, 0.13036811004581145, -0.04481755092515754,
+                              0.009036422447889145};
   TanhPoly p{};
-  p.near_limit = p.wide_limit = -1.f;
-  if (!(k >= 0x1p-12f && k <= 0x1p12f)) return p;
+  bool near_ok = true, wide_ok = true;
   double power = static_cast<double>(cap_log2) * k;
   for (int i = 0; i < 5; ++i) {
-    if (i < 3) p.near[i] = static_cast<float>(near[i] * power);
+    if (i < 3) {
+      p.near[i] = static_cast<float>(near[i] * power);
+      near_ok = near_ok && std::isnormal(p.near[i]);
+    }
     p.wide[i] = static_cast<float>(wide[i] * power);
+    wide_ok = wide_ok && std::isnormal(p.wide[i]);
     power *= static_cast<double>(k) * k;
   }
-  p.near_limit = 0.5f / k;
-  p.wide_limit = 1.0f / k;
+  // (scores whose squares overflow are beyond both: 1 / k < 2^60)
+  const bool square_ok = k > 0x1p-60f;
+  p.near_limit = near_ok && square_ok ? 0.4f / k : -INFINITY;
+  p.wide_limit = wide_ok && square_ok ? 1.0f / k : -INFINITY;
+  // an unused tier still sees tiles in which every key is hidden: any positive
+  // polynomial keeps -infinity
+  if (!near_ok) std::fill_n(p.near, 3, 1.f);
+  if (!wide_ok) std::fill_n(p.wide, 5, 1.f);
   return p;
 }
 
@@ -973,9 +981,10 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         named_barrier_sync(pair_id, 64);
         top = fmaxf(*red_at(0, 0), *red_at(0, 1));
         const int exponent = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127 for zero and subnormals
-        const int ex = min(max(14 - exponent, -100), 100);
+        const int ex = min(max(14 - exponent, -113), 126);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-        mul *= __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        // (kept above zero: -infinity, a hidden key, times it stays -infinity)
+        mul = fmaxf(mul * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23), FLT_MIN);
 #pragma unroll
         for (int i = 0; i < kChunksHalf; ++i) {
           float f[8];
@@ -1060,11 +1069,11 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       uint64_t l_pair[2] = {0, 0};
       if constexpr (kCap && !kBias) {
         // tanh is monotone, so the maximum was taken on raw scores.  Below the
-        // polynomials' range s P(s^2) keeps falling, past c log2e tanh(-1/2) or
+        // polynomials' range s P(s^2) keeps falling, past c log2e tanh(-0.4) or
         // tanh(-1); such keys' weights are below e^-20 either way when m is that far
         // above, so only the largest score is compared with the range.
         const bool none = m_run == -INFINITY;
-        const bool near = none || (mt <= p.tanh_poly.near_limit && m_run + 0.462f * p.mod.cap_log2 >= 20.f * kLog2e);
+        const bool near = none || (mt <= p.tanh_poly.near_limit && m_run + 0.379f * p.mod.cap_log2 >= 20.f * kLog2e);
         const bool wide = none || (mt <= p.tanh_poly.wide_limit && m_run + 0.761f * p.mod.cap_log2 >= 20.f * kLog2e);
         const uint64_t neg_m = pack2(-m_use, -m_use);
         if (__all_sync(0xffffffffu, near)) {

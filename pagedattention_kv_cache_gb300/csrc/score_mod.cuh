@@ -4,6 +4,9 @@
 //     biased:  - slope_h log2e |p - t|
 #pragma once
 
+#include <cfloat>
+#include <cmath>
+
 #include "common.cuh"
 
 namespace pkv {
@@ -25,7 +28,7 @@ inline ScoreMod make_score_mod(float raw_scale, float softcap, const float* slop
   ScoreMod m;
   if (softcap > 0.f) {
     m.cap_log2 = softcap * kLog2e;
-    m.raw_to_x = raw_scale / softcap;
+    m.raw_to_x = fmaxf(fminf(raw_scale / softcap, FLT_MAX), -FLT_MAX);
   }
   m.slopes = slopes;
   m.first_keys = first_keys;
@@ -33,8 +36,8 @@ inline ScoreMod make_score_mod(float raw_scale, float softcap, const float* slop
   return m;
 }
 
-// 0 or finite and positive (a NaN fails both).
-inline bool softcap_valid(float softcap) { return softcap >= 0.f && softcap <= 3.0e38f; }
+// 0 or in [1e-30, 1e30], where c log2e and scale / c stay inside fp32 (a NaN fails both).
+inline bool softcap_valid(float softcap) { return softcap == 0.f || (softcap >= 1e-30f && softcap <= 1e30f); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -42,12 +45,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// tanh(x) = 1 - 2 / (1 + e^2x): two special-function operations.  Its error is
-// absolute, about 2^-22 (the sum 1 + e^2x is rounded once, the quotient once),
-// which is what counts in a score: c log2e 2^-22 is 2e-5 for a cap of 50.
-// Overflow of e^2x gives 1, underflow -1, a NaN stays one.
+// tanh(x) = 1 - 2 / (1 + e^2x), whose error is absolute, about 2^-22; below 1/4
+// the first four terms of the series instead, so that the error is relative
+// (1.2e-6) and a large cap costs no accuracy.  Overflow of e^2x gives 1,
+// underflow -1, a NaN stays one.
 __device__ __forceinline__ float tanh_by_exp(float x) {
-  return 1.f - __fdividef(2.f, 1.f + ex2(x * (2.f * kLog2e)));
+  const float y = x * x;
+  const float series = x * fmaf(y, fmaf(y, fmaf(y, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  return fabsf(x) < 0.25f ? series : 1.f - __fdividef(2.f, 1.f + ex2(x * (2.f * kLog2e)));
 }
 
 }  // namespace pkv

@@ -8,7 +8,7 @@ import torch
 # Half a step of a rounding, relative to the value.
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 # A score's error: a dot product of d <= 128 terms in fp32 with sum |q k| scale <= 25 is off by at
-# most 128 * 2^-24 * 25 = 2e-4; a cap c <= 60 adds c * 4e-6 = 2.4e-4 (the kernels' tanh); the two
+# most 128 * 2^-24 * 25 = 2e-4; a cap adds 7e-6 of the score (the kernels' tanh), 1.8e-4 of 25; the two
 # together stay below 5e-4, and a weight's relative error (numerator and sum) below twice that.
 SCORE = 1e-3
 

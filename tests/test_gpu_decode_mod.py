@@ -111,6 +111,12 @@ def test_scores_far_beyond_the_cap():
     check(_run(q, kc, vc, table, lens, 128 ** -0.5, softcap=5.0), ref, dev, torch.bfloat16, 333)
 
 
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 1.0, 300.0, 1e4, 1e6, 1e30])
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 128), (torch.float32, 64)])
+def test_caps_of_every_size(cap, dtype, d):
+    _compare(21, LENS, None, cap, False, d=d, dtype=dtype)
+
+
 def test_scores_that_overflow_are_capped():
     # every product of a key has that key's sign and is beyond float32: the score is +-infinity, the capped score
     # +-5.  (Products of both signs would sum to infinity - infinity, which float32 scores leave undefined.)

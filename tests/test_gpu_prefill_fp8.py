@@ -84,7 +84,7 @@ def test_full_attention():
 
 
 # q far outside f16's range either way: each row is scaled by a power of two, and a row of zeros stays one
-@pytest.mark.parametrize("q_scale", [0.0, 1e-30, 1e-6, 30.0, 3e4, 1e9])
+@pytest.mark.parametrize("q_scale", [0.0, 1e-37, 1e-30, 1e-6, 30.0, 3e4, 1e9, 1e36])
 def test_q_magnitudes(q_scale):
     c = Case(61, [40, 0], [130, 20], q_scale=q_scale)
     c.q[5] = 0

@@ -196,6 +196,13 @@ def test_scores_around_and_far_beyond_the_cap(q_scale, cap):
     Case(35, [100, 0], [140, 60], q_scale=q_scale).compare(cap=cap)
 
 
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 1.0, 300.0, 1e4, 1e6, 1e30])
+def test_caps_of_every_size(cap):
+    c = Case(41, [100, 0], [140, 60])
+    c.compare(cap=cap)
+    c.compare(cap=cap, alibi=True)
+
+
 def test_scores_that_overflow_are_capped():
     # every product of a key has that key's sign and is beyond float32: the score is +-infinity, the capped score +-5
     c = Case(35, [100, 0], [140, 60], q_scale=1e30)

@@ -100,6 +100,7 @@ def _decode(**kw):
 
 @pytest.mark.parametrize("change,status", [
     (dict(cap=-1.0), "EINVAL"), (dict(cap=float("nan")), "EINVAL"), (dict(cap=float("inf")), "EINVAL"),
+    (dict(cap=1e-31), "EINVAL"), (dict(cap=1e31), "EINVAL"),
     (dict(out=None), "EINVAL"), (dict(hq=3), "EINVAL"), (dict(splits=-1), "EINVAL"), (dict(bs=0), "EINVAL"),
     (dict(d=96), "EUNSUPPORTED"), (dict(hkv=16, hq=16), "EUNSUPPORTED"), (dict(dtype=7), "EUNSUPPORTED"),
     (dict(q=P + 8), "EALIGN"), (dict(batch=0), "OK")])
@@ -121,6 +122,7 @@ def _prefill_mod(**kw):
 @pytest.mark.parametrize("change,status", [
     (dict(cap=-1.0), "EINVAL"), (dict(cap=float("nan")), "EINVAL"), (dict(prefix=P, causal=0), "EINVAL"),
     (dict(scale=0.0), "EINVAL"), (dict(scale=-1.0), "EINVAL"), (dict(scale=float("nan")), "EINVAL"),
+    (dict(scale=1e-39), "EINVAL"), (dict(cap=1e31), "EINVAL"),
     (dict(causal=2), "EINVAL"), (dict(bt=None), "EINVAL"), (dict(bt=None, k=P, v=P, tk=0), "EINVAL"),
     (dict(bs=0), "EINVAL"), (dict(nb=0), "EINVAL"), (dict(nb=1 << 30, bs=16), "EINVAL"), (dict(cq=None), "EINVAL"),
     (dict(hq=12, hkv=2), "EUNSUPPORTED"), (dict(d=80), "EUNSUPPORTED"), (dict(dtype=_lib.F32), "EUNSUPPORTED"),
