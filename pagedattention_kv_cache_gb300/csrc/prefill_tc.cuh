@@ -49,8 +49,11 @@
 //          holds its 64 scores in registers at a cap of 96, and one kernel that
 //          branched on the modifiers at run time spilled (a batch of 16 chunks,
 //          56 GFLOP, no modifier given: 70.7 us against the plain kernel's 62.6).
-//   kFp8   an E4M3 cache: raw codes arrive in a ring of 64-key half tiles, and
-//          two more warps widen them to f16 in the K and V rings.
+//   kFp8   an E4M3 cache: a tile's codes arrive in part of its K or V stage, and
+//          two more warps widen them to f16 in place, a quarter of the tile (32
+//          keys) at a time through registers.  (A ring of its own for the codes
+//          fitted three half tiles; the loads in flight bounded it: a batch of 16
+//          chunks, 56 GFLOP, 79 us.)
 #pragma once
 
 #include <algorithm>
@@ -72,7 +75,7 @@ template <bool kFp8>
 constexpr int threads() {
   return 32 * (2 + 2 * kSoftmaxWarps + (kFp8 ? kWidenWarps : 0));
 }
-constexpr int kRawRows = 64;  // kFp8: keys per slot of the raw-code ring (half a tile)
+constexpr int kQuarter = 32;  // kFp8: keys widened at a time
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;    // S_A at 0, S_B at 128
 constexpr uint32_t kColO = 256;  // O_A at 256, O_B at 384
@@ -83,25 +86,20 @@ constexpr uint32_t kRedBytes = 2 * 2 * 2 * kBM * 4;  // row maxima / sums exchan
 // Sizes for head dimension D (64 or 128): a row of D bf16 is D / 64 slabs of
 // 128 bytes (one 128-byte swizzle atom each), and each slab of a tile is a
 // TMA box of its own.
-template <int D, bool kFp8 = false>
+template <int D>
 struct Geo {
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   static constexpr int kSlabs = D / 64;
   static constexpr uint32_t kTileQ = kSlabs * kSlabQ;
   static constexpr uint32_t kTileKV = kSlabs * kSlabKV;
-  // kFp8: slots of raw codes, as many as shared memory holds beside the f16 rings
-  static constexpr int kRawSlots = kFp8 ? (D == 128 ? 3 : 6) : 0;
-  static constexpr uint32_t kRawSlot = kRawRows * D;
-  static constexpr uint32_t kRawOffset = 2 * kTileQ + 2 * kStages * kTileKV;
-  static constexpr uint32_t kRedOffset = kRawOffset + kRawSlots * kRawSlot;
+  static constexpr uint32_t kRedOffset = 2 * kTileQ + 2 * kStages * kTileKV;
   static constexpr uint32_t kBarOffset = kRedOffset + kRedBytes;
   static constexpr uint32_t kSmemBytes = kBarOffset + 256 + 1024;  // barriers + 1 KB for alignment
   // one CTA per SM even when two would fit (each holds all 512 TMEM columns)
   static constexpr uint32_t kLaunchSmem = kSmemBytes > 120 * 1024 ? kSmemBytes : 120 * 1024;
   static constexpr size_t kRecordBytes = static_cast<size_t>(kBM) * D * 4 + static_cast<size_t>(kBM) * 8;
 };
-static_assert(Geo<128>::kSmemBytes <= 227 * 1024 && Geo<128, true>::kSmemBytes <= 227 * 1024,
-              "shared memory plan exceeds an SM");
+static_assert(Geo<128>::kSmemBytes <= 227 * 1024, "shared memory plan exceeds an SM");
 constexpr float kRescaleLog2 = 8.0f;
 
 // Key-range split of long work items, used only when the pairs do not fill
@@ -136,9 +134,8 @@ enum Bar {
   V_TAIL = O_FINAL + 2,
   V_HEAD,  // kMod: the first V tile, once its rows before the first visible key are zeroed
   Q_READY,  // kFp8: Q rewritten as scaled f16
-  RAW_FULL,
-  RAW_EMPTY = RAW_FULL + 6,
-  NUM_BARS = RAW_EMPTY + 6
+  RAW_FULL,  // kFp8, per K stage, then per V stage: the codes have arrived
+  NUM_BARS = RAW_FULL + 2 * kStages
 };
 static_assert(NUM_BARS * 8 + 16 <= 256, "barrier area too small");
 
@@ -376,6 +373,10 @@ __device__ __forceinline__ void cap_scores(const TcParams& p, uint32_t* r) {
   } else if (!__any_sync(0xffffffffu, top > p.tanh_poly.wide_limit)) {
 #pragma unroll
     for (int e = 0; e < 64; e += 2) unpack2u(capped_pair(r[e], r[e + 1], p.tanh_poly.wide, 0ull), r[e], r[e + 1]);
+  } else if (p.mod.cap_log2 <= kAbsCapLog2) {
+#pragma unroll
+    for (int e = 0; e < 64; ++e)
+      r[e] = __float_as_uint(p.mod.cap_log2 * tanh_by_exp_abs(__uint_as_float(r[e]) * p.mod.raw_to_x));
   } else {
 #pragma unroll
     for (int e = 0; e < 64; ++e)
@@ -500,8 +501,8 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   unsigned char* sq = smem;  // Q_A, then Q_B
   unsigned char* sk = sq + 2 * kTileQ;
   unsigned char* sv = sk + kStages * kTileKV;
-  float* red = reinterpret_cast<float*>(smem + Geo<D, kFp8>::kRedOffset);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Geo<D, kFp8>::kBarOffset);
+  float* red = reinterpret_cast<float*>(smem + Geo<D>::kRedOffset);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Geo<D>::kBarOffset);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_ticket = abort_flag + 1;  // split tiles' tickets, one per query tile
@@ -515,8 +516,8 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     *abort_flag = 0;
     mbar_init(&bars[Q_FULL], 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars[K_FULL + s], kFp8 ? 2 * kWidenWarps : 1);  // kFp8: every widening warp, for both halves
-      mbar_init(&bars[V_FULL + s], kFp8 ? 2 * kWidenWarps : 1);
+      mbar_init(&bars[K_FULL + s], kFp8 ? kWidenWarps : 1);
+      mbar_init(&bars[V_FULL + s], kFp8 ? kWidenWarps : 1);
       mbar_init(&bars[K_EMPTY + s], 1);
       mbar_init(&bars[V_EMPTY + s], 1);
     }
@@ -530,18 +531,22 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     if constexpr (kMod) mbar_init(&bars[V_HEAD], 1);
     if constexpr (kFp8) {
       mbar_init(&bars[Q_READY], 2 * kSoftmaxWarps);
-      for (int s = 0; s < Geo<D, kFp8>::kRawSlots; ++s) {
-        mbar_init(&bars[RAW_FULL + s], 1);
-        mbar_init(&bars[RAW_EMPTY + s], kWidenWarps);
-      }
+      for (int s = 0; s < 2 * kStages; ++s) mbar_init(&bars[RAW_FULL + s], 1);
     }
     fence_mbar_init();
   }
   const Waiter wait{abort_flag, p.err};
+  // kFp8: where the codes of row r of a tile lie in its stage
+  auto raw_offset = [](int r) -> uint32_t {
+    return D == 128 ? kSlabKV + r * 128 : (r / kQuarter) * (kQuarter * 128) + kQuarter * 64 + (r % kQuarter) * 64;
+  };
   // Loads tile j's K (is_v = false) or V into stage j % kStages, after the
   // stage's previous occupant (tile j - kStages) was released.  One thread issues
-  // the plain kernel's copies; with kMod the whole warp does, a piece per lane
-  // (block sizes that share few factors of 2 with 128 make many pieces).
+  // the plain kernel's copies; the other forms' the whole warp, a piece per lane
+  // (block sizes that share few factors of 2 with 128 make many pieces).  kFp8:
+  // the codes of each quarter go to the end of its own part of the stage, which the
+  // widened rows then take: at head_dim 128 the rows of the second slab, at 64 the
+  // second half of the quarter's rows.
   auto load_tile = [&](int j, bool is_v) {
     const int st = j % kStages;
     const int use = j / kStages;
@@ -550,6 +555,31 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     unsigned char* dst = (is_v ? sv : sk) + st * kTileKV;
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
     const int key0 = (j0 + j) * kBN;
+    if constexpr (kFp8) {
+      __syncwarp();
+      uint64_t* raw_full = &bars[RAW_FULL + (is_v ? kStages : 0) + st];
+      for (int r = lane * p.piece_rows; r < kBN; r += 32 * p.piece_rows) {
+        const int key = key0 + r;
+        if (key >= nk) continue;
+        const int blk = key / p.block_size;
+        const int phys = __ldg(table + blk);
+        if (phys < 0 || phys >= p.num_blocks) {
+          raise_error(p.err, PKV_DERR_BLOCK_RANGE);
+          continue;
+        }
+        const int row = phys * p.block_size + (key - blk * p.block_size);
+        unsigned char* to = dst + raw_offset(r);
+        mbar_expect_tx(raw_full, p.piece_rows * D);
+        if (p.piece_rows > 1)
+          tc::tma_load_3d(to, map, 0, g, row, raw_full);
+        else  // a tensor copy of one 64-byte row could start off its 128-byte boundary
+          bulk_g2s(to, (is_v ? p.v_codes : p.k_codes) + (static_cast<size_t>(row) * p.hkv + g) * D, D, raw_full,
+                   l2_normal_policy());
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(raw_full);
+      return;
+    }
     if constexpr (kMod) {
       __syncwarp();
       const int piece = p.paged ? p.piece_rows : kBN;
@@ -599,39 +629,6 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     }
     mbar_arrive(full);
   };
-  // kFp8: the codes of half tile n (K and V tiles alternate, two halves each) into
-  // slot n % kRawSlots of the raw ring, a piece per lane of the calling warp
-  auto load_raw = [&](int n) {
-    constexpr int kSlots = kFp8 ? Geo<D, kFp8>::kRawSlots : 1;
-    const int slot = n % kSlots;
-    const int use = n / kSlots;
-    const bool is_v = (n >> 1) & 1;
-    uint64_t* full = &bars[RAW_FULL + slot];
-    if (use > 0) wait(&bars[RAW_EMPTY + slot], (use - 1) & 1);
-    __syncwarp();
-    unsigned char* dst = smem + Geo<D, kFp8>::kRawOffset + slot * Geo<D, kFp8>::kRawSlot;
-    const int key0 = (j0 + (n >> 2)) * kBN + (n & 1) * kRawRows;
-    for (int r = lane * p.piece_rows; r < kRawRows; r += 32 * p.piece_rows) {
-      const int key = key0 + r;
-      if (key >= nk) continue;
-      const int blk = key / p.block_size;
-      const int phys = __ldg(table + blk);
-      if (phys < 0 || phys >= p.num_blocks) {
-        raise_error(p.err, PKV_DERR_BLOCK_RANGE);
-        continue;
-      }
-      const int row = phys * p.block_size + (key - blk * p.block_size);
-      mbar_expect_tx(full, p.piece_rows * D);
-      if (p.piece_rows > 1)
-        tc::tma_load_3d(dst + r * D, is_v ? &tm_v : &tm_k, 0, g, row, full);
-      else  // a tensor copy of one 64-byte row could start off its 128-byte boundary
-        bulk_g2s(dst + r * D, (is_v ? p.v_codes : p.k_codes) + (static_cast<size_t>(row) * p.hkv + g) * D, D, full,
-                 l2_normal_policy());
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full);
-  };
-  const int n_raw_early = kFp8 ? min(4 * n_tiles, Geo<D, kFp8>::kRawSlots) : 0;
   // the producer thread issues Q and the first K/V tiles (stages still free)
   // before the CTA-wide sync, so their latency overlaps the TMEM allocation
   const int n_early = min(n_tiles, kStages);
@@ -657,13 +654,9 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   if constexpr (kMod || kFp8) {
     if (warp == 0) {
       __syncwarp();  // the barriers are initialised
-      if constexpr (kFp8) {
-        for (int n = 0; n < n_raw_early; ++n) load_raw(n);
-      } else {
-        for (int j = 0; j < n_early; ++j) {
-          load_tile(j, false);
-          load_tile(j, true);
-        }
+      for (int j = 0; j < n_early; ++j) {
+        load_tile(j, false);
+        load_tile(j, true);
       }
     }
   }
@@ -694,7 +687,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     };
     if constexpr (kFp8) {
       if (parts > 1 && p.piece_rows > 1) {  // as below
-        for (int key = j0 * kBN + n_raw_early / 4 * kRawRows + lane * p.piece_rows; key < min((j0 + n_tiles) * kBN, nk);
+        for (int key = (j0 + n_early) * kBN + lane * p.piece_rows; key < min((j0 + n_tiles) * kBN, nk);
              key += 32 * p.piece_rows) {
           const int blk = key / p.block_size;
           const int phys = __ldg(table + blk);
@@ -705,7 +698,10 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         }
         __syncwarp();
       }
-      for (int n = n_raw_early; n < 4 * n_tiles; ++n) load_raw(n);
+      for (int j = n_early; j < n_tiles; ++j) {
+        load_tile(j, false);
+        load_tile(j, true);
+      }
     } else if constexpr (kMod) {
       if (parts > 1) {
         // a split part streams a key range no other CTA reads: request it into
@@ -859,64 +855,63 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     }
   } else if (kFp8 && warp >= 2 + 2 * kSoftmaxWarps) {
     // ------------------------------------------------------------ kFp8: widen codes to f16
-    // Each warp takes 32 rows of every half tile.  Sixteen codes (one 16-byte
-    // chunk) become two chunks of the swizzled f16 row.  A group of eight lanes
-    // takes two neighbouring rows, at head_dim 128 from opposite slabs: its loads
-    // cover 128 distinct bytes modulo 128, and its stores the even chunk positions
-    // of one row and the odd ones of the other, so neither has bank conflicts.
-    constexpr int kSlots = kFp8 ? Geo<D, kFp8>::kRawSlots : 1;
+    // Each warp takes two quarters of every tile: a quarter's codes go to registers,
+    // then their f16 rows over them.  Sixteen codes (one 16-byte chunk) become two
+    // chunks of the swizzled f16 row.  A group of eight lanes takes two
+    // neighbouring rows, at head_dim 128 from opposite slabs: its loads cover 128
+    // distinct bytes modulo 128, and its stores the even chunk positions of one row
+    // and the odd ones of the other, so neither has bank conflicts.
     constexpr int kIter = D / 16;
     const int me = warp - 2 - 2 * kSoftmaxWarps;
     const int odd = (lane >> 2) & 1;
-    const int row0 = me * 32 + 2 * (lane >> 3) + odd;  // + 8 per two (head_dim 128) or one iterations
+    const int row0 = 2 * (lane >> 3) + odd;  // in the quarter; + 8 per two (head_dim 128) or one iterations
     const uint32_t at0 = ((2 * (lane & 3)) ^ (row0 & 7)) << 4;
-    for (int n = 0; n < 4 * n_tiles; ++n) {
-      const int slot = n % kSlots;
-      const int j = n >> 2;
-      const bool is_v = (n >> 1) & 1;
-      const int half = n & 1;
+    for (int n = 0; n < 2 * n_tiles; ++n) {
+      const int j = n >> 1;
+      const bool is_v = n & 1;
       const int st = j % kStages;
-      wait(&bars[RAW_FULL + slot], (n / kSlots) & 1);
-      const unsigned char* raw =
-          smem + Geo<D, kFp8>::kRawOffset + slot * Geo<D, kFp8>::kRawSlot + row0 * D + (lane & 3) * 16;
-      uint4 codes[kIter];
+      unsigned char* stage = (is_v ? sv : sk) + st * kTileKV;
+      wait(&bars[RAW_FULL + (is_v ? kStages : 0) + st], (j / kStages) & 1);
 #pragma unroll
-      for (int i = 0; i < kIter; ++i) {
-        if constexpr (D == 128)
-          codes[i] = lds128(raw + (i >> 1) * 8 * D + ((i & 1) ^ odd) * 64);
-        else
-          codes[i] = lds128(raw + i * 8 * D);
-      }
-      if (half == 0 && j >= kStages) wait(&bars[(is_v ? V_EMPTY : K_EMPTY) + st], (j / kStages - 1) & 1);
-      unsigned char* dst = (is_v ? sv : sk) + st * kTileKV + (half * kRawRows + row0) * 128 + at0;
-      const int rows = nk - (j0 + j) * kBN - half * kRawRows - row0;  // row0 + i of the half tile holds a key: i < rows
-      auto widen = [&](bool partial) {
+      for (int h = 0; h < 2; ++h) {
+        const int first = (2 * me + h) * kQuarter;  // first row of the quarter
+        const unsigned char* raw = stage + raw_offset(first) + row0 * D + (lane & 3) * 16;
+        uint4 codes[kIter];
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
-          const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-          uint32_t f[8];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) e4m3x4_to_f16x4(w[u], f[2 * u], f[2 * u + 1]);
-          const int step = D == 128 ? (i >> 1) * 8 : i * 8;
-          if (partial && step >= rows) {  // past the last key: whatever the slot holds
-#pragma unroll
-            for (int u = 0; u < 8; ++u) f[u] = 0u;
-          }
-          unsigned char* to = dst + step * 128 + (D == 128 ? ((i & 1) ^ odd) * kSlabKV : 0);
-          *reinterpret_cast<uint4*>(to) = make_uint4(f[0], f[1], f[2], f[3]);
-          *reinterpret_cast<uint4*>(to + (at0 & 16 ? -16 : 16)) = make_uint4(f[4], f[5], f[6], f[7]);
+          if constexpr (D == 128)
+            codes[i] = lds128(raw + (i >> 1) * 8 * D + ((i & 1) ^ odd) * 64);
+          else
+            codes[i] = lds128(raw + i * 8 * D);
         }
-      };
-      if (nk >= (j0 + j) * kBN + (half + 1) * kRawRows)
-        widen(false);
-      else
-        widen(true);
+        __syncwarp();  // every code of the quarter is in registers
+        unsigned char* dst = stage + (first + row0) * 128 + at0;
+        const int rows = nk - (j0 + j) * kBN - first - row0;  // row0 + i of the quarter holds a key: i < rows
+        auto widen = [&](bool partial) {
+#pragma unroll
+          for (int i = 0; i < kIter; ++i) {
+            const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) e4m3x4_to_f16x4(w[u], f[2 * u], f[2 * u + 1]);
+            const int step = D == 128 ? (i >> 1) * 8 : i * 8;
+            if (partial && step >= rows) {  // past the last key: whatever the stage held
+#pragma unroll
+              for (int u = 0; u < 8; ++u) f[u] = 0u;
+            }
+            unsigned char* to = dst + step * 128 + (D == 128 ? ((i & 1) ^ odd) * kSlabKV : 0);
+            *reinterpret_cast<uint4*>(to) = make_uint4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<uint4*>(to + (at0 & 16 ? -16 : 16)) = make_uint4(f[4], f[5], f[6], f[7]);
+          }
+        };
+        if (nk >= (j0 + j) * kBN + first + kQuarter)
+          widen(false);
+        else
+          widen(true);
+      }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars[RAW_EMPTY + slot]);
-        mbar_arrive(&bars[(is_v ? V_FULL : K_FULL) + st]);
-      }
+      if (lane == 0) mbar_arrive(&bars[(is_v ? V_FULL : K_FULL) + st]);
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue of tile X, one half of the keys
@@ -970,10 +965,12 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
           return reinterpret_cast<uint4*>(q_row + ((ch ^ (row & 7)) << 4));
         };
         float top = 0.f;
+        uint4 qc[kChunksHalf];
 #pragma unroll
         for (int i = 0; i < kChunksHalf; ++i) {
+          qc[i] = *q_chunk(i);
           float f[8];
-          Chunk<__nv_bfloat16>::unpack(*q_chunk(i), f);
+          Chunk<__nv_bfloat16>::unpack(qc[i], f);
 #pragma unroll
           for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(f[u]));
         }
@@ -988,7 +985,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
 #pragma unroll
         for (int i = 0; i < kChunksHalf; ++i) {
           float f[8];
-          Chunk<__nv_bfloat16>::unpack(*q_chunk(i), f);
+          Chunk<__nv_bfloat16>::unpack(qc[i], f);
           *q_chunk(i) = make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
                                    pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
         }
@@ -1085,12 +1082,18 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
           for (int e = 0; e < 32; ++e)
             r[e] = exp2_of_pair_bf16(capped_pair(r[2 * e], r[2 * e + 1], p.tanh_poly.wide, neg_m), l_pair[e % 2]);
         } else {
+          auto cap_all = [&](auto&& tanh_of) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            const float s = __uint_as_float(r[e]);
-            const float z = p.mod.cap_log2 * tanh_by_exp(s * p.mod.raw_to_x);
-            r[e] = __float_as_uint(masked && s == -INFINITY ? s : z);
-          }
+            for (int e = 0; e < 64; ++e) {
+              const float s = __uint_as_float(r[e]);
+              const float z = p.mod.cap_log2 * tanh_of(s * p.mod.raw_to_x);
+              r[e] = __float_as_uint(masked && s == -INFINITY ? s : z);
+            }
+          };
+          if (p.mod.cap_log2 <= kAbsCapLog2)
+            cap_all([](float x) { return tanh_by_exp_abs(x); });
+          else
+            cap_all([](float x) { return tanh_by_exp(x); });
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = exp2_pair_bf16(r[2 * e], r[2 * e + 1], 1.f, -m_use, l_pair[e % 2]);
         }
@@ -1335,7 +1338,7 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
   alignas(64) CUtensorMap tm_q, tm_k, tm_v;
   if (encode_bf16_3d(&tm_q, a.q, kD, a.hq, a.total_q, 64, G, TQ) != PKV_OK) return PKV_ECUDA;
   const bool paged = a.block_tables != nullptr;
-  const int piece = paged ? piece_rows(a, kFp8 ? kRawRows : kBN) : kBN;
+  const int piece = paged ? piece_rows(a, kFp8 && D == 64 ? kQuarter : kBN) : kBN;
   const void* kb = paged ? a.k_cache : a.k;
   const void* vb = paged ? a.v_cache : a.v;
   const uint64_t rows = paged ? static_cast<uint64_t>(a.num_blocks) * a.block_size : a.total_k;
@@ -1390,7 +1393,7 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
     p.records = ws + 2 * flags;
   }
   auto kernel = prefill_tc_kernel<G, D, kForm>;
-  constexpr uint32_t kSmemBytes = Geo<D, kFp8>::kLaunchSmem;
+  constexpr uint32_t kSmemBytes = Geo<D>::kLaunchSmem;
   static std::atomic<uint64_t> smem_allowed{0};
   if (allow_smem(kernel, kSmemBytes, smem_allowed) != cudaSuccess) return PKV_ECUDA;
   dim3 grid(a.batch * a.hkv, pairs * p.parts_max);

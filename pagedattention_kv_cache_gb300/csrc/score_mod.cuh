@@ -45,14 +45,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// tanh(x) = 1 - 2 / (1 + e^2x), whose error is absolute, about 2^-22; below 1/4
-// the first four terms of the series instead, so that the error is relative
-// (1.2e-6) and a large cap costs no accuracy.  Overflow of e^2x gives 1,
-// underflow -1, a NaN stays one.
+// tanh(x) = 1 - 2 / (1 + e^2x), whose error is absolute, about 2^-22.  Overflow
+// of e^2x gives 1, underflow -1, a NaN stays one.
+__device__ __forceinline__ float tanh_by_exp_abs(float x) {
+  return 1.f - __fdividef(2.f, 1.f + ex2(x * (2.f * kLog2e)));
+}
+
+// The same with the first four terms of the series below 1/4, so that the error
+// is relative (1.2e-6) and a large cap costs no accuracy.
 __device__ __forceinline__ float tanh_by_exp(float x) {
   const float y = x * x;
   const float series = x * fmaf(y, fmaf(y, fmaf(y, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
-  return fabsf(x) < 0.25f ? series : 1.f - __fdividef(2.f, 1.f + ex2(x * (2.f * kLog2e)));
+  return fabsf(x) < 0.25f ? series : tanh_by_exp_abs(x);
 }
+
+// Caps (x log2 e) up to which the absolute error will do: 2^-22 of it is 1.2e-4.
+constexpr float kAbsCapLog2 = 512.f;
 
 }  // namespace pkv
