@@ -120,6 +120,17 @@ __device__ __forceinline__ void wait_or_abort(uint64_t* bar, uint32_t parity, vo
 
 __device__ __forceinline__ int align_tokens(const Params& p) { return p.align > 1 ? p.align : 1; }
 
+// What the automatic split rounds each sequence up to: the split alignment; in
+// the modified and chunk kernels at least kMinTokensPerCta, so that a CTA gets
+// few short sequences (each is a pass through the pipeline of its own: 85
+// sequences of 0 to 2 tokens on four CTAs took 146 us).
+template <bool kFew>
+__device__ __forceinline__ int count_align(const Params& p) {
+  const int a = align_tokens(p);
+  if constexpr (!kFew) return a;
+  return a > kMinTokensPerCta ? a : kMinTokensPerCta;
+}
+
 __device__ __forceinline__ long long round_up(long long n, int a) { return (n + a - 1) / a * a; }
 
 __device__ __forceinline__ int context_len(const Params& p, int b) {
@@ -194,7 +205,7 @@ template <bool kMod, bool kVar = false>
 __device__ void plan_auto(const Params& p, Plan& plan, long long* sh) {
   const int tid = threadIdx.x;
   const int nthreads = blockDim.x;
-  const int A = align_tokens(p);
+  const int A = count_align<kMod || kVar>(p);
   const long long grid = gridDim.x;
   if (p.batch <= nthreads) {
     // one pass when the batch fits the block: each thread loads one length,
@@ -312,7 +323,7 @@ __device__ __forceinline__ bool for_each_segment(const Params& p, const Plan& pl
   if (plan.b_first < 0) return true;
   // positions run over the flattened contexts, each rounded up to the split
   // alignment; a part's end is clipped to the sequence's real length
-  const int A = align_tokens(p);
+  const int A = count_align<kMod || kVar>(p);
   long long cu = plan.cu_first;
   for (int b = plan.b_first; b < p.batch && cu < plan.end; ++b) {
     const int ctx = seq_len<kVar>(p, b);
