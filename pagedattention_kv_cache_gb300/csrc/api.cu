@@ -103,13 +103,13 @@ int encode_u8_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64_t
 }
 
 int encode_paged_kv(void* map, const void* base, uint32_t block_size, uint32_t hkv, uint64_t num_blocks,
-                    int elem_bytes) {
+                    int elem_bytes, int head_dim) {
   std::call_once(g_encode_once, find_encode);
   if (!g_encode || (elem_bytes != 1 && elem_bytes != 2)) return PKV_ECUDA;
   // dims innermost first: head_dim, token in block, KV head, block; the
   // token stride (all heads of a token) is larger than the head stride
-  const cuuint64_t row = 128 * static_cast<cuuint64_t>(elem_bytes);
-  const cuuint64_t dims[4] = {128, block_size, hkv, num_blocks};
+  const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * elem_bytes;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(head_dim), block_size, hkv, num_blocks};
   const cuuint64_t strides[3] = {hkv * row, row, static_cast<cuuint64_t>(block_size) * hkv * row};
   const cuuint32_t box[4] = {128u / static_cast<cuuint32_t>(elem_bytes), 16, hkv, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};

@@ -44,14 +44,14 @@ int encode_bf16_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64
 int encode_u8_3d(void* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b2);
 
 // Encodes the 4-D tensor map of one paged K or V pool [num_blocks,
-// block_size, hkv, 128] whose box is 16 tokens of every KV head and 128 bytes
+// block_size, hkv, head_dim] whose box is 16 tokens of every KV head and 128 bytes
 // of head_dim, ordered (head, token) in shared memory with 128-byte swizzle:
 // rows of one head's 16 tokens are 128 bytes apart, so any eight consecutive
 // tokens fill the eight swizzle phases.  block_size must be a multiple of 16.
-// elem_bytes: 2 (bf16, box of 64 elements, two copies per 16-token box) or 1
-// (E4M3 codes, box of 128, one copy).
+// elem_bytes: 2 (bf16, box of 64 elements, one copy per 64 of head_dim and
+// 16-token box) or 1 (E4M3 codes, box of 128, one copy).
 int encode_paged_kv(void* map, const void* base, uint32_t block_size, uint32_t hkv, uint64_t num_blocks,
-                    int elem_bytes);
+                    int elem_bytes, int head_dim);
 
 // Launches kernel<<<grid, block, smem, stream>>>(args...) with programmatic
 // stream serialization allowed (see pdl_enter).

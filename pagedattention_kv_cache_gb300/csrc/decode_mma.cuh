@@ -60,14 +60,15 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* m
 // 16-key chunks a consumer warp takes per stage: two for an FP8 cache (its
 // stages hold twice the tokens in the same bytes, and the second chunk's
 // scores overlap the first's latency), one for bf16.
-template <typename TC>
+// A token row of 128 bytes (FP8, or bf16 with head_dim 64) takes two.
+template <typename TC, int D = 128>
 __host__ __device__ constexpr int mma_chunks_per_warp() {
-  return std::is_same<TC, __nv_fp8_e4m3>::value ? 2 : 1;
+  return D * sizeof(TC) == 128 ? 2 : 1;
 }
 
 // kVar: chunks of 1 to QL new tokens per sequence (cu_q / cu_k), R = G QL rows
 // of which a sequence uses its first G nq.
-template <int G, int QL, typename TC = __nv_bfloat16, bool kMod = false, bool kVar = false>
+template <int G, int QL, typename TC = __nv_bfloat16, bool kMod = false, bool kVar = false, int D = 128>
 __global__ void __launch_bounds__(288, 1)
     paged_decode_mma_kernel(const Params p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v) {
@@ -85,9 +86,9 @@ __global__ void __launch_bounds__(288, 1)
   using T = __nv_bfloat16;
   constexpr bool kFp8 = std::is_same<TC, __nv_fp8_e4m3>::value;
   constexpr int ES = static_cast<int>(sizeof(TC));  // bytes per cache element
-  constexpr int NH = ES;                             // tensor copies per K (or V) box: 128-byte rows
-  constexpr int NSUB = mma_chunks_per_warp<TC>();
-  constexpr int D = 128;
+  constexpr int NH = D * ES / 128;                   // tensor copies per K (or V) box: 128-byte rows
+  constexpr int NSUB = mma_chunks_per_warp<TC, D>();
+  constexpr int NK = D / 16;                         // k16 steps of Q K^T
   constexpr int R = G * QL;
   static_assert(R <= 16, "at most 16 rows per KV head");
   constexpr int HH = R <= 8 ? 1 : 2;  // fragment row halves (r0, r0 + 8) that hold query rows
@@ -95,7 +96,8 @@ __global__ void __launch_bounds__(288, 1)
   // M dimension (8 m-tiles of 16) and the rows in N: half the MMAs and half
   // the accumulator registers of O = P V, whose M rows 8..15 would be empty
   constexpr bool kT = HH == 1;
-  constexpr int NO = kT ? 8 : 16;
+  constexpr int NO = kT ? D / 16 : 16;
+  static_assert(D == 128 || (D == 64 && kT && !kFp8), "head_dim 64: bf16, at most 8 rows");
   constexpr float kRescale = 8.0f;
   const int rows_per_seq = QL * p.hq;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(288, 1)
   for_each_segment<kMod, kVar>(p, plan, [&](const Segment& seg) -> bool {
     // Q as the A operand: rows r0 / r0 + 8, columns 16 kk + 2c (+1) and + 8
     // (bf16), or 16 kk + 4c (+1) and 16 kk + 4c + 2 (+3) as scaled f16 (FP8)
-    uint32_t qf[8][4];
+    uint32_t qf[NK][4];
     float qmul[2] = {p.scale_log2, p.scale_log2};
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(288, 1)
           }
       } else {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
+        for (int kk = 0; kk < NK; ++kk) {
           qf[kk][hh] = qrow ? __ldg(qrow + kk * 8 + c) : 0u;
           qf[kk][2 + hh] = qrow ? __ldg(qrow + kk * 8 + 4 + c) : 0u;
         }
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(288, 1)
             }
           } else {
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
+            for (int k4 = 0; k4 < NK / 2; ++k4) {
 #pragma unroll
               for (int nb = 0; nb < 2; ++nb) {
                 uint32_t b[4];
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(288, 1)
               // O^T += V^T P^T: m-tile t covers head_dim 16t .. 16t + 15; the four
               // 8x8 matrices are (keys 0-7 | 8-15) x (head_dim 16t + 0-7 | + 8-15)
 #pragma unroll
-              for (int tm = 0; tm < 8; ++tm) {
+              for (int tm = 0; tm < NO; ++tm) {
                 uint32_t a[4];
                 pkv::ldsm_x4_trans(vbase + vrowt + (tm >> 2) * hs + (((2 * (tm & 3) + vjt) ^ xr) << 4), a);
                 pkv::mma_bf16_16816(o[tm], a, pf[0], pf[2]);

@@ -16,9 +16,9 @@ from _modified import check, cuda, i32, slopes_of
 pytestmark = pytest.mark.gpu
 
 
-def _weights(dtype, d):
-    """Type of the weights in the P V product: bf16 on the tensor-core kernel, else fp32."""
-    return torch.bfloat16 if dtype == torch.bfloat16 and d == 128 else torch.float32
+def _weights(dtype):
+    """Type of the weights in the P V product: bf16 on the tensor-core kernel (bf16 caches), else fp32."""
+    return dtype
 
 
 def _case(seed, *, lens, block_size, hq, hkv, d=128, dtype=torch.bfloat16, q_scale=3.0):
@@ -63,7 +63,7 @@ def _compare(seed, lens, first, cap, alibi, *, splits=0, block_size=16, hq=8, hk
     ref, dev = omod.decode_attention(as_np(q), as_np(kc), as_np(vc), table.numpy(), lens, d ** -0.5, cap, slopes, first)
     table = _hide(kc, vc, tables, lens, first, block_size, table)
     out = _run(q, kc, vc, table, ln, d ** -0.5, splits, softcap=cap, alibi_slopes=slopes, first_keys=first)
-    check(out, ref, dev, _weights(dtype, d), max(lens, default=0), f"cap {cap} alibi {alibi} first {first is not None}")
+    check(out, ref, dev, _weights(dtype), max(lens, default=0), f"cap {cap} alibi {alibi} first {first is not None}")
     return out
 
 
@@ -87,8 +87,20 @@ def test_block_sizes(block_size):
 @pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 64), (torch.float32, 64), (torch.float32, 128)])
 @pytest.mark.parametrize("group,hkv", [(1, 3), (2, 8), (4, 1), (8, 2)])
 @pytest.mark.parametrize("splits", [0, 4])
-def test_other_types_and_head_dims(dtype, d, group, hkv, splits):
-    _compare(90 + group, LENS, FIRST, 30.0, True, splits=splits, hq=group * hkv, hkv=hkv, d=d, dtype=dtype, block_size=24)
+@pytest.mark.parametrize("block_size", [24, 16])
+def test_other_types_and_head_dims(dtype, d, group, hkv, splits, block_size):
+    _compare(90 + group, LENS, FIRST, 30.0, True, splits=splits, hq=group * hkv, hkv=hkv, d=d, dtype=dtype,
+             block_size=block_size)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.bfloat16), (64, torch.float32)])
+def test_many_short_sequences(d, dtype):
+    # more sequences than threads of a block, most of them a token or two (or none) long
+    rng = np.random.default_rng(2)
+    lens = rng.integers(0, 4, size=500).tolist()
+    lens[77], lens[400] = 900, 333
+    first = [int(x) for x in rng.integers(-1, 3, size=500)]
+    _compare(22, lens, first, 30.0, True, d=d, dtype=dtype)
 
 
 def test_no_modifier_is_the_plain_call():
