@@ -451,7 +451,7 @@ __device__ __forceinline__ void merge_parts(const Params& p, const Segment& seg,
 // out by shuffles, so a part of a row costs one fma per column instead of a
 // rescaling of its own.  A chunk has up to eight times decode's rows: with the
 // loop above, 4 tokens after 8192 keys of E4M3 took 38.8 us, with this one 25.1;
-// one token 18.0 and 14.6.  A row that no part saw a key of becomes zeros.
+// one token 18.0 and 14.6.  A chunk's row that no part saw a key of becomes zeros.
 template <typename T, int D, bool kVar>
 __device__ __forceinline__ void merge_weighted(const Params& p, const Segment& seg, int rows_per_seq, int first,
                                                int step, int count, bool final, int nthreads_c) {
@@ -495,7 +495,8 @@ __device__ __forceinline__ void merge_weighted(const Params& p, const Segment& s
 #pragma unroll
       for (int off = 1; off < kJ; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
       top = fmaxf(top, m);
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+      // (l = 0: saw no key; a part whose scores were NaN has l NaN and must show)
+      const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - top);
       const float a = m == -INFINITY ? 0.f : exp2f(m - top);
       float sum = w * ml.y;
 #pragma unroll
@@ -521,7 +522,7 @@ __device__ __forceinline__ void merge_weighted(const Params& p, const Segment& s
       const float lr = __shfl_sync(0xffffffffu, l, r * kJ), mr = __shfl_sync(0xffffffffu, m, r * kJ);
       if (row0 + r >= rows) continue;
       if (final) {
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        const float inv = kVar && lr == 0.f ? 0.f : 1.f / lr;
 #pragma unroll
         for (int e = 0; e < PER; ++e) out[static_cast<size_t>(row0 + r) * D + e] = static_cast<T>(acc[r][e] * inv);
       } else {

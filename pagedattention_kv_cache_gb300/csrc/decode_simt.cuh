@@ -195,7 +195,12 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
         const float mnew = fmaxf(m[h], mt);
         if (mnew == -INFINITY) {
 #pragma unroll
-          for (int r = 0; r < S::ROUNDS; ++r) sc[r][h] = 0.f;
+          for (int r = 0; r < S::ROUNDS; ++r) {
+            if constexpr (kMod) {
+              if (sc[r][h] != sc[r][h]) l[h] = sc[r][h];  // NaN scores only: the row is NaN
+            }
+            sc[r][h] = 0.f;
+          }
           continue;
         }
         if (mnew != m[h]) {

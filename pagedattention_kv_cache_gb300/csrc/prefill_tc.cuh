@@ -308,6 +308,13 @@ __device__ __forceinline__ uint32_t exp2_of_pair_bf16(uint64_t x, uint64_t& acc)
   return out;
 }
 
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Maximum of three floats in one instruction.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -1005,7 +1012,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
 #pragma unroll
       for (int e = 0; e < 64; ++e) {
         // (a cap tells a key not seen, -infinity, from a score that overflowed)
-        if constexpr (kCap && !kBias) r[e] = __float_as_uint(fmaxf(__uint_as_float(r[e]), -FLT_MAX));
+        if constexpr (kCap && !kBias) r[e] = __float_as_uint(max_nan(__uint_as_float(r[e]), -FLT_MAX));
         if (off + e > span) r[e] = __float_as_uint(-INFINITY);
       }
     };
@@ -1245,6 +1252,10 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
           // order, so the result does not depend on the order they finished in
           float mq[kMaxParts], lq[kMaxParts];
           float mm = -INFINITY;
+          // a part that saw no key of the row has l = 0; one with a NaN among its
+          // scores must count, or the row would come out as if it had none
+          auto counts = [](float l) { return kForm == kPlain ? l > 0.f : l != 0.f; };
+          constexpr float kNone = kForm == kPlain ? 0.f : -1.f;
 #pragma unroll
           for (int q = 0; q < kMaxParts; ++q) {
             mq[q] = -INFINITY;
@@ -1252,14 +1263,15 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
             if (q < parts) {
               mq[q] = q == part ? m_run : __ldcg(record(q) + kBM * kD + row);
               lq[q] = q == part ? l_run : __ldcg(record(q) + kBM * kD + kBM + row);
-              if (lq[q] > 0.f) mm = fmaxf(mm, mq[q]);
+              if (counts(lq[q])) mm = fmaxf(mm, mq[q]);
             }
           }
           float total = 0.f;
 #pragma unroll
           for (int q = 0; q < kMaxParts; ++q) {
-            mq[q] = lq[q] > 0.f ? exp2f(mq[q] - mm) : 0.f;  // now the part's weight
-            total += mq[q] * lq[q];
+            // now the part's weight, kNone where it saw no key
+            mq[q] = counts(lq[q]) ? exp2f(mq[q] - mm) : kNone;
+            if (mq[q] != kNone) total += mq[q] * lq[q];
           }
           const float inv = total > 0.f ? (kFp8 ? p.v_scale : 1.f) / total : 0.f;
 #pragma unroll
@@ -1285,7 +1297,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
 #pragma unroll
                   for (int u = 0; u < 2; ++u) {
                     const int q = q0 + u;
-                    if (q >= parts || mq[q] == 0.f) continue;  // saw no key of this row: weight 0
+                    if (q >= parts || mq[q] == kNone) continue;
                     float v8[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
                     if (q == part) {
 #pragma unroll

@@ -178,6 +178,52 @@ def test_bad_lengths_and_pages_raise_bits():
     check(out[2:], ref[2:], dev[2:], torch.bfloat16, 20)
 
 
+def test_captured_without_a_workspace():
+    q, kc, vc, _, table, lens = [cuda(x) for x in _case(14, lens=[3000, 650, 33, 0], block_size=16, hq=8, hkv=2)]
+    call = lambda: pkv.paged_decode_attn_mod(q, kc, vc, table, lens, 0.1, softcap=20.0)  # noqa: E731
+    ref = call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and pkv.device_error() == 0
+
+
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.bfloat16), (64, torch.float32)])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_nan_reaches_only_the_rows_that_see_it(d, dtype, splits):
+    lens = [1500, 40, 1500, 1]
+    q, kc, vc, tables, table, ln = _case(15, lens=lens, block_size=16, hq=4, hkv=2, d=d, dtype=dtype)
+    first = i32([0, 0, 700, 0])
+    ref, dev = omod.decode_attention(as_np(q), as_np(kc), as_np(vc), table.numpy(), lens, 0.1, 20.0, None, first)
+    q[0, 3, 5] = float("nan")  # a head of the first sequence
+    kc[tables[2][0], 3, 1, 0] = float("nan")  # a key before the third sequence's first
+    kc[tables[2][80], 3, 0, 0] = float("nan")  # one after it, of KV head 0
+    kc[tables[3][0], 0, 1, 0] = float("nan")  # the only key of the last, of KV head 1
+    out = _run(q, kc, vc, table, ln, 0.1, splits, softcap=20.0, first_keys=first)
+    want = torch.zeros(4, 4, dtype=torch.bool)
+    want[0, 3], want[2, :2], want[3, 2:] = True, True, True
+    bad = torch.isnan(out).all(-1)
+    assert torch.equal(bad.cpu(), want)
+    check(out[~bad], ref[~want.numpy()], dev[~want.numpy()], _weights(dtype), 1500)
+
+
+def test_empty_batch():
+    q = torch.zeros(0, 8, 128, dtype=torch.bfloat16, device="cuda")
+    kc = torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros(0, 1, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    assert pkv.paged_decode_attn_mod(q, kc, kc, table, lens, 0.1, softcap=5.0).shape == q.shape
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    codes = torch.zeros(4, 16, 2, 128, dtype=torch.uint8, device="cuda")
+    assert pkv.paged_varlen_prefill_attn_mod(q, cu, cu, 0, 0, 0.1, k_cache=kc, v_cache=kc, block_tables=table).shape == q.shape
+    assert pkv.paged_varlen_prefill_attn_fp8(q, codes, codes, table, cu, cu, 0, 0, 0.1, 1.0, 1.0).shape == q.shape
+    assert pkv.device_error() == 0
+
+
 def test_binding_refusals():
     q, kc, vc, _, table, lens = [cuda(x) for x in _case(12, lens=[20, 20], block_size=16, hq=4, hkv=2)]
     call = pkv.paged_decode_attn_mod

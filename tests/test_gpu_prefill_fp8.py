@@ -117,6 +117,54 @@ def test_short_chunks_on_the_decode_kernel(block_size, group, hkv, new):
     assert torch.equal(a, c.compare(workspace=ws)) and int(ws[:65536].count_nonzero()) == 0
 
 
+def test_short_chunks_of_more_sequences_than_threads():
+    rng = np.random.default_rng(4)
+    cached, new = rng.integers(0, 40, size=400).tolist(), rng.integers(0, 5, size=400).tolist()
+    cached[7], cached[390] = 3000, 1500
+    Case(70, cached, new, hq=4, hkv=2).compare()
+
+
+def test_more_than_eight_kv_heads():
+    Case(71, [100, 0, 700], [40, 130, 2], hq=12, hkv=12).compare()
+    Case(72, [2000, 3], [2, 1], hq=48, hkv=12).compare()
+
+
+def test_nan_reaches_only_the_rows_that_see_it():
+    for new in (70, 4):  # the prefill kernel, and the decode kernel
+        c = Case(73, [1500], [new], hq=2, hkv=1)
+        ref, dev = c.reference()
+        pos = 1500 + new - 3  # a NaN key that the last three rows see
+        c.kc[c.tables[0][pos // 16], pos % 16, 0, 5] = 0x7F
+        c.q[1, 0, 9] = float("nan")
+        out = c.call()
+        torch.cuda.synchronize()
+        bad = torch.isnan(out).all(-1)
+        want = torch.zeros(new, 2, dtype=torch.bool)
+        want[new - 3:], want[1, 0] = True, True
+        assert torch.equal(bad.cpu(), want)
+        keep = ~want.numpy()
+        check(out[~bad], ref[keep], dev[keep], torch.float16, 1600)
+
+
+def test_captured_without_a_workspace():
+    # the call's own workspace comes from the graph's pool, and its counters are zeroed in the graph
+    for new in (60, 3):
+        c = Case(74, [3000, 40], [new, 2], block_size=64, hq=4, hkv=2)
+        q, kc, vc, table, cu_q, cu_k = [x.cuda() for x in (c.q, c.kc, c.vc, c.table, c.cu_q, c.cu_k)]
+        call = lambda: pkv.paged_varlen_prefill_attn_fp8(q, kc, vc, table, cu_q, cu_k, new, 3000 + new, c.scale,  # noqa: E731
+                                                         K_SCALE, V_SCALE)
+        ref = call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call()
+        for _ in range(3):
+            out.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, ref) and pkv.device_error() == 0
+
+
 def test_short_chunk_through_the_c_abi_without_its_workspace():
     # with no workspace, or one that is too small, the prefill kernel runs it
     c = Case(68, [1300, 17], [4, 2], hq=4, hkv=2)

@@ -149,6 +149,40 @@ def test_short_chunks_on_the_decode_kernel(block_size, group, hkv, new, mods):
     assert int(ws[:65536].count_nonzero()) == 0
 
 
+def test_short_chunks_of_more_sequences_than_threads():
+    rng = np.random.default_rng(4)
+    cached, new = rng.integers(0, 40, size=400).tolist(), rng.integers(0, 5, size=400).tolist()
+    cached[7], cached[390] = 3000, 1500
+    c = Case(43, cached, new, hq=4, hkv=2)
+    c.compare(cap=20.0, alibi=True, first=c.positions() - 9, prefix=rng.integers(0, 50, size=400).tolist())
+
+
+def test_more_than_eight_kv_heads():
+    Case(44, [100, 0, 700], [40, 130, 2], hq=12, hkv=12).compare(cap=20.0, alibi=True)
+    c = Case(45, [2000, 3], [2, 1], hq=48, hkv=12)
+    c.compare(first=c.positions() - 700)
+
+
+@pytest.mark.parametrize("mods", ["masked", "cap", "alibi", "both"])
+@pytest.mark.parametrize("new", [70, 4])
+def test_nan_reaches_only_the_rows_that_see_it(mods, new):
+    c = Case(46, [1500], [new], hq=2, hkv=1)
+    slopes = slopes_of(2) if mods in ("alibi", "both") else None
+    cap = 20.0 if mods in ("cap", "both") else 0.0
+    ref, dev = c.reference(True, cap, slopes, None, None)
+    pos = 1500 + new - 3  # a NaN key that the last three rows see
+    c.kc[c.tables[0][pos // 16], pos % 16, 0, 5] = float("nan")
+    c.q[1, 0, 9] = float("nan")
+    out = c.call(True, cap, slopes)
+    torch.cuda.synchronize()
+    bad = torch.isnan(out).all(-1)
+    want = torch.zeros(new, 2, dtype=torch.bool)
+    want[new - 3:], want[1, 0] = True, True
+    assert torch.equal(bad.cpu(), want)
+    keep = ~want.numpy()
+    check(out[~bad], ref[keep], dev[keep], torch.bfloat16, 1600)
+
+
 def test_short_chunk_of_sequences_without_a_key():
     c = Case(99, [2000, 30, 0], [2, 3, 1], hq=4, hkv=2)
     first = np.array([1 << 30, 1 << 30, 0, 5, 1 << 30, 1 << 30])
