@@ -133,8 +133,8 @@ enum Bar {
   O_FINAL = P_FULL + 2,  // per query tile
   V_TAIL = O_FINAL + 2,
   V_HEAD,  // kMod: the first V tile, once its rows before the first visible key are zeroed
-  Q_READY,  // kFp8: Q rewritten as scaled f16
-  RAW_FULL,  // kFp8, per K stage, then per V stage: the codes have arrived
+  Q_READY,  // kFp8, per query tile: Q rewritten as scaled f16
+  RAW_FULL = Q_READY + 2,  // kFp8, per K stage, then per V stage: the codes have arrived
   NUM_BARS = RAW_FULL + 2 * kStages
 };
 static_assert(NUM_BARS * 8 + 16 <= 256, "barrier area too small");
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     mbar_init(&bars[V_TAIL], 1);
     if constexpr (kMod) mbar_init(&bars[V_HEAD], 1);
     if constexpr (kFp8) {
-      mbar_init(&bars[Q_READY], 2 * kSoftmaxWarps);
+      for (int x = 0; x < 2; ++x) mbar_init(&bars[Q_READY + x], kSoftmaxWarps);
       for (int s = 0; s < 2 * kStages; ++s) mbar_init(&bars[RAW_FULL + s], 1);
     }
     fence_mbar_init();
@@ -817,12 +817,18 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
           tc::mma_ts_k128(tmem + kColO + x * kD, tmem + kColS + x * kBN, v_desc + ((st * kTileKV) >> 4), idesc_pv,
                           j > 0 ? 1u : 0u);
       };
-      wait(&bars[kFp8 ? Q_READY : Q_FULL], 0);
+      wait(&bars[Q_FULL], 0);
       if (n_tiles > 0) {
         wait.ready(&bars[K_FULL], 0);
         tc::fence_after_sync();
         for (int x = 0; x < 2; ++x)
-          if (n_x[x] > 0) issue_qk(x, 0);
+          if (n_x[x] > 0) {
+            if constexpr (kFp8) {
+              wait(&bars[Q_READY + x], 0);
+              tc::fence_after_sync();
+            }
+            issue_qk(x, 0);
+          }
         if (leader) tc::commit(&bars[K_EMPTY]);
       }
       for (int x = 0; x < 2; ++x)
@@ -964,23 +970,25 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       // largest element in [2^14, 2^15): exact but for elements 2^28 times
       // smaller than that.  The power comes off with the softmax scale.
       if (n_x > 0) {
-        wait(&bars[Q_FULL], 0);
+        // tile A first: its products can start while B's rows are rewritten
+        wait(&bars[x == 1 && n_a > 0 ? Q_READY : Q_FULL], 0);
+        if (x == 1) wait(&bars[Q_FULL], 0);
         constexpr int kChunksHalf = D / 16;  // this half's 16-byte chunks of the row
         unsigned char* q_row = sq + x * kTileQ + (D == 128 ? half * kSlabQ : 0) + row * 128;
         auto q_chunk = [&](int i) {
           const int ch = D == 128 ? i : half * kChunksHalf + i;
           return reinterpret_cast<uint4*>(q_row + ((ch ^ (row & 7)) << 4));
         };
-        float top = 0.f;
+        uint32_t top2 = 0u;  // a bf16 pair: the largest magnitudes of even and odd columns
         uint4 qc[kChunksHalf];
 #pragma unroll
         for (int i = 0; i < kChunksHalf; ++i) {
           qc[i] = *q_chunk(i);
-          float f[8];
-          Chunk<__nv_bfloat16>::unpack(qc[i], f);
+          const uint32_t w[4] = {qc[i].x, qc[i].y, qc[i].z, qc[i].w};
 #pragma unroll
-          for (int u = 0; u < 8; ++u) top = fmaxf(top, fabsf(f[u]));
+          for (int u = 0; u < 4; ++u) asm("max.bf16x2 %0, %0, %1;" : "+r"(top2) : "r"(w[u] & 0x7fff7fffu));
         }
+        float top = fmaxf(__uint_as_float(top2 << 16), __uint_as_float(top2 & 0xffff0000u));
         *red_at(0, half) = top;
         named_barrier_sync(pair_id, 64);
         top = fmaxf(*red_at(0, 0), *red_at(0, 1));
@@ -999,7 +1007,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[Q_READY]);
+      if (lane == 0) mbar_arrive(&bars[Q_READY + x]);
     }
 
     // kMod: keys the row does not see get -infinity; lo <= key <= hi in one unsigned comparison
