@@ -26,6 +26,9 @@
 // paged_decode_mma_kernel (mma.sync tensor cores, 16-token tensor copies)
 // runs every bf16 or FP8 cache with head_dim 128; paged_decode_kernel (CUDA
 // cores, 1-D bulk copies of token spans) runs fp32 caches and head_dim 64.
+// Two template switches give both kernels further uses: kMod, score modifiers
+// (decode_mod.cu; bf16 with head_dim 64 then runs on the tensor cores too), and,
+// for the first, kVar, short chunks of new tokens (chunk_decode.cu).
 //
 // Verify (speculative-decoding target pass, QL > 1): query token i of
 // sequence b sits at position context_lens[b] - QL + i and attends keys up to
@@ -35,7 +38,8 @@
 // Files: decode_plan.cuh (parameters, split plan, merge), decode_simt.cuh
 // and decode_mma.cuh (the two kernels), this file (host side: launch shapes,
 // the split workspace layout and the dispatch over group sizes).  The entry
-// points that include it are decode.cu, verify.cu and fp8.cu.
+// points that include it are decode.cu, decode_mod.cu, verify.cu, fp8.cu and
+// chunk_decode.cu.
 #pragma once
 
 #include <algorithm>

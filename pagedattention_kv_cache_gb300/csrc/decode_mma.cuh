@@ -1,6 +1,6 @@
 // paged_decode_mma_kernel: the tensor-core decode / verify kernel (bf16 and
-// FP8 caches, head_dim 128).  The CTA plan, split and merge it uses are in
-// decode_plan.cuh.
+// FP8 caches, head_dim 128; bf16 with score modifiers also head_dim 64) and, with
+// kVar, short chunks.  The CTA plan, split and merge it uses are in decode_plan.cuh.
 #pragma once
 
 #include "decode_plan.cuh"
