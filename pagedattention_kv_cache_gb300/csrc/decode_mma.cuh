@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(288, 1)
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int ex = amax > 0.f ? min(max(14 - ilogbf(amax), -100), 100) : 0;
+        // (bf16's whole range, and 2^ex and 2^-ex normal floats)
+        const int ex = amax > 0.f ? min(max(14 - ilogbf(amax), -113), 126) : 0;
         const float up = ldexpf(1.f, ex);
         qmul[hh] = p.scale_log2 * ldexpf(1.f, -ex);
 #pragma unroll

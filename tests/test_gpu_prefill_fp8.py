@@ -92,6 +92,21 @@ def test_q_magnitudes(q_scale):
     c.compare(label=f"q x {q_scale}")
 
 
+# the decode kernel's rows: a short chunk, and one decoded token per sequence
+@pytest.mark.parametrize("q_scale", [1e-37, 1e9, 1e36])
+def test_q_magnitudes_on_the_decode_kernel(q_scale):
+    c = Case(75, [1500, 700, 40], [2, 1, 1], q_scale=q_scale)
+    c.scale = c.d ** -0.5 * min(1.0, 3.0 / q_scale)  # scores of a few units
+    assert pkv.chunk_workspace_bytes(3, c.hq, c.hkv, c.d, 2, 1502) > 0
+    c.compare(label=f"chunk, q x {q_scale}")
+    ref, dev = c.reference()
+    out = pkv.paged_decode_attn_fp8(c.q[1:].cuda(), c.kc.cuda(), c.vc.cuda(), c.table.cuda(), i32(c.totals).cuda(), c.scale,
+                                    K_SCALE, V_SCALE)
+    torch.cuda.synchronize()
+    assert pkv.device_error() == 0
+    check(out, ref[1:], dev[1:], torch.float16, 1502, f"decode, q x {q_scale}")
+
+
 def test_codes_of_every_value():
     # every finite E4M3 code (subnormals among them) as K and as V
     codes = torch.tensor([x for x in range(256) if x & 0x7F != 0x7F], dtype=torch.uint8)
