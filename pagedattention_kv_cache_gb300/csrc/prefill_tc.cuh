@@ -101,6 +101,11 @@ struct Geo {
 };
 static_assert(Geo<128>::kSmemBytes <= 227 * 1024, "shared memory plan exceeds an SM");
 constexpr float kRescaleLog2 = 8.0f;
+// kFp8: weights enter P V as f16, whose subnormals end at 2^-24, so they are taken 2^7 times
+// as large (with the lazy rescale at most 2^15): a weight then counts down to 2^-32 of the
+// row's largest.  Without the factor 131072 keys 17.4 below a dominant one, 0.36 % of the
+// mass, came out as nothing.
+constexpr float kF16WeightLog2 = 7.0f;
 
 // Key-range split of long work items, used only when the pairs do not fill
 // the GPU (small batches with long histories) and a workspace is given.  With
@@ -266,7 +271,7 @@ __device__ __forceinline__ uint32_t exp2_pair_bf16(uint32_t s0, uint32_t s1, flo
   return out;
 }
 
-// The same with f16 weights (kFp8): at most 2^8 (the lazy rescale), far inside f16's range.
+// The same with f16 weights (kFp8), which reach 2^15 (kF16WeightLog2 and the lazy rescale).
 __device__ __forceinline__ uint32_t exp2_pair_f16(uint32_t s0, uint32_t s1, float scale, float neg_m, uint64_t& acc) {
   uint32_t out;
   asm("{\n\t.reg .b64 x, c, m;\n\t.reg .f32 a, b, sa, sb;\n\t.reg .b16 pa, pb, one;\n\t"
@@ -1062,6 +1067,11 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       named_barrier_sync(pair_id, 64);
       const float mt = fmaxf(*red_at(j & 1, 0), *red_at(j & 1, 1));
       float m_tile = mt * mul;
+      if constexpr (kFp8) {
+        // the reference of the weights, below the maximum: the factor cancels against the row sum and in the merge of
+        // parts, which see the same reference (past 2^20 the difference would not be exact enough to bound them)
+        if (fabsf(m_tile) < 0x1p20f) m_tile -= kF16WeightLog2;
+      }
       if constexpr (kCap && !kBias) {
         m_tile = mt == -INFINITY ? mt : p.mod.cap_log2 * tanh_by_exp(mt * p.mod.raw_to_x);
       }

@@ -13,7 +13,7 @@ from oracle import fp8 as of8
 from oracle import modified as omod
 
 from _harness import as_np
-from _modified import check, i32
+from _modified import SCORE, check, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -212,6 +212,31 @@ def test_split_key_ranges():
     for _ in range(3):
         assert torch.equal(a, c.compare(workspace=ws))
     assert int(ws[:65536].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,workspace", [(9, False), (9, None), (4, None)])
+def test_one_dominant_key_before_a_long_flat_tail(d, new, workspace):
+    # key 0 scores 17.4, every other key 0: a tail key's weight is 2^-25.1 of the largest, 131072 of them
+    # 0.36 % of the mass, and only they have a value.  A weight enters P V as f16 in units in which the row's
+    # largest is 2^7 or more, so it is off by 2^-11 of itself or, as a subnormal, by 2^-25 of those units: 2^-32
+    # of the largest weight
+    tail = 131072
+    c = Case(76, [tail], [new], block_size=256, hq=2, hkv=2, d=d)
+    codes = torch.zeros_like(c.kc)
+    codes[c.tables[0][0], 0, :, 3] = 0x7E  # 448 K_SCALE = 7
+    c.kc, c.vc = codes, torch.full_like(c.vc, 0x7E)  # 448 V_SCALE = 5.25
+    c.vc[c.tables[0][0], 0] = 0
+    c.q.zero_()
+    c.q[..., 3] = 1.0
+    c.scale = 17.4 / 7
+    ref, dev = c.reference()
+    out = c.call(workspace=workspace)
+    torch.cuda.synchronize()
+    assert pkv.device_error() == 0
+    keys = tail + new
+    allowed = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 * 1.01 + SCORE) * dev + keys * 2.0 ** -32 * 5.25 + keys * 2.0 ** -24 * ref
+    assert 0.018 < ref.min() and (np.abs(out.double().cpu().numpy() - ref) <= allowed).all()
 
 
 def test_pool_past_32_bit_offsets():
