@@ -1272,8 +1272,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
           float mm = -INFINITY;
           // a part that saw no key of the row has l = 0; one with a NaN among its
           // scores must count, or the row would come out as if it had none
-          auto counts = [](float l) { return kForm == kPlain ? l > 0.f : l != 0.f; };
-          constexpr float kNone = kForm == kPlain ? 0.f : -1.f;
+          constexpr float kNone = -1.f;
 #pragma unroll
           for (int q = 0; q < kMaxParts; ++q) {
             mq[q] = -INFINITY;
@@ -1281,14 +1280,14 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
             if (q < parts) {
               mq[q] = q == part ? m_run : __ldcg(record(q) + kBM * kD + row);
               lq[q] = q == part ? l_run : __ldcg(record(q) + kBM * kD + kBM + row);
-              if (counts(lq[q])) mm = fmaxf(mm, mq[q]);
+              if (lq[q] != 0.f) mm = fmaxf(mm, mq[q]);
             }
           }
           float total = 0.f;
 #pragma unroll
           for (int q = 0; q < kMaxParts; ++q) {
             // now the part's weight, kNone where it saw no key
-            mq[q] = counts(lq[q]) ? exp2f(mq[q] - mm) : kNone;
+            mq[q] = lq[q] != 0.f ? exp2f(mq[q] - mm) : kNone;
             if (mq[q] != kNone) total += mq[q] * lq[q];
           }
           const float inv = total > 0.f ? (kFp8 ? p.v_scale : 1.f) / total : 0.f;

@@ -174,6 +174,36 @@ def test_long_items_split_head_dim_64():
     assert d <= 1.6e-2, d
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("workspace", [None, False])
+def test_nan_shows_whether_the_key_range_is_split_or_not(d, workspace):
+    # a part of a split row whose scores hold a NaN must not pass for one that saw no key
+    gen = torch.Generator().manual_seed(5)
+    hq, hkv, bs, cached, nq = 4, 2, 64, 6000, 70
+    blocks = -(-(cached + nq) // bs)
+    kc, vc = [torch.randn(blocks, bs, hkv, d, generator=gen).bfloat16() for _ in range(2)]
+    q = torch.randn(nq, hq, d, generator=gen).bfloat16()
+    assert pkv.prefill_workspace_bytes(1, hq, hkv, d, nq) > 0
+    cu_q, cu_k = [torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (nq, cached + nq)]
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda")[None]
+    for parts in ("row", "first", "last"):
+        k2, q2 = kc.clone(), q.clone()
+        want = torch.zeros(nq, hq, dtype=torch.bool)
+        if parts == "row":  # a query row: every score of it
+            q2[7, 1, 9] = float("nan")
+            want[7, 1] = True
+        else:  # a key of KV head 1, seen by every row, or by the last three
+            pos = 20 if parts == "first" else cached + nq - 3
+            k2[pos // bs, pos % bs, 1, 5] = float("nan")
+            want[0 if parts == "first" else nq - 3:, 2:] = True
+        out = pkv.paged_varlen_prefill_attn(q2.cuda(), cu_q, cu_k, nq, cached + nq, d ** -0.5, k_cache=k2.cuda(),
+                                            v_cache=vc.cuda(), block_tables=table, workspace=workspace)
+        torch.cuda.synchronize()
+        assert pkv.device_error() == 0
+        assert torch.equal(torch.isnan(out).all(-1).cpu(), want), parts
+        assert torch.equal(torch.isnan(out).any(-1).cpu(), want), parts
+
+
 def test_split_workspace_shared_by_calls_of_growing_size():
     # one workspace: a one-sequence split (few tickets, large records), then three sequences (more
     # tickets), then one again; the tickets stay in the fixed counter area, clear of every call's
