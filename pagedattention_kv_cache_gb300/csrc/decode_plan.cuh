@@ -416,9 +416,10 @@ __device__ __forceinline__ void merge_parts(const Params& p, const Segment& seg,
           const float mn = fmaxf(mm[r], ml[jj][r].x);
           // absent parts and rows, and parts that saw no key of this row (a
           // verify row whose part holds only keys past its position), carry
-          // m = -inf: they add nothing, and a row none of whose parts saw a
-          // key keeps m = -inf, l = 0 and a zero row
-          if (mn == -INFINITY) continue;
+          // m = -inf and l = 0: they add nothing, and a row none of whose parts saw
+          // a key keeps m = -inf, l = 0 and a zero row.  A part all of whose
+          // scores were NaN has m = -inf and l NaN, and makes the row NaN
+          if (mn == -INFINITY && ml[jj][r].y == 0.f) continue;
           const float a = exp2f(mm[r] - mn);
           const float w = exp2f(ml[jj][r].x - mn);
           ll[r] = fmaf(ll[r], a, ml[jj][r].y * w);

@@ -193,16 +193,6 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
 #pragma unroll
         for (int off = S::LPT; off < 32; off <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
         const float mnew = fmaxf(m[h], mt);
-        if (mnew == -INFINITY) {
-#pragma unroll
-          for (int r = 0; r < S::ROUNDS; ++r) {
-            if constexpr (kMod) {
-              if (sc[r][h] != sc[r][h]) l[h] = sc[r][h];  // NaN scores only: the row is NaN
-            }
-            sc[r][h] = 0.f;
-          }
-          continue;
-        }
         if (mnew != m[h]) {
           const float corr = exp2f(m[h] - mnew);
           l[h] *= corr;
@@ -210,9 +200,11 @@ __global__ void __launch_bounds__(288, 1) paged_decode_kernel(const Params p) {
           for (int e = 0; e < S::EPL; ++e) acc[h][e] *= corr;
           m[h] = mnew;
         }
+        // no key so far, or NaN scores only: weights 0, or NaN, which makes the row NaN
+        const float mref = mnew == -INFINITY ? 0.f : mnew;
 #pragma unroll
         for (int r = 0; r < S::ROUNDS; ++r) {
-          const float pr = exp2f(sc[r][h] - mnew);
+          const float pr = exp2f(sc[r][h] - mref);
           l[h] += pr;
           sc[r][h] = pr;
         }

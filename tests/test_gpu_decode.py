@@ -210,3 +210,39 @@ def test_workspace_shared_by_calls_of_growing_batch():
         torch.cuda.synchronize()
         assert pkv.device_error() == 0
         assert torch.equal(shared, fresh), w.batch
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16 d64", "f32", "f32 d64", "verify", "fp8"])
+@pytest.mark.parametrize("splits", [0, 1, 5])
+def test_nan_keys_show_wherever_they_lie(kind, splits):
+    # a stretch of NaN keys of KV head 1, at either end or in the middle, long enough to fill whole parts of a
+    # split (or a warp's whole stage): its heads are NaN, the others untouched
+    hq, hkv, bs, n = 4, 2, 16, 1500
+    d = 64 if kind.endswith("d64") else 128
+    dtype = torch.float32 if kind.startswith("f32") else torch.bfloat16
+    gen = torch.Generator().manual_seed(6)
+    blocks = -(-n // bs)
+    ql = 2 if kind == "verify" else 1
+    q = torch.randn(1, ql, hq, d, generator=gen).to(dtype).cuda()
+    kc, vc = [torch.randn(blocks, bs, hkv, d, generator=gen).to(dtype) for _ in range(2)]
+    if kind == "fp8":
+        kc, vc = [(x.float() * 64).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) for x in (kc, vc)]
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+
+    def run(keys):
+        if kind == "fp8":
+            return pkv.paged_decode_attn_fp8(q[:, 0], keys.cuda(), vc.cuda(), table, lens, 0.1, 1 / 64, 1 / 64, num_splits=splits)
+        if kind == "verify":
+            return pkv.paged_verify_attn(q, keys.cuda(), vc.cuda(), table, lens, 0.1, num_splits=splits)[0]
+        return pkv.paged_decode_attn(q[:, 0], keys.cuda(), vc.cuda(), table, lens, 0.1, num_splits=splits)
+
+    plain = run(kc)
+    for lo, hi in ((0, 1), (0, 32), (0, 256), (0, 300), (0, 304), (32, 64), (500, 900), (1000, n), (0, n)):
+        keys = kc.clone()
+        keys.view(-1, hkv, d)[lo:hi, 1] = 0x7F if kind == "fp8" else float("nan")
+        out = run(keys)
+        torch.cuda.synchronize()
+        assert pkv.device_error() == 0
+        assert torch.isnan(out[:, 2:]).all(), (lo, hi)
+        assert torch.equal(out[:, :2], plain[:, :2]), (lo, hi)
