@@ -419,11 +419,14 @@ __device__ __forceinline__ void bias_scores(uint32_t* r, float slope, int dist0,
   }
 }
 
-// kForm other than kPlain: a value the warp's lanes agree on, told to the compiler as
-// such (it can then live in a uniform register and leaves the 96 per thread alone).
-template <Form kForm>
+// A value the warp's lanes agree on, told to the compiler as such (it can then live in
+// a uniform register and leaves the 96 per thread alone).  The plain form takes it only
+// where it spills without (head_dim 128, G = 1: a batch of 16 chunks 39.1 us without, 37.7
+// with; the other groups and head_dim 64 run 0.2 to 1.5 % slower with it, the 16k history
+// at head_dim 64 4 %).
+template <int G, int D, Form kForm>
 __device__ __forceinline__ int warp_uniform(int v) {
-  if constexpr (kForm == kPlain) return v;
+  if constexpr (kForm == kPlain && !(G == 1 && D == 128)) return v;
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
@@ -450,10 +453,10 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   const int pairs = p.q_tiles / 2;
   const int pt = pairs - 1 - static_cast<int>(blockIdx.y) / p.parts_max;
   const int part = static_cast<int>(blockIdx.y) % p.parts_max;
-  const int q_begin = warp_uniform<kForm>(__ldg(p.cu_q + seq));
-  const int nq = warp_uniform<kForm>(__ldg(p.cu_q + seq + 1)) - q_begin;
-  const int k_begin = warp_uniform<kForm>(__ldg(p.cu_k + seq));
-  const int nk = warp_uniform<kForm>(__ldg(p.cu_k + seq + 1)) - k_begin;
+  const int q_begin = warp_uniform<G, D, kForm>(__ldg(p.cu_q + seq));
+  const int nq = warp_uniform<G, D, kForm>(__ldg(p.cu_q + seq + 1)) - q_begin;
+  const int k_begin = warp_uniform<G, D, kForm>(__ldg(p.cu_k + seq));
+  const int nk = warp_uniform<G, D, kForm>(__ldg(p.cu_k + seq + 1)) - k_begin;
   // cu_seqlens must describe rows inside q / out (and the packed k / v), and no
   // sequence may have more rows than max_seqlen_q, which sized the grid: such a
   // sequence is skipped whole and raises the range bit
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   int prefix_end = 0;
   int lo_pair = 0;
   if constexpr (kMod) {
-    if (p.mod.prefix_lens) prefix_end = warp_uniform<kForm>(min(max(__ldg(p.mod.prefix_lens + seq), 0), nk));
+    if (p.mod.prefix_lens) prefix_end = warp_uniform<G, D, kForm>(min(max(__ldg(p.mod.prefix_lens + seq), 0), nk));
     if (p.mod.first_keys) {
       int least = INT32_MAX;
       for (int t = tok0 + static_cast<int>(threadIdx.x % 32); t < min(nq, tok0 + 2 * TQ); t += 32)
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   volatile int* s_ticket = abort_flag + 1;  // split tiles' tickets, one per query tile
 
   const int tid = threadIdx.x;
-  const int warp = warp_uniform<kForm>(tid / 32);
+  const int warp = warp_uniform<G, D, kForm>(tid / 32);
   const int lane = tid % 32;
   const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
 
