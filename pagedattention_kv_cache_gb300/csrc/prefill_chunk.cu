@@ -127,7 +127,8 @@ extern "C" int pkv_paged_varlen_prefill_attn_mod(
   if (st != PKV_OK) return st;
   if (on_decode_kernel(a, max_seqlen_k)) return pkv::chunk_decode_launch(a, false, stream);
   if (a.mod.slopes)
-    return softcap > 0.f ? pkv::prefill_tc_capped_biased_launch(a, stream) : pkv::prefill_tc_biased_launch(a, stream);
+    return softcap > 0.f || !pkv::raw_bias_scale(scale) ? pkv::prefill_tc_capped_biased_launch(a, stream)
+                                                        : pkv::prefill_tc_biased_launch(a, stream);
   return softcap > 0.f ? pkv::prefill_tc_capped_launch(a, stream) : pkv::prefill_tc_masked_launch(a, stream);
 }
 

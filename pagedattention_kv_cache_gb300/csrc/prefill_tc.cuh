@@ -370,6 +370,7 @@ __device__ __forceinline__ uint64_t capped_pair(uint32_t s0, uint32_t s1, const 
 
 // Caps the raw scores of one row and 64 consecutive keys (r) in place, into the
 // exp2 domain.  The polynomials hold for the whole warp's scores or not at all.
+// No cap (a bias at a scale outside raw_bias_scale): the domain alone.
 __device__ __forceinline__ void cap_scores(const TcParams& p, uint32_t* r) {
   float mx[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -385,6 +386,9 @@ __device__ __forceinline__ void cap_scores(const TcParams& p, uint32_t* r) {
   } else if (!__any_sync(0xffffffffu, top > p.tanh_poly.wide_limit)) {
 #pragma unroll
     for (int e = 0; e < 64; e += 2) unpack2u(capped_pair(r[e], r[e + 1], p.tanh_poly.wide, 0ull), r[e], r[e + 1]);
+  } else if (p.mod.cap_log2 == 0.f) {  // (both limits are -infinity then)
+#pragma unroll
+    for (int e = 0; e < 64; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * p.scale_log2);
   } else if (p.mod.cap_log2 <= kAbsCapLog2) {
 #pragma unroll
     for (int e = 0; e < 64; ++e)

@@ -39,6 +39,12 @@ inline ScoreMod make_score_mod(float raw_scale, float softcap, const float* slop
 // 0 or in [1e-30, 1e30], where c log2e and scale / c stay inside fp32 (a NaN fails both).
 inline bool softcap_valid(float softcap) { return softcap == 0.f || (softcap >= 1e-30f && softcap <= 1e30f); }
 
+// Scales at which a distance bias may be held in raw score units, slope / scale
+// per key (one operation per score less than after scaling): far enough from
+// fp32's ends that slope / scale times a distance below 2^31 stays inside for
+// slopes below 2^33.  At 1e-37 a slope of 0.5 left it from 68 keys of distance on.
+inline bool raw_bias_scale(float scale) { return scale >= 0x1p-64f && scale <= 0x1p64f; }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -237,6 +237,18 @@ def test_caps_of_every_size(cap):
     c.compare(cap=cap, alibi=True)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_scale", [1e36, 1e-36])
+def test_distance_bias_at_scales_of_every_size(d, q_scale):
+    # q times a power of ten and the scale divided by it: the scores, and what the bias adds to them, stay.  Rows see
+    # keys some way ahead of them only, so every score they have is biased by 100 or more at the steepest slope
+    c = Case(48, [0, 100, 2], [300, 270, 9], d=d, q_scale=q_scale)
+    c.scale = d ** -0.5 * 3.0 / q_scale
+    c.compare(causal=False, alibi=True, label="every key")
+    c.compare(causal=False, alibi=True, first=c.positions() + 260, label="keys from 260 on")
+    c.compare(causal=False, alibi=True, cap=20.0, first=c.positions() + 260, label="capped")
+
+
 def test_scores_that_overflow_are_capped():
     # every product of a key has that key's sign and is beyond float32: the score is +-infinity, the capped score +-5
     c = Case(35, [100, 0], [140, 60], q_scale=1e30)
