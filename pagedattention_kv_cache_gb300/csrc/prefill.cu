@@ -263,9 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p) {
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        const float mr = m_run[e >> 1];
-        const float p0 = mr == -INFINITY ? 0.f : exp2f(s[j][e] - mr);
-        const float p1 = mr == -INFINITY ? 0.f : exp2f(s[j][e + 1] - mr);
+        // (m = -inf: no key so far, weights 0; or NaN scores only, weights NaN)
+        const float mr = m_run[e >> 1] == -INFINITY ? 0.f : m_run[e >> 1];
+        const float p0 = exp2f(s[j][e] - mr);
+        const float p1 = exp2f(s[j][e + 1] - mr);
         const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
         rs[e >> 1] += __low2float(pb) + __high2float(pb);
         pf[j / 2][(j & 1) * 2 + (e >> 1)] = *reinterpret_cast<const uint32_t*>(&pb);

@@ -204,6 +204,38 @@ def test_nan_shows_whether_the_key_range_is_split_or_not(d, workspace):
         assert torch.equal(torch.isnan(out).any(-1).cpu(), want), parts
 
 
+@pytest.mark.parametrize("block_size", [24, 64])
+def test_nan_of_a_whole_key_tile_or_row_shows(block_size):
+    # block sizes of the two prefill kernels: a query row that is NaN, or the first keys of a KV head, whole tiles of them
+    gen = torch.Generator().manual_seed(7)
+    hq, hkv, d, cached, nq = 4, 2, 128, 300, 70
+    blocks = -(-(cached + nq) // block_size)
+    kc, vc = [torch.randn(blocks, block_size, hkv, d, generator=gen).bfloat16() for _ in range(2)]
+    q = torch.randn(nq, hq, d, generator=gen).bfloat16()
+    cu_q, cu_k = [torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (nq, cached + nq)]
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda")[None]
+
+    def run(q, kc):
+        out = pkv.paged_varlen_prefill_attn(q.cuda(), cu_q, cu_k, nq, cached + nq, d ** -0.5, k_cache=kc.cuda(),
+                                            v_cache=vc.cuda(), block_tables=table, workspace=False)
+        torch.cuda.synchronize()
+        assert pkv.device_error() == 0
+        return out
+
+    plain = run(q, kc)
+    q2 = q.clone()
+    q2[7, 1, 9] = float("nan")
+    out = run(q2, kc)
+    assert torch.isnan(out[7, 1]).all()
+    out[7, 1] = plain[7, 1]
+    assert torch.equal(out, plain)
+    for keys in (64, 128, 256):
+        k2 = kc.clone()
+        k2.view(-1, hkv, d)[:keys, 1] = float("nan")
+        out = run(q, k2)
+        assert torch.isnan(out[:, 2:]).all() and torch.equal(out[:, :2], plain[:, :2]), keys
+
+
 def test_split_workspace_shared_by_calls_of_growing_size():
     # one workspace: a one-sequence split (few tickets, large records), then three sequences (more
     # tickets), then one again; the tickets stay in the fixed counter area, clear of every call's
