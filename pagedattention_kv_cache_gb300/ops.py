@@ -152,19 +152,12 @@ def paged_decode_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     nb, bs, hkv, d2 = k_cache.shape
     if d2 != d or v_cache.shape != k_cache.shape or block_tables.shape[0] != B or context_lens.shape[0] != B:
         raise ValueError("inconsistent shapes between q, caches, block_tables and context_lens")
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, "out", dtype=torch.bfloat16, device=dev, shape=q.shape)
-    if workspace is None:
-        workspace = decode_workspace(B, hq, d, num_splits, device=dev)
-    else:
-        _need(workspace, "workspace", device=dev)
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    handle = _stream(stream, dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _decode_workspace_args, workspace, B, hq, d, num_splits, dev)
     st = _lib.load().pkv_paged_decode_attn_fp8(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
         _ptr(context_lens), B, hq, hkv, d, bs, nb, ctypes.c_float(scale), ctypes.c_float(k_scale),
-        ctypes.c_float(v_scale), num_splits, ws_ptr, ws_bytes, _stream(stream, dev))
+        ctypes.c_float(v_scale), num_splits, ws_ptr, ws_bytes, handle)
     _lib.check("pkv_paged_decode_attn_fp8", st)
     return out
 
@@ -204,19 +197,12 @@ def paged_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     nb, bs, hkv, d2 = k_cache.shape
     if d2 != d or block_tables.shape[0] != B or context_lens.shape[0] != B:
         raise ValueError("inconsistent shapes between q, caches, block_tables and context_lens")
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
-    if workspace is None:
-        workspace = decode_workspace(B, hq, d, num_splits, device=dev)
-    else:
-        _need(workspace, "workspace", device=dev)
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    handle = _stream(stream, dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _decode_workspace_args, workspace, B, hq, d, num_splits, dev)
     st = _lib.load().pkv_paged_decode_attn(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
         _ptr(context_lens), B, hq, hkv, d, bs, nb, ctypes.c_float(scale), num_splits, ws_ptr, ws_bytes,
-        _dtype_code(q), _stream(stream, dev))
+        _dtype_code(q), handle)
     _lib.check("pkv_paged_decode_attn", st)
     return out
 
@@ -237,19 +223,12 @@ def paged_verify_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     nb, bs, hkv, d2 = k_cache.shape
     if d2 != d or block_tables.shape[0] != B or context_lens.shape[0] != B:
         raise ValueError("inconsistent shapes between q, caches, block_tables and context_lens")
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
-    if workspace is None:
-        workspace = decode_workspace(B, ql * hq, d, num_splits, device=dev)
-    else:
-        _need(workspace, "workspace", device=dev)
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    handle = _stream(stream, dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _decode_workspace_args, workspace, B, ql * hq, d, num_splits, dev)
     st = _lib.load().pkv_paged_verify_attn(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
         _ptr(context_lens), B, ql, hq, hkv, d, bs, nb, ctypes.c_float(scale), num_splits, ws_ptr, ws_bytes,
-        _dtype_code(q), _stream(stream, dev))
+        _dtype_code(q), handle)
     _lib.check("pkv_paged_verify_attn", st)
     return out
 
@@ -269,13 +248,12 @@ def paged_decode_attn_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     nb, bs, hkv, d2 = k_cache.shape
     if d2 != d or block_tables.shape[0] != B or context_lens.shape[0] != B:
         raise ValueError("inconsistent shapes between q, caches, block_tables and context_lens")
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
+    handle = _stream(stream, dev)
+    (out,) = _buffers(stream, q, out, tuple)
     st = _lib.load().pkv_paged_decode_attn_noalloc(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
         _ptr(context_lens), B, hq, hkv, d, bs, nb, ctypes.c_float(scale), num_splits, _dtype_code(q),
-        _stream(stream, dev))
+        handle)
     _lib.check("pkv_paged_decode_attn_noalloc", st)
     return out
 
@@ -319,8 +297,8 @@ def paged_varlen_prefill_attn(q: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_se
     """Packed varlen prefill attention; keys through block_tables (cache) or from packed k/v.
 
     workspace: None = a zero-filled workspace cached per device (calls that may
-    overlap on different streams must pass their own); False = never split long
-    query tiles; or a tensor from prefill_workspace().
+    overlap on different streams must pass their own), or with `stream` one for this
+    call; False = never split long query tiles; or a tensor from prefill_workspace().
     """
     dev = _device(q, "q")
     _need(q, "q", ndim=3)
@@ -353,23 +331,21 @@ def paged_varlen_prefill_attn(q: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_se
         total_k = k.shape[0]
         if v.shape != k.shape:
             raise ValueError("k and v shapes differ")
-    if out is None:
-        out = torch.empty_like(q)
-    _need(out, "out", dtype=q.dtype, device=dev, shape=q.shape)
-    ws_bytes = 0
+    handle = _stream(stream, dev)
     if workspace is None:
-        ws_bytes = prefill_workspace_bytes(B, hq, hkv, d, int(max_seqlen_q))
-        workspace = _cached_prefill_workspace(ws_bytes, dev) if ws_bytes > 0 else None
-    elif workspace is False:
-        workspace = None
+        nbytes = prefill_workspace_bytes(B, hq, hkv, d, int(max_seqlen_q))
+        if nbytes > 0 and stream is None:
+            workspace = _cached_prefill_workspace(nbytes, dev)
     else:
-        _need(workspace, "workspace", dtype=torch.uint8, device=dev)
-        ws_bytes = workspace.numel()
+        nbytes = 0
+        if workspace is not False:
+            _need(workspace, "workspace", dtype=torch.uint8, device=dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _workspace_args, workspace, nbytes, B, dev)
     st = _lib.load().pkv_paged_varlen_prefill_attn(
         _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q),
         _ptr(cu_seqlens_k), int(max_seqlen_q), int(max_seqlen_k), _ptr(block_tables), mb, B, total_q,
-        total_k, hq, hkv, d, bs, nb, ctypes.c_float(scale), 1 if causal else 0, _ptr(workspace), ws_bytes,
-        _dtype_code(q), _stream(stream, dev))
+        total_k, hq, hkv, d, bs, nb, ctypes.c_float(scale), 1 if causal else 0, ws_ptr, ws_bytes,
+        _dtype_code(q), handle)
     _lib.check("pkv_paged_varlen_prefill_attn", st)
     return out
 

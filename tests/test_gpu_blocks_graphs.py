@@ -133,3 +133,44 @@ def test_store_and_decode_captured_in_a_cuda_graph():
             ref = oa.paged_decode_attention(as_np(s_q[layer][:5]), k2, v2, meta["block_tables"][:5],
                                             meta["context_lens"][:5], d ** -0.5)
             assert_close(s_out[layer][:5], ref, torch.bfloat16, f"graph replay {replay} layer {layer}")
+
+
+def _split_calls():
+    """Calls that split over the context and allocate their output and workspace, on inputs of their own."""
+    gen = torch.Generator().manual_seed(8)
+    hq, hkv, d, bs, n, nq = 8, 2, 128, 16, 3000, 70
+    blocks = -(-n // bs)
+    kc, vc = [torch.randn(blocks, bs, hkv, d, generator=gen).bfloat16().cuda() for _ in range(2)]
+    k8, v8 = [(x.float() * 64).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) for x in (kc, vc)]
+    q = torch.randn(nq, hq, d, generator=gen).bfloat16().cuda()
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda")[None]
+    lens, cu_q, cu_k = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([n], [0, nq], [0, n])]
+    return {
+        "decode": lambda **kw: pkv.paged_decode_attn(q[:1], kc, vc, table, lens, 0.1, **kw),
+        "fp8": lambda **kw: pkv.paged_decode_attn_fp8(q[:1], k8, v8, table, lens, 0.1, 1 / 64, 1 / 64, **kw),
+        "verify": lambda **kw: pkv.paged_verify_attn(q[None, :2], kc, vc, table, lens, 0.1, **kw),
+        "prefill": lambda **kw: pkv.paged_varlen_prefill_attn(q, cu_q, cu_k, nq, n, 0.1, k_cache=kc, v_cache=vc,
+                                                              block_tables=table, **kw),
+    }
+
+
+@pytest.mark.parametrize("kind", ["decode", "fp8", "verify", "prefill"])
+def test_call_on_another_stream_while_the_current_one_is_busy(kind, monkeypatch):
+    # the call's own workspace is allocated and zeroed on the stream it runs on: here the current stream is still
+    # busy, and its pool holds a freed block of other bytes that a workspace from there would be
+    monkeypatch.setattr(pkv.ops, "_prefill_ws", {})
+    call = _split_calls()[kind]
+    ref = call()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(pkv.ops, "_prefill_ws", {})
+    del_me = torch.full((64 << 20,), 1, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del del_me
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(200_000_000)
+    out = call(stream=side)
+    side.synchronize()
+    again = call(stream=side)
+    torch.cuda.synchronize()
+    assert pkv.device_error() == 0
+    assert torch.equal(out, ref) and torch.equal(again, ref)
