@@ -297,8 +297,9 @@ def paged_varlen_prefill_attn(q: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_se
     """Packed varlen prefill attention; keys through block_tables (cache) or from packed k/v.
 
     workspace: None = a zero-filled workspace cached per device (calls that may
-    overlap on different streams must pass their own), or with `stream` one for this
-    call; False = never split long query tiles; or a tensor from prefill_workspace().
+    overlap on different streams must pass their own), or with `stream` and in a captured
+    graph one for this call; False = never split long query tiles; or a tensor from
+    prefill_workspace().
     """
     dev = _device(q, "q")
     _need(q, "q", ndim=3)
@@ -334,7 +335,7 @@ def paged_varlen_prefill_attn(q: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_se
     handle = _stream(stream, dev)
     if workspace is None:
         nbytes = prefill_workspace_bytes(B, hq, hkv, d, int(max_seqlen_q))
-        if nbytes > 0 and stream is None:
+        if nbytes > 0 and stream is None and not torch.cuda.is_current_stream_capturing():
             workspace = _cached_prefill_workspace(nbytes, dev)
     else:
         nbytes = 0

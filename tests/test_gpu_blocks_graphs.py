@@ -174,3 +174,27 @@ def test_call_on_another_stream_while_the_current_one_is_busy(kind, monkeypatch)
     torch.cuda.synchronize()
     assert pkv.device_error() == 0
     assert torch.equal(out, ref) and torch.equal(again, ref)
+
+
+def test_captured_prefill_keeps_its_workspace_when_larger_calls_follow(monkeypatch):
+    # a captured call without a workspace: eager calls that need a larger one replace the one cached for eager calls,
+    # and what they free must not be what the graph writes to
+    monkeypatch.setattr(pkv.ops, "_prefill_ws", {})
+    call = _split_calls()["prefill"]
+    ref = call()
+    torch.cuda.synchronize()
+    before = dict(pkv.ops._prefill_ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    assert pkv.ops._prefill_ws.keys() == before.keys() and all(pkv.ops._prefill_ws[i] is before[i] for i in before)
+    pkv.ops._prefill_ws.clear()
+    del before
+    # whatever the eager workspace was is free: other tensors take its place, and must not change
+    others = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(200)]
+    for _ in range(2):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert pkv.device_error() == 0 and torch.equal(out, ref)
+    assert all(bool((x == 7).all()) for x in others)
