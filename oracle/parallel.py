@@ -36,9 +36,19 @@ def host_cores() -> int:
         return os.cpu_count() or 1
 
 
-def _worker_init() -> None:
-    for var in ("OMP_NUM_THREADS", "OPENBLAS_NUM_THREADS", "MKL_NUM_THREADS"):
-        os.environ[var] = "1"
+def _one_thread_pool(workers: int):
+    """Spawned workers with one BLAS thread each.  numpy reads the limits while it is imported, which a
+    worker does before any initializer of ours runs, so they are in the environment it starts with."""
+    saved = {var: os.environ.get(var) for var in ("OMP_NUM_THREADS", "OPENBLAS_NUM_THREADS", "MKL_NUM_THREADS")}
+    os.environ.update(dict.fromkeys(saved, "1"))
+    try:
+        return mp.get_context("spawn").Pool(workers)
+    finally:
+        for var, value in saved.items():
+            if value is None:
+                del os.environ[var]
+            else:
+                os.environ[var] = value
 
 
 def _is_file_spec(spec) -> bool:
@@ -152,7 +162,7 @@ class OraclePool:
 
     def __init__(self, workers: int | None = None):
         self.workers = workers or host_cores()
-        self._pool = mp.get_context("spawn").Pool(self.workers, initializer=_worker_init)
+        self._pool = _one_thread_pool(self.workers)
         self._dirs: list[str] = []
 
     # ------------------------------------------------------------ shared inputs
