@@ -51,6 +51,10 @@
  *    and raises a bit in the per-device error word (pkv_get_device_error);
  *    the kernels never trap.
  *  - Element offsets are computed in 64-bit; counts are int32.
+ *  - NaN: an attention row is NaN when its q, or K of a key that it sees, holds
+ *    one, wherever the key lies and however the work is split.  V of every key of
+ *    a sequence that any of its rows may read must be finite: the prefill and
+ *    verify calls weigh a key that a row does not see (a later token's) by 0.
  */
 #ifndef PAGEDKV_H
 #define PAGEDKV_H
@@ -377,7 +381,7 @@ size_t pkv_paged_varlen_prefill_workspace_bytes(int32_t batch, int32_t num_q_hea
  * is the table entry of a block that holds only such keys.
  *
  * softcap         0 = none, else in [1e-30, 1e30]
- * alibi_slopes    device, float32 [num_q_heads], or NULL
+ * alibi_slopes    device, float32 [num_q_heads], finite, or NULL
  * first_keys      device, int32, or NULL: [batch] for decode, [total_q] for the prefill call
  * prefix_lens     device, int32 [batch], or NULL: any value (clamped to [0, nk]); needs causal = 1
  *
@@ -456,8 +460,10 @@ size_t pkv_paged_short_chunk_workspace_bytes(int32_t batch, int32_t num_q_heads,
  *   other arguments, range checks, workspace and its size function as for
  *   pkv_paged_varlen_prefill_attn (short chunks:
  *   pkv_paged_short_chunk_workspace_bytes)
- * The weights enter the P V product as f16 (the row sums add the same rounded
- * weights), q as f16 after a power-of-two scaling of each row.
+ * The weights enter the P V product as f16, taken 2^7 times as large (the row
+ * sums add the same rounded weights): a weight is off by 2^-11 of itself or 2^-32
+ * of its row's largest.  q enters as f16 after a power-of-two scaling of each row,
+ * whatever its magnitude.
  * Supported: head_dim 64 or 128; G in {1, 2, 4, 8}; every block size.
  */
 int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,

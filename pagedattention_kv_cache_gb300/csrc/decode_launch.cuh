@@ -25,9 +25,9 @@
 //    waiting) elect the CTAs that merge the parts by log-sum-exp.
 // paged_decode_mma_kernel (mma.sync tensor cores, 16-token tensor copies)
 // runs every bf16 or FP8 cache with head_dim 128; paged_decode_kernel (CUDA
-// cores, 1-D bulk copies of token spans) runs fp32 caches and head_dim 64.
+// cores, 1-D bulk copies of token spans) runs fp32 caches, and bf16 with head_dim 64.
 // Two template switches give both kernels further uses: kMod, score modifiers
-// (decode_mod.cu; bf16 with head_dim 64 then runs on the tensor cores too), and,
+// (decode_mod.cu; bf16 with head_dim 64 runs on the tensor cores there), and,
 // for the first, kVar, short chunks of new tokens (chunk_decode.cu).
 //
 // Verify (speculative-decoding target pass, QL > 1): query token i of

@@ -1,5 +1,6 @@
-// paged_decode_kernel: the CUDA-core decode / verify kernel (fp32 caches and
-// head_dim 64).  The CTA plan, split and merge it uses are in decode_plan.cuh.
+// paged_decode_kernel: the CUDA-core decode kernel (fp32 caches, and bf16 caches
+// with head_dim 64 where no score modifiers are compiled in).  The CTA plan,
+// split and merge it uses are in decode_plan.cuh.
 #pragma once
 
 #include "decode_plan.cuh"

@@ -53,7 +53,15 @@ int check_args(const PrefillArgs& a, int max_seqlen_k) {
 // decode / tcgen05): 4 tokens x 1 sequence after 512 keys 16.9 / 13.8, after
 // 2048 21.0 / 25.2; x 16 sequences 27.6 / 14.5 and 30.2 / 35.6; 1 token x 1
 // sequence after 128 keys 8.3 / 8.9, after 512 10.2 / 13.8; two waves (64
-// sequences) 16.9 / 28.3 after 32 keys.
+// sequences) 16.9 / 28.3 after 32 keys.  bf16 moves twice the bytes: 2 tokens x 1
+// sequence after 1024 keys 13.0 / 15.9, after 8192 18.7 / 32.5 (E4M3 13.3 / 16.8 and
+// 17.8 / 34.3); x 64 after 512 28.0 / 47.0 (23.6 / 50.7).  Fewer KV heads, 2 of
+// them with G = 4, 1 token: x 1 after 1024 bf16 11.0 / 15.6, x 16 after 8192 32.6 / 85.3.
+// The rule looks at the rows, not at the number of sequences within a wave, and
+// is on the wrong side just past its border where several share it: 2 tokens
+// x 16 sequences after 512 keys 20.7 / 13.7 (bf16 20.1 / 12.2), after 1024 22.9 / 19.2
+// (24.0 / 17.1), bf16 after 2048 30.9 / 27.9 and after 8192 89.0 / 87.2; 2 KV heads,
+// G = 4, 1 token x 64 after 2048 bf16 30.9 / 27.9 (E4M3 23.4 / 30.1).
 bool short_chunk(int batch, int group, int num_kv_heads, int head_dim, int max_seqlen_q, int max_seqlen_k) {
   const long long rows = static_cast<long long>(max_seqlen_q) * group;
   if (head_dim != 128 || num_kv_heads > 8 || rows > 8) return false;
