@@ -955,18 +955,20 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     const int lim = p.causal ? min(pos, nk - 1) : nk - 1;
     // kMod: the row sees keys lo .. hi; a row that sees none gets a range no key is
     // in.  Taken anew for each tile that needs it: held through the loop, the two
-    // would cost registers.
+    // would cost registers.  Rows past the last token see none: a warp's rows share the
+    // decision to rescale, and such a row's scores of keys that were not read (stale
+    // shared memory) would change the other rows' rounding from run to run.
     auto seen_range = [&](int& lo, int& hi) {
       hi = max(lim, prefix_end - 1);
       lo = p.mod.first_keys && tok < nq ? max(__ldg(p.mod.first_keys + q_begin + tok), 0) : 0;
-      if (lo > hi) lo = hi = INT32_MAX;
+      if (lo > hi || tok >= nq) lo = hi = INT32_MAX;
     };
     int lo_most = 0;     // the largest lo of the warp
     float slope = 0.f;   // per key of distance, in the units of bias_scores
     if constexpr (kMod) {
       int hi;
       seen_range(lo_most, hi);
-      lo_most = __reduce_max_sync(0xffffffffu, lo_most);
+      lo_most = __reduce_max_sync(0xffffffffu, tok < nq ? lo_most : 0);
       if constexpr (kBias) slope = __ldg(p.mod.slopes + g * G + row % G) * p.bias_mul;
     }
     float mul = kBias && kCap ? 1.f : p.scale_log2;  // scores as held in registers to exponents
@@ -1047,10 +1049,19 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       tc::tmem_ld32(s_addr + half * 64 + 32, r + 32);
       tc::tmem_wait_ld();
       if constexpr (kMod) {
-        if constexpr (kBias && kCap) cap_scores(p, r);
-        if constexpr (kBias) bias_scores(r, slope, key0 - pos, key0 + 63 > cached + tok_first);
         const int seen_by_all = p.causal ? max(cached + tok_first, prefix_end - 1) : nk - 1;
         masked = key0 + 63 > seen_by_all || key0 < lo_most;
+        if constexpr (kBias && kCap) {
+          // the scores' size chooses how the cap is taken: keys that were not read (stale shared memory), or lie past
+          // the sequence's end, must not count
+          if (key0 < lo_pair || key0 + 63 >= nk) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (key0 + e < lo_pair || key0 + e >= nk) r[e] = 0u;
+          }
+          cap_scores(p, r);
+        }
+        if constexpr (kBias) bias_scores(r, slope, key0 - pos, key0 + 63 > cached + tok_first);
         if (masked) hide(key0);
       } else if (key0 + 63 > (p.causal ? cached + tok_first : nk - 1)) {
 #pragma unroll
