@@ -429,15 +429,3 @@ def test_parallel_driver_reproduces_the_serial_oracle():
         specs.update(q=qp, cu_seqlens_q=meta["cu_seqlens_q"], cu_seqlens_k=meta["cu_seqlens_k"],
                      block_tables=meta["block_tables"], scale=0.2, causal=True)
         assert np.array_equal(pool.prefill(specs, 3, sum(new)), want_p)
-
-
-def test_parallel_workers_start_with_one_blas_thread(monkeypatch):
-    # numpy reads the limits when it is imported, so they must be in the environment a worker starts with
-    from oracle.parallel import OraclePool
-
-    monkeypatch.delenv("OPENBLAS_NUM_THREADS", raising=False)
-    monkeypatch.setenv("OMP_NUM_THREADS", "5")
-    with OraclePool(1) as pool:
-        start = pool._pool.apply(eval, ("open('/proc/self/environ', 'rb').read()",)).split(b"\0")
-    assert b"OPENBLAS_NUM_THREADS=1" in start and b"OMP_NUM_THREADS=1" in start
-    assert os.environ["OMP_NUM_THREADS"] == "5" and "OPENBLAS_NUM_THREADS" not in os.environ
