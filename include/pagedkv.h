@@ -92,6 +92,7 @@ typedef enum {
 #define PKV_DERR_BLOCK_RANGE 0x2u    /* a block table entry that must be read is outside [0, num_blocks) */
 #define PKV_DERR_LEN_RANGE 0x4u      /* context_lens / cu_seqlens inconsistent with the table width or the batch */
 #define PKV_DERR_WAIT_TIMEOUT 0x8u   /* a pipeline wait gave up (about 1 s); the results are invalid */
+#define PKV_DERR_POSITION_RANGE 0x10u /* kv_rope_store: a position outside [0, max_position) */
 
 /* Library ABI version (major * 10000 + minor * 100 + patch). */
 int pkv_version(void);
@@ -475,6 +476,120 @@ int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const void* k_ca
                                       int32_t num_blocks, float scale, float k_scale, float v_scale,
                                       int32_t causal, void* workspace, size_t workspace_bytes,
                                       pkv_stream_t stream);
+
+/*
+ * The rotating stores and the 4-bit cache.
+ *
+ * 4-bit cache of one layer: k_cache and v_cache are each bytes [num_blocks,
+ * block_size, pkv_q4_row_bytes(num_kv_heads, head_dim)].  A token's row is
+ *   num_kv_heads * head_dim / 2 code bytes   byte i of a head: the codes of its
+ *                                            elements 2i (low nibble) and 2i + 1
+ *   num_kv_heads * head_dim / 16 scale bytes E4M3, one per 16 elements of a head
+ *   unused bytes up to a multiple of 16
+ * and an element is (code - 8) * scale * T, T the tensor's float scale (k_scale
+ * or v_scale).  Storing x: the scale is e4m3(amax / (7 T)) of the 16 elements'
+ * largest magnitude (round to nearest even, saturating at 448), and the code
+ * is 8 + x / (scale * T) rounded to nearest even, between 0 and 15 (8 where that
+ * step is 0).  All in float32.  A group that holds a NaN gets a NaN scale and
+ * reads as NaN; infinities saturate.
+ * A zero-filled cache reads as zeros.  head_dim 64 or 128.
+ */
+typedef enum {
+  PKV_CACHE_SAME = 0, /* the rows' own type */
+  PKV_CACHE_E4M3 = 1, /* E4M3 codes with one float scale per tensor (pkv_kv_store_fp8) */
+  PKV_CACHE_Q4 = 2    /* the 4-bit rows above */
+} pkv_cache_format;
+
+/* Bytes of a token's row in a 4-bit K (or V) cache; 0 for sizes that are not supported. */
+int64_t pkv_q4_row_bytes(int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * kv_rope_store: one step's q and k rotated by position, and k and v stored as by
+ * pkv_kv_store (pkv_kv_store_fp8, pkv_kv_store_q4).  For token i at position
+ * p = positions[i], c = cos_sin[p][0 .. rot_dim/2), s = cos_sin[p][rot_dim/2 ..):
+ *   (a, b) -> (a c[j] - b s[j], b c[j] + a s[j])
+ * for the pairs j = 0 .. rot_dim/2 - 1 of each head of q and k: (j, j + rot_dim/2),
+ * or with `interleaved` (2j, 2j + 1).  Elements past rot_dim, and v, stay.  The
+ * rotated element is rounded to float32 and then to the rows' type, and a
+ * quantized cache stores that value.
+ *
+ *   q_out           device, [num_tokens, num_q_heads, head_dim], contiguous.  May be q
+ *                   itself where q is contiguous; overlaps nothing else
+ *   q, k, v         device; element j of head h of token i is at i * stride + h *
+ *                   head_dim + j (rows of a fused projection need no copy)
+ *   *_stride        elements, at least heads * head_dim, a multiple of 16 bytes
+ *   positions       device, int32 [num_tokens]
+ *   cos_sin         device, float32 [max_position, rot_dim]
+ *   k_cache,v_cache device, in `format`'s layout
+ *   slot_mapping    device, int32 [num_tokens]; -1 stores nothing (q is rotated all the same)
+ *   dtype           F32 or BF16, of q, k, v and q_out (E4M3 and 4-bit caches: BF16)
+ *   k_scale,v_scale finite and > 0 (ignored for PKV_CACHE_SAME)
+ * head_dim a multiple of 32, at most 512 (4 bits: 64 or 128); rot_dim a multiple
+ * of 32, at most head_dim.  A token whose position is outside the table is
+ * skipped whole and raises PKV_DERR_POSITION_RANGE; a slot outside the cache
+ * raises PKV_DERR_SLOT_RANGE and stores nothing.  Duplicate slots are a caller
+ * error, as for pkv_kv_store.
+ */
+int pkv_kv_rope_store(void* q_out, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride, const int32_t* positions, const float* cos_sin,
+                      int32_t max_position, int32_t rot_dim, int32_t interleaved, void* k_cache,
+                      void* v_cache, const int32_t* slot_mapping, int32_t num_tokens,
+                      int32_t num_blocks, int32_t block_size, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, pkv_cache_format format, float k_scale,
+                      float v_scale, pkv_dtype dtype, pkv_stream_t stream);
+
+/*
+ * kv_store_q4: pkv_kv_store's slot scatter of bf16 rows [num_tokens, num_kv_heads,
+ * head_dim] into a 4-bit cache.
+ */
+int pkv_kv_store_q4(const void* k, const void* v, void* k_cache, void* v_cache,
+                    const int32_t* slot_mapping, int32_t num_tokens, int32_t num_blocks,
+                    int32_t block_size, int32_t num_kv_heads, int32_t head_dim, float k_scale,
+                    float v_scale, pkv_stream_t stream);
+
+/*
+ * kv_load_q4: the rows at slot_mapping read back from a 4-bit cache as bf16
+ * [num_tokens, num_kv_heads, head_dim] (a prefix moved to another cache or to
+ * the host).  The value (code - 8) * (scale * T) in float32, rounded to bf16.
+ * Slot -1 gives a row of zeros; a slot outside the cache too, and raises
+ * PKV_DERR_SLOT_RANGE.
+ */
+int pkv_kv_load_q4(void* k, void* v, const void* k_cache, const void* v_cache,
+                   const int32_t* slot_mapping, int32_t num_tokens, int32_t num_blocks,
+                   int32_t block_size, int32_t num_kv_heads, int32_t head_dim, float k_scale,
+                   float v_scale, pkv_stream_t stream);
+
+/*
+ * paged_decode_attn_q4: pkv_paged_decode_attn over a 4-bit cache: the same result
+ * as on the values that the cache stands for.  q, out bf16; every other
+ * argument, the workspace and its size function are pkv_paged_decode_attn's.
+ * q's rows may have any magnitude (they enter the products scaled by a power of two).
+ * Supported: head_dim 64 or 128; at most 8 KV heads; G in {1, 2, 4, 8}; every
+ * block size.
+ */
+int pkv_paged_decode_attn_q4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                             const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                             int32_t num_blocks, float scale, float k_scale, float v_scale,
+                             int32_t num_splits, void* workspace, size_t workspace_bytes,
+                             pkv_stream_t stream);
+
+/*
+ * paged_varlen_prefill_attn_q4: pkv_paged_varlen_prefill_attn_fp8 over a 4-bit
+ * cache; the new rows are stored first (pkv_kv_store_q4, pkv_kv_rope_store).
+ * Arguments, range checks, workspace and its size functions are the E4M3 call's.
+ * Supported: head_dim 64 or 128; G in {1, 2, 4, 8}; every block size.
+ */
+int pkv_paged_varlen_prefill_attn_q4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                     int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                     int32_t num_blocks, float scale, float k_scale, float v_scale,
+                                     int32_t causal, void* workspace, size_t workspace_bytes,
+                                     pkv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -31,12 +31,19 @@ DERR_SLOT_RANGE = 0x1
 DERR_BLOCK_RANGE = 0x2
 DERR_LEN_RANGE = 0x4
 DERR_WAIT_TIMEOUT = 0x8
+DERR_POSITION_RANGE = 0x10
+
+# pkv_cache_format
+CACHE_SAME = 0
+CACHE_E4M3 = 1
+CACHE_Q4 = 2
 
 # (name, restype, argtypes) of every exported symbol
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _F = ctypes.c_float
 _S = ctypes.c_size_t
+_L = ctypes.c_int64
 SIGNATURES = [
     ("pkv_version", ctypes.c_int, []),
     ("pkv_status_string", ctypes.c_char_p, [ctypes.c_int]),
@@ -65,6 +72,16 @@ SIGNATURES = [
      [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _F, _P, _P, _P, _P, _S,
       ctypes.c_int, _P]),
     ("pkv_paged_varlen_prefill_attn_fp8", ctypes.c_int,
+     [_P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F, _F, _I, _P, _S, _P]),
+    ("pkv_q4_row_bytes", _L, [_I, _I]),
+    ("pkv_kv_rope_store", ctypes.c_int,
+     [_P, _P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_int, _F, _F,
+      ctypes.c_int, _P]),
+    ("pkv_kv_store_q4", ctypes.c_int, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P]),
+    ("pkv_kv_load_q4", ctypes.c_int, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P]),
+    ("pkv_paged_decode_attn_q4", ctypes.c_int,
+     [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _F, _F, _I, _P, _S, _P]),
+    ("pkv_paged_varlen_prefill_attn_q4", ctypes.c_int,
      [_P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F, _F, _I, _P, _S, _P]),
 ]
 

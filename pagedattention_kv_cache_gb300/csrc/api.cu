@@ -122,7 +122,7 @@ int encode_paged_kv(void* map, const void* base, uint32_t block_size, uint32_t h
 
 }  // namespace pkv
 
-extern "C" int pkv_version(void) { return 10100; }
+extern "C" int pkv_version(void) { return 10200; }
 
 extern "C" const char* pkv_status_string(int status) {
   switch (status) {

@@ -49,6 +49,8 @@ int prefill_tc_capped_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_biased_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_capped_biased_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_fp8_launch(const PrefillArgs& a, cudaStream_t stream);
+// Chunks over a 4-bit cache.
+int chunk_q4_launch(const PrefillArgs& a, cudaStream_t stream);
 // Chunks of at most 8 rows per KV head (max_seqlen_q * G <= 8) on the decode
 // kernel; workspace bytes it needs on the current device (0: an error).
 int chunk_decode_launch(const PrefillArgs& a, bool fp8, cudaStream_t stream);

@@ -1,6 +1,6 @@
-// paged_varlen_prefill_attn_mod and paged_varlen_prefill_attn_fp8: a chunk of
-// new tokens per sequence over its keys, with modified scores, or over an
-// FP8 E4M3 cache.
+// paged_varlen_prefill_attn_mod, paged_varlen_prefill_attn_fp8 and
+// paged_varlen_prefill_attn_q4: a chunk of new tokens per sequence over its keys,
+// with modified scores, or over an FP8 E4M3 or a 4-bit cache.
 //
 // Row r of sequence i sits at p = nk - nq + r.  For query head h (KV head
 // h / G) and every key t that the row sees,
@@ -140,17 +140,17 @@ extern "C" int pkv_paged_varlen_prefill_attn_mod(
   return softcap > 0.f ? pkv::prefill_tc_capped_launch(a, stream) : pkv::prefill_tc_masked_launch(a, stream);
 }
 
-extern "C" int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
-                                                 const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
-                                                 int32_t max_seqlen_q, int32_t max_seqlen_k,
-                                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                                 int32_t batch, int32_t total_q, int32_t num_q_heads,
-                                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-                                                 int32_t num_blocks, float scale, float k_scale, float v_scale,
-                                                 int32_t causal, void* workspace, size_t workspace_bytes,
-                                                 pkv_stream_t stream) {
+namespace {
+
+// Arguments of a chunk over a quantized cache; PKV_OK when a launch may follow,
+// 1 when there is nothing to do, else the negative status to return.
+int quantized_args(PrefillArgs& a, void* out, const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int32_t max_seqlen_q,
+                   int32_t max_seqlen_k, const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch,
+                   int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                   int32_t num_blocks, float scale, float k_scale, float v_scale, int32_t causal, void* workspace,
+                   size_t workspace_bytes) {
   if (!(k_scale > 0.f) || !(v_scale > 0.f) || isinf(k_scale) || isinf(v_scale)) return PKV_EINVAL;
-  PrefillArgs a{};
   a.out = out;
   a.q = q;
   a.k_cache = k_cache;
@@ -175,11 +175,47 @@ extern "C" int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   const int chk = check_args(a, max_seqlen_k);
-  if (chk != PKV_OK) return chk > 0 ? PKV_OK : chk;
+  if (chk != PKV_OK) return chk;
   if (!block_tables) return PKV_EINVAL;
   int st = PKV_OK;
   a.err = pkv::device_error_word(&st);
   if (st != PKV_OK) return st;
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                                 const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                                 int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                 int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                                 int32_t num_blocks, float scale, float k_scale, float v_scale,
+                                                 int32_t causal, void* workspace, size_t workspace_bytes,
+                                                 pkv_stream_t stream) {
+  PrefillArgs a{};
+  const int chk = quantized_args(a, out, q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                 block_tables, max_blocks_per_seq, batch, total_q, num_q_heads, num_kv_heads, head_dim,
+                                 block_size, num_blocks, scale, k_scale, v_scale, causal, workspace, workspace_bytes);
+  if (chk != PKV_OK) return chk > 0 ? PKV_OK : chk;
   if (on_decode_kernel(a, max_seqlen_k)) return pkv::chunk_decode_launch(a, true, stream);
   return pkv::prefill_tc_fp8_launch(a, stream);
+}
+
+extern "C" int pkv_paged_varlen_prefill_attn_q4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                                int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                                int32_t num_blocks, float scale, float k_scale, float v_scale,
+                                                int32_t causal, void* workspace, size_t workspace_bytes,
+                                                pkv_stream_t stream) {
+  PrefillArgs a{};
+  const int chk = quantized_args(a, out, q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                 block_tables, max_blocks_per_seq, batch, total_q, num_q_heads, num_kv_heads, head_dim,
+                                 block_size, num_blocks, scale, k_scale, v_scale, causal, workspace, workspace_bytes);
+  if (chk != PKV_OK) return chk > 0 ? PKV_OK : chk;
+  return pkv::chunk_q4_launch(a, stream);
 }

@@ -104,6 +104,16 @@ def pad_decode(md: dict, batch: int) -> dict:
     return {"slot_mapping": slots, "context_lens": lens, "block_tables": tables}
 
 
+def rope_cos_sin(max_position: int, rot_dim: int, base: float = 10000.0) -> np.ndarray:
+    """The float32 [max_position, rot_dim] table kv_rope_store takes: per position the cosines of its
+    rot_dim / 2 angles position * base^(-2j / rot_dim), then their sines (angles and functions in float64)."""
+    if rot_dim <= 0 or rot_dim % 2 or max_position < 0:
+        raise ValueError("rot_dim must be even and positive, max_position non-negative")
+    angle = np.arange(max_position, dtype=np.float64)[:, None] * float(base) ** (
+        -np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
+    return np.concatenate([np.cos(angle), np.sin(angle)], axis=1).astype(np.float32)
+
+
 def to_device(md: dict, device) -> dict:
     """Copy every numpy array of a metadata dict to an int32 tensor on ``device``."""
     return {k: (torch.from_numpy(np.ascontiguousarray(v)).to(device) if isinstance(v, np.ndarray) else v)

@@ -547,6 +547,217 @@ def paged_varlen_prefill_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     return out
 
 
+def q4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of a token's row in a 4-bit K (or V) cache; head_dim 64 or 128."""
+    n = int(_lib.load().pkv_q4_row_bytes(num_kv_heads, head_dim))
+    if n == 0:
+        raise ValueError(f"no 4-bit cache of {num_kv_heads} KV heads with head_dim {head_dim}")
+    return n
+
+
+def q4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """A zero-filled 4-bit K (or V) cache, uint8 [num_blocks, block_size, q4_row_bytes]; it reads as zeros."""
+    return torch.zeros(num_blocks, block_size, q4_row_bytes(num_kv_heads, head_dim), dtype=torch.uint8,
+                       device=device or torch.cuda.current_device())
+
+
+def _need_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, num_kv_heads: int, head_dim: int, device) -> None:
+    _need(k_cache, "k_cache", dtype=torch.uint8, ndim=3, device=device)
+    _need(v_cache, "v_cache", dtype=torch.uint8, device=device, shape=k_cache.shape)
+    row = q4_row_bytes(num_kv_heads, head_dim)
+    if k_cache.shape[2] != row:
+        raise ValueError(f"a 4-bit cache of {num_kv_heads} KV heads with head_dim {head_dim} has rows of {row} bytes, "
+                         f"got {k_cache.shape[2]}")
+
+
+def kv_store_q4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                slot_mapping: torch.Tensor, k_scale: float, v_scale: float, stream=None) -> None:
+    """Quantizing store: bf16 rows [N, Hkv, D] into 4-bit caches (q4_cache); slot -1 skips."""
+    dev = _device(k, "k")
+    _need(k, "k", dtype=torch.bfloat16, ndim=3)
+    _need(v, "v", dtype=torch.bfloat16, device=dev, shape=k.shape)
+    n, hkv, d = k.shape
+    _need_q4(k_cache, v_cache, hkv, d, dev)
+    _need(slot_mapping, "slot_mapping", dtype=torch.int32, device=dev, shape=(n,))
+    nb, bs, _ = k_cache.shape
+    st = _lib.load().pkv_kv_store_q4(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n, nb, bs, hkv, d,
+                                     k_scale, v_scale, _stream(stream, dev))
+    _lib.check("pkv_kv_store_q4", st)
+
+
+def kv_load_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor, k_scale: float, v_scale: float,
+               num_kv_heads: int, head_dim: int, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The K and V rows at slot_mapping of 4-bit caches as bf16 [N, Hkv, D]; slot -1 gives zeros."""
+    dev = _device(k_cache, "k_cache")
+    _need_q4(k_cache, v_cache, num_kv_heads, head_dim, dev)
+    _need(slot_mapping, "slot_mapping", dtype=torch.int32, ndim=1, device=dev)
+    n, (nb, bs, _) = slot_mapping.shape[0], k_cache.shape
+    handle = _stream(stream, dev)
+    with torch.cuda.stream(stream):  # (None: the current one)
+        k, v = [torch.empty(n, num_kv_heads, head_dim, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    st = _lib.load().pkv_kv_load_q4(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n, nb, bs,
+                                    num_kv_heads, head_dim, k_scale, v_scale, handle)
+    _lib.check("pkv_kv_load_q4", st)
+    return k, v
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype, device) -> int:
+    """Checks rows [N, heads, D] whose heads are contiguous; returns the stride from one token to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.get_device() != device.index:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
+    n, heads, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    if n <= 1:
+        return heads * d
+    if t.stride(0) < heads * d:
+        raise ValueError(f"{name}'s rows overlap")
+    return t.stride(0)
+
+
+def _rope_store(fn: str, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, fmt: int, k_scale: float,
+                v_scale: float, interleaved: bool, q_out, stream) -> torch.Tensor:
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev = q.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"q is on {dev} but the current CUDA device is cuda:{torch.cuda.current_device()}")
+    dtype = q.dtype if fmt == _lib.CACHE_SAME else torch.bfloat16
+    code = _dtype_code(q)
+    qs, ks, vs = _need_rows(q, "q", dtype, dev), _need_rows(k, "k", dtype, dev), _need_rows(v, "v", dtype, dev)
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    if k.shape != (n, hkv, d) or v.shape != k.shape:
+        raise ValueError("expected q [N, Hq, D] and k, v [N, Hkv, D]")
+    _need(positions, "positions", dtype=torch.int32, device=dev, shape=(n,))
+    _need(slot_mapping, "slot_mapping", dtype=torch.int32, device=dev, shape=(n,))
+    _need(cos_sin, "cos_sin", dtype=torch.float32, ndim=2, device=dev)
+    if fmt == _lib.CACHE_Q4:
+        _need_q4(k_cache, v_cache, hkv, d, dev)
+    else:
+        _need(k_cache, "k_cache", ndim=4, device=dev)
+        _need(v_cache, "v_cache", dtype=k_cache.dtype, device=dev, shape=k_cache.shape)
+        if fmt == _lib.CACHE_SAME and k_cache.dtype != dtype:
+            raise TypeError(f"k_cache must be {dtype}, got {k_cache.dtype}")
+        if fmt == _lib.CACHE_E4M3 and k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError("k_cache must hold E4M3 codes (uint8 or float8_e4m3fn)")
+        if k_cache.shape[2:] != k.shape[1:]:
+            raise ValueError("k/v rows and the cache disagree on (Hkv, D)")
+    handle = _stream(stream, dev)
+    if q_out is None:
+        if stream is None:
+            q_out = torch.empty((n, hq, d), dtype=dtype, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                q_out = torch.empty((n, hq, d), dtype=dtype, device=dev)
+    else:
+        _need(q_out, "q_out", dtype=dtype, device=dev, shape=q.shape)
+    st = _lib.load().pkv_kv_rope_store(
+        _ptr(q_out), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
+        cos_sin.shape[1], 1 if interleaved else 0, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n, k_cache.shape[0],
+        k_cache.shape[1], hq, hkv, d, fmt, k_scale, v_scale, code, handle)
+    _lib.check(fn, st)
+    return q_out
+
+
+def kv_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                  k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor, *,
+                  interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotate q [N, Hq, D] and k [N, Hkv, D] by position and store k, v as kv_store does; returns the rotated q.
+
+    positions: int32 [N]; cos_sin: float32 [max_position, rot_dim], cosines then sines (metadata.rope_cos_sin).
+    The first rot_dim elements of each head turn in pairs (j, j + rot_dim / 2), with `interleaved` (2j, 2j + 1).
+    q, k, v may be views of a fused projection's rows (heads contiguous, any stride from token to token).
+    q_out: contiguous [N, Hq, D]; may be q itself when q is contiguous.
+    """
+    return _rope_store("pkv_kv_rope_store", q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                       _lib.CACHE_SAME, 1.0, 1.0, interleaved, q_out, stream)
+
+
+def kv_rope_store_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                      cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                      k_scale: float, v_scale: float, *, interleaved: bool = False,
+                      q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kv_rope_store of bf16 rows into E4M3 caches (kv_store_fp8's codes of the rotated k, and of v)."""
+    return _rope_store("pkv_kv_rope_store", q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                       _lib.CACHE_E4M3, k_scale, v_scale, interleaved, q_out, stream)
+
+
+def kv_rope_store_q4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                     k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor, k_scale: float,
+                     v_scale: float, *, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """kv_rope_store of bf16 rows into 4-bit caches (kv_store_q4's rows of the rotated k, and of v)."""
+    return _rope_store("pkv_kv_rope_store", q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, _lib.CACHE_Q4,
+                       k_scale, v_scale, interleaved, q_out, stream)
+
+
+def paged_decode_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, scale: float, k_scale: float, v_scale: float, num_kv_heads: int, *,
+                         num_splits: int = 0, workspace: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Decode attention over 4-bit caches (q4_cache); q / out bf16 [B, Hq, D].
+
+    num_splits, workspace: as for paged_decode_attn.
+    """
+    dev = _device(q, "q")
+    _need(q, "q", dtype=torch.bfloat16, ndim=3)
+    B, hq, d = q.shape
+    _need_q4(k_cache, v_cache, num_kv_heads, d, dev)
+    _need(block_tables, "block_tables", dtype=torch.int32, ndim=2, device=dev)
+    _need(context_lens, "context_lens", dtype=torch.int32, ndim=1, device=dev)
+    nb, bs, _ = k_cache.shape
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("inconsistent shapes between q, block_tables and context_lens")
+    handle = _stream(stream, dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _decode_workspace_args, workspace, B, hq, d, num_splits, dev)
+    st = _lib.load().pkv_paged_decode_attn_q4(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+        _ptr(context_lens), B, hq, num_kv_heads, d, bs, nb, scale, k_scale, v_scale, num_splits, ws_ptr, ws_bytes, handle)
+    _lib.check("pkv_paged_decode_attn_q4", st)
+    return out
+
+
+def paged_varlen_prefill_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                                 max_seqlen_q: int, max_seqlen_k: int, scale: float, k_scale: float, v_scale: float,
+                                 num_kv_heads: int, *, causal: bool = True,
+                                 workspace: torch.Tensor | bool | None = None,
+                                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Varlen prefill attention of new tokens over 4-bit caches (q4_cache); q / out bf16 [total_q, Hq, D].
+
+    The new rows are stored first (kv_store_q4, kv_rope_store_q4).  workspace: as for paged_varlen_prefill_attn_mod.
+    """
+    dev = _device(q, "q")
+    _need(q, "q", dtype=torch.bfloat16, ndim=3)
+    total_q, hq, d = q.shape
+    _need_q4(k_cache, v_cache, num_kv_heads, d, dev)
+    _need(block_tables, "block_tables", dtype=torch.int32, ndim=2, device=dev)
+    _need(cu_seqlens_q, "cu_seqlens_q", dtype=torch.int32, ndim=1, device=dev)
+    _need(cu_seqlens_k, "cu_seqlens_k", dtype=torch.int32, ndim=1, device=dev, shape=cu_seqlens_q.shape)
+    if cu_seqlens_q.shape[0] < 1:
+        raise ValueError("cu_seqlens_q must hold batch + 1 offsets")
+    B = cu_seqlens_q.shape[0] - 1
+    nb, bs, _ = k_cache.shape
+    if block_tables.shape[0] != B:
+        raise ValueError("block_tables rows must equal the batch")
+    handle = _stream(stream, dev)
+    out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _chunk_workspace_args, workspace, B, hq, num_kv_heads, d,
+                                                int(max_seqlen_q), int(max_seqlen_k), True, dev)
+    st = _lib.load().pkv_paged_varlen_prefill_attn_q4(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(max_seqlen_q),
+        int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], B, total_q, hq, num_kv_heads, d, bs, nb, scale,
+        k_scale, v_scale, 1 if causal else 0, ws_ptr, ws_bytes, handle)
+    _lib.check("pkv_paged_varlen_prefill_attn_q4", st)
+    return out
+
+
 def device_error(reset: bool = True) -> int:
     """Read (and by default clear) the current device's error word; synchronises the device."""
     flags = ctypes.c_uint32(0)
