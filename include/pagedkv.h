@@ -576,9 +576,18 @@ int pkv_paged_decode_attn_q4(void* out, const void* q, const void* k_cache, cons
                              pkv_stream_t stream);
 
 /*
+ * pkv_paged_short_chunk_workspace_bytes for paged_varlen_prefill_attn_q4, whose
+ * short chunks run on the decode kernel with head_dim 64 too.
+ */
+size_t pkv_paged_short_chunk_q4_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                                int32_t num_kv_heads, int32_t head_dim,
+                                                int32_t max_seqlen_q, int32_t max_seqlen_k);
+
+/*
  * paged_varlen_prefill_attn_q4: pkv_paged_varlen_prefill_attn_fp8 over a 4-bit
  * cache; the new rows are stored first (pkv_kv_store_q4, pkv_kv_rope_store).
- * Arguments, range checks, workspace and its size functions are the E4M3 call's.
+ * Arguments, range checks and the workspace are the E4M3 call's (short chunks:
+ * pkv_paged_short_chunk_q4_workspace_bytes).
  * Supported: head_dim 64 or 128; G in {1, 2, 4, 8}; every block size.
  */
 int pkv_paged_varlen_prefill_attn_q4(void* out, const void* q, const void* k_cache, const void* v_cache,

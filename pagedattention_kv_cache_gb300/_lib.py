@@ -81,6 +81,7 @@ SIGNATURES = [
     ("pkv_kv_load_q4", ctypes.c_int, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P]),
     ("pkv_paged_decode_attn_q4", ctypes.c_int,
      [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _F, _F, _I, _P, _S, _P]),
+    ("pkv_paged_short_chunk_q4_workspace_bytes", _S, [_I, _I, _I, _I, _I, _I]),
     ("pkv_paged_varlen_prefill_attn_q4", ctypes.c_int,
      [_P, _P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _F, _F, _I, _P, _S, _P]),
 ]

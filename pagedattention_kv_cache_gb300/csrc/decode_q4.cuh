@@ -1,0 +1,494 @@
+// paged_decode_q4_kernel: decode, and chunks of at most 8 rows per KV head
+// (kVar), over the 4-bit cache of q4.cuh.  The CTA plan, split and merge are
+// decode_plan.cuh's.
+//
+// Bound: HBM, each token's K and V row once (576 bytes each with 8 KV heads of
+// 128).  At 4.5 bits an element the bytes leave about three issued instructions
+// per element of a lane, so what the kernel is built around is a short way from
+// codes to matrix operands:
+//  * A word of eight codes becomes four f16 pairs with two shifts, four
+//    and-ors and four fmas: a nibble in mantissa bits 9..6 under the exponent of
+//    16 is the number 16 + n, in bits 5..2 under the exponent of 256 it is
+//    256 + n, and x s - 24 s (or - 264 s) is (n - 8) s.  s is the group's scale
+//    over 4 (so that 264 s stays below f16's end); every step is exact, since
+//    (n - 8) s has 7 significant bits and 264 s at most 10.  (The conversion
+//    instructions of the FP8 kernel run at 16 results per clock and SM, which
+//    alone would take longer than the bytes.)
+//  * S^T = K Q^T: the 16 keys of a chunk in the M dimension and the R <= 8 rows
+//    in N, so one m16n8k16 per 16 elements of head_dim wastes only the rows past
+//    R.  A lane takes a whole quarter of its two keys' head rows (16 bytes each at
+//    head_dim 128); q's fragments are laid out to match.
+//  * O^T += V^T P^T: P^T's fragment is the transpose of S^T's, one movmatrix per
+//    eight keys.  A lane takes 16 (head_dim 64: 8) consecutive elements of four keys:
+//    one scale each.
+//  * Both products see the softmax rows in the columns of their accumulators, so a
+//    lane owns the state of rows 2c and 2c + 1 and rescaling needs no exchange.  The
+//    row maximum is a reference only: it moves when a score passes it by 2^8
+//    (a vote per chunk), so the usual chunk takes no maximum across lanes.
+//  * Which token stands in which fragment row is free as long as K and V agree;
+//    token_of spreads the rows over the banks.
+// q enters as f16 after a power-of-two scaling of each row (as in the FP8 kernel);
+// weights as f16 times 2^7, so that they count down to 2^-31 of the row's largest.
+#pragma once
+
+#include "decode_plan.cuh"
+#include "q4.cuh"
+
+namespace {
+
+constexpr int kQ4Warps = 16;  // consumer warps (at most): one per (KV head, token phase)
+constexpr int kQ4Stages = 6;  // at most
+constexpr int kQ4Smem = 224 * 1024;
+constexpr int kQ4Chunk = 16;  // keys per consumer warp and stage
+
+// d (16x8 fp32) += a (16x16 f16, row) * b (16x8 f16, col)
+__device__ __forceinline__ void mma_q4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Transposes an 8x8 matrix of 16-bit elements spread over the warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// acc + the f16 in the low (high) half of h
+__device__ __forceinline__ void add_halves(uint32_t h, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 a, b, one;\n\tmov.b32 {a, b}, %2;\n\tmov.b16 one, 0x3c00;\n\t"
+      "fma.rn.f32.f16 %0, a, one, %0;\n\tfma.rn.f32.f16 %1, b, one, %1;\n\t}"
+      : "+f"(lo), "+f"(hi)
+      : "r"(h));
+}
+
+// A scale pair (s, -24 s, -264 s), each over 4.
+struct Q4Scale {
+  uint32_t s, low, high;
+  __device__ __forceinline__ explicit Q4Scale(uint32_t quarter)
+      : s(quarter), low(hmul2(quarter, 0xce00ce00u)), high(hmul2(quarter, 0xdc20dc20u)) {}
+};
+// The four f16 pairs of a word: nibbles (0, 4), (1, 5), (2, 6) and (3, 7), as (n - 8) times the scale pair.
+__device__ __forceinline__ void widen_q4(uint32_t w, const Q4Scale& k, uint32_t (&f)[4]) {
+  const uint32_t y0 = w << 2, y1 = w >> 6;
+  f[0] = hfma2((y0 & 0x003c003cu) | 0x5c005c00u, k.s, k.high);
+  f[1] = hfma2((y0 & 0x03c003c0u) | 0x4c004c00u, k.s, k.low);
+  f[2] = hfma2((y1 & 0x003c003cu) | 0x5c005c00u, k.s, k.high);
+  f[3] = hfma2((y1 & 0x03c003c0u) | 0x4c004c00u, k.s, k.low);
+}
+
+// The token (of eight) that stands in fragment row i: rows i and i + 1, which one
+// 16-byte load phase reads, differ in parity, and so do rows 0, 2, 4, 6 from one
+// to the next, which V's loads take together (two rows of 8 heads of 128, 576
+// bytes each, are 64 bytes apart modulo 128).
+__device__ __forceinline__ int token_of(int i) { return i & 1 ? 4 + ((i >> 1) ^ 1) : i >> 1; }
+
+template <int G, int QL, int D, bool kVar>
+__global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel(const Params p) {
+  pkv::pdl_enter();
+  {
+    // warm L2 with small block tables while the plan reads the lengths
+    const size_t lines = (static_cast<size_t>(p.batch) * p.max_blocks * 4 + 127) / 128;
+    if (lines <= 512) {
+      const char* tb = reinterpret_cast<const char*>(p.block_tables);
+      for (size_t i = threadIdx.x; i < lines; i += blockDim.x)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(tb + i * 128) : "memory");
+    }
+  }
+  using T = __nv_bfloat16;
+  constexpr int R = G * QL;
+  static_assert(R <= 8, "at most 8 rows per KV head");
+  constexpr int NW = D / 32;   // code words of a lane's quarter of a key
+  constexpr int NO = D / 16;   // m-tiles of O^T
+  constexpr float kRescale = 8.0f;
+  constexpr float kWeightLog2 = 7.0f;
+  const int rows_per_seq = QL * p.hq;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int tid = threadIdx.x;
+  const int warp = tid / 32;
+  const int lane = tid % 32;
+  const int nw = p.nw;
+  const int row_bytes = pkv::q4_row_bytes(p.hkv, D);
+  unsigned char* stage_base = smem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stage_base + p.stages * p.stage_bytes);
+  uint64_t* empty = full + kQ4Stages;
+  long long* sh = reinterpret_cast<long long*>(empty + kQ4Stages);
+  int* sh_flag = reinterpret_cast<int*>(sh + 64);
+  float* merge = reinterpret_cast<float*>(sh_flag + 32);  // records of the phases past the first
+  volatile int* abort_flag = sh_flag + 1;
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < p.stages; ++s) {
+      pkv::mbar_init(&full[s], 1);
+      pkv::mbar_init(&empty[s], nw);
+    }
+    pkv::fence_mbar_init();
+  }
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    if (covered_len<true, kVar>(p, b) != 0) continue;
+    int first = b * rows_per_seq, count = rows_per_seq;
+    if constexpr (kVar) {
+      if (seq_len<kVar>(p, b) == 0) continue;  // no rows, or skipped
+      first = __ldg(p.cu_q + b) * p.hq;
+      count = (__ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b)) * p.hq;
+    }
+    T* o = static_cast<T*>(p.out) + static_cast<size_t>(first) * D;
+    for (int i = tid; i < count * D; i += blockDim.x) o[i] = static_cast<T>(0.0f);
+  }
+  Plan plan;
+  if (p.num_splits > 0) {
+    plan_fixed<true>(p, plan);
+    __syncthreads();
+  } else {
+    plan_auto<true, kVar>(p, plan, sh);
+  }
+
+  if (warp == nw) {
+    // ------------------------------------------------------------ producer
+    // A stage's tokens are contiguous runs of rows, one per block: a copy of K and
+    // one of V per run, a run per lane.
+    const uint64_t policy = pkv::l2_evict_first_policy();
+    int it = 0;
+    for_each_segment<true, kVar>(p, plan, [&](const Segment& seg) -> bool {
+      const int32_t* table = p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks;
+      for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
+        const int s = it % p.stages;
+        const uint32_t use = it / p.stages;
+        const int end = min(t + p.t_stage, seg.t1);
+        const int last = (end - 1) / p.block_size;
+        const int first = t / p.block_size + lane;
+        int phys = first <= last ? __ldg(table + first) : 0;
+        if (lane == 0 && use > 0) wait_or_abort(&empty[s], (use & 1u) ^ 1u, abort_flag, p.err);
+        __syncwarp();
+        for (int blk = first; blk <= last; blk += 32) {
+          if (blk != first) phys = __ldg(table + blk);
+          if (phys < 0 || phys >= p.num_blocks) {
+            pkv::raise_error(p.err, PKV_DERR_BLOCK_RANGE);
+            continue;
+          }
+          const int a = max(t, blk * p.block_size);
+          const uint32_t bytes = static_cast<uint32_t>(min(end - a, (blk + 1) * p.block_size - a)) * row_bytes;
+          const size_t src =
+              (static_cast<size_t>(phys) * p.block_size + (a - blk * p.block_size)) * static_cast<size_t>(row_bytes);
+          unsigned char* dst = stage_base + s * p.stage_bytes + (a - t) * row_bytes;
+          pkv::mbar_expect_tx(&full[s], 2 * bytes);
+          pkv::bulk_g2s(dst, p.k_cache + src, bytes, &full[s], policy);
+          pkv::bulk_g2s(dst + p.stage_bytes / 2, p.v_cache + src, bytes, &full[s], policy);
+        }
+        __syncwarp();
+        if (lane == 0) pkv::mbar_arrive(&full[s]);
+      }
+      return true;
+    });
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = warp % p.hkv;
+  const int phase = warp / p.hkv;
+  const int r0 = lane >> 2;  // fragment rows r0 and r0 + 8 (keys of S^T, elements of O^T); column r0 of B operands
+  const int c = lane & 3;
+  const int nthreads_c = nw * 32;
+  const int tw0 = phase * kQ4Chunk;  // this warp's keys of a stage
+  // offsets in a stage of what this lane reads: two keys' quarter and scales, four V rows' elements and scales
+  const int scales = pkv::q4_scale_offset(p.hkv, D) + g * (D / 16);
+  const int k_at = (tw0 + token_of(r0)) * row_bytes;
+  const int k_codes = k_at + g * (D / 2) + c * (D / 8);
+  const int k_scales = k_at + scales + c * (D / 64);
+  const int va = token_of(2 * c), vb = token_of(2 * c + 1);
+  const int v_a = (tw0 + va) * row_bytes, v_b = (tw0 + vb) * row_bytes;
+  const int v_codes = g * (D / 2) + r0 * (D / 16);
+  const int v_scales = scales + (D == 128 ? r0 : r0 >> 1);
+  const int half = 8 * row_bytes;  // from fragment rows r0 to r0 + 8
+  int it = 0;
+
+  for_each_segment<true, kVar>(p, plan, [&](const Segment& seg) -> bool {
+    // Q as the B operand: column r0, and for word w of this lane's quarter the pairs (0, 4), (1, 5), (2, 6), (3, 7)
+    uint32_t qf[NW][4];
+    float mul[2];  // of rows 2c and 2c + 1: the power that scaled q comes off with the scale (and K's 1/4)
+    {
+      const bool row_here = kVar ? r0 / G < seg.nq && r0 < R : r0 < R;
+      const size_t row = kVar ? static_cast<size_t>(seg.q0) + r0 / G : static_cast<size_t>(seg.b) * QL + r0 / G;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (row * p.hq + g * G + r0 % G) * D +
+                                                        c * (D / 4));
+      float f[NW][8];
+      float amax = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const uint4 x = row_here ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+        Chunk<T>::unpack(x, f[w]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[w][i]));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int ex = amax > 0.f ? min(max(14 - ilogbf(amax), -113), 126) : 0;
+      const float up = ldexpf(1.f, ex);
+      const float down = p.scale_log2 * 4.f * ldexpf(1.f, -ex);
+      mul[0] = __shfl_sync(0xffffffffu, down, 8 * c);
+      mul[1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[w][i] = pkv::pack_f16x2(f[w][i] * up, f[w][i + 4] * up);
+    }
+    int lim[2] = {seg.ctx - 1, seg.ctx - 1};  // the last key that rows 2c and 2c + 1 see
+    if constexpr (kVar) {
+      if (p.causal)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) lim[i] = seg.ctx - seg.nq + (2 * c + i) / G;
+    }
+    float o[NO][4];
+#pragma unroll
+    for (int j = 0; j < NO; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY};
+    float l[2] = {0.f, 0.f};
+
+    for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
+      const int s = it % p.stages;
+      const uint32_t use = it / p.stages;
+      wait_or_abort(&full[s], use & 1u, abort_flag, p.err);
+      const int nv = min(seg.t1 - t - tw0, kQ4Chunk);  // keys of this chunk
+      if (nv > 0) {
+        const unsigned char* ks = stage_base + s * p.stage_bytes;
+        const unsigned char* vs = ks + p.stage_bytes / 2;
+        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+        {
+          uint32_t wx[NW], wy[NW], sx, sy;  // keys r0 and r0 + 8
+          if constexpr (D == 128) {
+            const uint4 x = pkv::lds128(ks + k_codes), y = pkv::lds128(ks + k_codes + half);
+            wx[0] = x.x, wx[1] = x.y, wx[2] = x.z, wx[3] = x.w;
+            wy[0] = y.x, wy[1] = y.y, wy[2] = y.z, wy[3] = y.w;
+            sx = *reinterpret_cast<const uint16_t*>(ks + k_scales);
+            sy = *reinterpret_cast<const uint16_t*>(ks + k_scales + half);
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(ks + k_codes);
+            const uint2 y = *reinterpret_cast<const uint2*>(ks + k_codes + half);
+            wx[0] = x.x, wx[1] = x.y, wy[0] = y.x, wy[1] = y.y;
+            sx = ks[k_scales];
+            sy = ks[k_scales + half];
+          }
+          // (s, s') of the quarter's groups, over 4
+          const uint32_t hx = hmul2(pkv::e4m3x2_to_f16x2(sx), 0x34003400u);
+          const uint32_t hy = hmul2(pkv::e4m3x2_to_f16x2(sy), 0x34003400u);
+#pragma unroll
+          for (int grp = 0; grp < NW / 2; ++grp) {
+            const Q4Scale kx(pkv::prmt(hx, 0, grp ? 0x3232u : 0x1010u)), ky(pkv::prmt(hy, 0, grp ? 0x3232u : 0x1010u));
+#pragma unroll
+            for (int w = 2 * grp; w < 2 * grp + 2; ++w) {
+              uint32_t fx[4], fy[4];
+              widen_q4(wx[w], kx, fx);
+              widen_q4(wy[w], ky, fy);
+              mma_q4(sa, fx[0], fy[0], fx[1], fy[1], qf[w][0], qf[w][1]);
+              mma_q4(sb, fx[2], fy[2], fx[3], fy[3], qf[w][2], qf[w][3]);
+            }
+          }
+        }
+        // scores of keys r0 (e = 0, 1) and r0 + 8 (2, 3) for rows 2c and 2c + 1
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = (sa[e] + sb[e]) * mul[e & 1];
+        const int key0 = t + tw0 + token_of(r0);
+        if (nv < kQ4Chunk || (kVar && t + tw0 + kQ4Chunk > seg.ctx - seg.nq)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + (e >= 2 ? 8 : 0);
+            if (key >= seg.t1 || key > lim[e & 1]) x[e] = -INFINITY;
+          }
+        }
+        const float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+        if (__any_sync(0xffffffffu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale ||
+                                        (m[0] == -INFINITY && top[0] != -INFINITY) ||
+                                        (m[1] == -INFINITY && top[1] != -INFINITY))) {
+          // (a row moves by its own scores only)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = top[i];
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            if (mx > m[i] + kRescale || (m[i] == -INFINITY && mx != -INFINITY)) {
+              const float corr = m[i] == -INFINITY ? 0.f : pkv::ex2(m[i] - mx);
+              m[i] = mx;
+              l[i] *= corr;
+#pragma unroll
+              for (int j = 0; j < NO; ++j) {
+                o[j][i] *= corr;
+                o[j][2 + i] *= corr;
+              }
+            }
+          }
+        }
+        const float base[2] = {m[0] == -INFINITY ? 0.f : m[0] - kWeightLog2, m[1] == -INFINITY ? 0.f : m[1] - kWeightLog2};
+        uint32_t pf[2];  // weights of keys r0 and r0 + 8, then of this lane's V rows
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          pf[i] = pkv::pack_f16x2(pkv::ex2(x[2 * i] - base[0]), pkv::ex2(x[2 * i + 1] - base[1]));
+          add_halves(pf[i], l[0], l[1]);
+          pf[i] = movmatrix(pf[i]);
+        }
+        uint32_t s_ab = vs[v_a + v_scales] | vs[v_b + v_scales] << 8;
+        uint32_t s_cd = vs[v_a + half + v_scales] | vs[v_b + half + v_scales] << 8;
+        if (nv < kQ4Chunk) {  // rows past the last key hold anything: scale 0 makes their values 0
+          s_ab &= (va < nv ? 0x00ffu : 0u) | (vb < nv ? 0xff00u : 0u);
+          s_cd &= (va + 8 < nv ? 0x00ffu : 0u) | (vb + 8 < nv ? 0xff00u : 0u);
+        }
+        const Q4Scale kab(hmul2(pkv::e4m3x2_to_f16x2(s_ab), 0x34003400u));
+        const Q4Scale kcd(hmul2(pkv::e4m3x2_to_f16x2(s_cd), 0x34003400u));
+        uint32_t wv[4][NW / 2];
+        const int v_off[4] = {v_a, v_b, v_a + half, v_b + half};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if constexpr (D == 128) {
+            const uint2 z = *reinterpret_cast<const uint2*>(vs + v_off[u] + v_codes);
+            wv[u][0] = z.x, wv[u][1] = z.y;
+          } else {
+            wv[u][0] = *reinterpret_cast<const uint32_t*>(vs + v_off[u] + v_codes);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < NW / 2; ++w)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // four elements of keys (2c, 2c + 1) and of (2c + 8, 2c + 9), a pair of keys per word
+            uint32_t fab[4], fcd[4];
+            widen_q4(pkv::prmt(wv[0][w], wv[1][w], h ? 0x7632u : 0x5410u), kab, fab);
+            widen_q4(pkv::prmt(wv[2][w], wv[3][w], h ? 0x7632u : 0x5410u), kcd, fcd);
+            const int tm = 4 * w + 2 * h;
+            mma_q4(o[tm], fab[0], fab[1], fcd[0], fcd[1], pf[0], pf[1]);
+            mma_q4(o[tm + 1], fab[2], fab[3], fcd[2], fcd[3], pf[0], pf[1]);
+          }
+      }
+      __syncwarp();
+      if (lane == 0) pkv::mbar_arrive(&empty[s]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+
+    // accumulator (tm, i) is element d0 + 2 tm of row 2c + i, (tm, 2 + i) the next one
+    const int d0 = r0 * (D / 8);
+    if (p.wph > 1) {
+      // merge the warps that share KV head g
+      constexpr int rec = D + 2;
+      float* mine = merge + static_cast<size_t>(warp - p.hkv) * R * rec;
+      if (phase > 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 2 * c + i;
+          if (row >= R) continue;
+#pragma unroll
+          for (int tm = 0; tm < NO; ++tm)
+            *reinterpret_cast<float2*>(mine + row * rec + d0 + 2 * tm) = make_float2(o[tm][i], o[tm][2 + i]);
+          if (r0 == 0) *reinterpret_cast<float2*>(mine + row * rec + D) = make_float2(m[i], l[i]);
+        }
+      }
+      pkv::named_barrier_sync(1, nthreads_c);
+      if (phase == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 2 * c + i;
+          if (row >= R) continue;
+          float mm = m[i];
+          for (int ph = 1; ph < p.wph; ++ph)
+            mm = fmaxf(mm, merge[(static_cast<size_t>((ph - 1) * p.hkv + g) * R + row) * rec + D]);
+          const float w0 = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mm);
+          float ll = l[i] * w0;
+#pragma unroll
+          for (int tm = 0; tm < NO; ++tm) {
+            o[tm][i] *= w0;
+            o[tm][2 + i] *= w0;
+          }
+          for (int ph = 1; ph < p.wph; ++ph) {
+            const float* src = merge + (static_cast<size_t>((ph - 1) * p.hkv + g) * R + row) * rec;
+            const float w = src[D] == -INFINITY ? 0.f : exp2f(src[D] - mm);
+            ll += w * src[D + 1];
+#pragma unroll
+            for (int tm = 0; tm < NO; ++tm) {
+              const float2 v = *reinterpret_cast<const float2*>(src + d0 + 2 * tm);
+              o[tm][i] = fmaf(w, v.x, o[tm][i]);
+              o[tm][2 + i] = fmaf(w, v.y, o[tm][2 + i]);
+            }
+          }
+          m[i] = mm;
+          l[i] = ll;
+        }
+      }
+      pkv::named_barrier_sync(1, nthreads_c);
+    }
+    // the result (whole sequence) or this part's state; V's scale comes off here (the weights' 2^7 cancels against l)
+    if (phase == 0) {
+      const float vscale = p.v_scale * 4.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = 2 * c + i;
+        if (row >= R || (kVar && row / G >= seg.nq)) continue;
+        const int head = (row / G) * p.hq + g * G + row % G;
+        if (seg.nparts == 1) {
+          const float inv = l[i] == 0.f ? 0.f : vscale / l[i];  // kVar: a row may see nothing
+          T* orow = static_cast<T*>(p.out) + ((kVar ? static_cast<size_t>(seg.q0) * p.hq
+                                                    : static_cast<size_t>(seg.b) * rows_per_seq) + head) * D + d0;
+          uint32_t w[NO];
+#pragma unroll
+          for (int tm = 0; tm < NO; ++tm) w[tm] = pkv::pack_bf16x2(o[tm][i] * inv, o[tm][2 + i] * inv);
+#pragma unroll
+          for (int u = 0; u < NO / 4; ++u)
+            reinterpret_cast<uint4*>(orow)[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+        } else {
+          float* po = p.part_o + (static_cast<size_t>(seg.slot) * rows_per_seq + head) * D + d0;
+#pragma unroll
+          for (int u = 0; u < NO / 2; ++u)
+            reinterpret_cast<float4*>(po)[u] = make_float4(o[2 * u][i] * vscale, o[2 * u][2 + i] * vscale,
+                                                           o[2 * u + 1][i] * vscale, o[2 * u + 1][2 + i] * vscale);
+          if (r0 == 0)
+            *reinterpret_cast<float2*>(p.part_ml + (static_cast<size_t>(seg.slot) * rows_per_seq + head) * 2) =
+                make_float2(m[i], l[i]);
+        }
+      }
+    }
+    if (seg.nparts > 1) combine_if_last<T, D, true, kVar>(p, seg, rows_per_seq, sh_flag, nthreads_c);
+    return true;
+  });
+}
+
+// ------------------------------------------------------------------ host side
+
+template <int G, int QL, int D, bool kVar>
+int launch_q4(Params& p, int sms, cudaStream_t stream) {
+  constexpr int R = G * QL;
+  const int row = pkv::q4_row_bytes(p.hkv, D);
+  p.wph = kQ4Warps / p.hkv;
+  p.nw = p.hkv * p.wph;
+  p.t_stage = kQ4Chunk * p.wph;
+  p.stage_bytes = static_cast<size_t>(p.t_stage) * row * 2;
+  p.align = 1;
+  const size_t misc = 2 * kQ4Stages * sizeof(uint64_t) + 64 * sizeof(long long) + 32 * sizeof(int) +
+                      static_cast<size_t>(p.nw - p.hkv) * R * (D + 2) * sizeof(float);
+  p.stages = std::min<int>(kQ4Stages, static_cast<int>((kQ4Smem - misc) / p.stage_bytes));
+  if (p.stages < 2) return PKV_EUNSUPPORTED;
+  auto kernel = paged_decode_q4_kernel<G, QL, D, kVar>;
+  static std::atomic<uint64_t> smem_allowed{0};  // the limit for every number of KV heads
+  if (pkv::allow_smem(kernel, kQ4Smem, smem_allowed) != cudaSuccess) return PKV_ECUDA;
+  const unsigned grid = p.num_splits > 0 ? static_cast<unsigned>(static_cast<long long>(p.batch) * p.num_splits)
+                                         : static_cast<unsigned>(sms * kAutoCtasPerSm);
+  if (grid == 0) return PKV_OK;
+  return pkv::launch_pdl(kernel, dim3(grid), dim3((p.nw + 1) * 32), p.stages * p.stage_bytes + misc, stream, p) ==
+                 cudaSuccess
+             ? PKV_OK
+             : PKV_ECUDA;
+}
+
+}  // namespace

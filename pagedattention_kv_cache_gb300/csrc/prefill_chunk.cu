@@ -62,9 +62,10 @@ int check_args(const PrefillArgs& a, int max_seqlen_k) {
 // x 16 sequences after 512 keys 20.7 / 13.7 (bf16 20.1 / 12.2), after 1024 22.9 / 19.2
 // (24.0 / 17.1), bf16 after 2048 30.9 / 27.9 and after 8192 89.0 / 87.2; 2 KV heads,
 // G = 4, 1 token x 64 after 2048 bf16 30.9 / 27.9 (E4M3 23.4 / 30.1).
-bool short_chunk(int batch, int group, int num_kv_heads, int head_dim, int max_seqlen_q, int max_seqlen_k) {
+bool short_chunk(int batch, int group, int num_kv_heads, int head_dim, int max_seqlen_q, int max_seqlen_k,
+                 bool q4 = false) {
   const long long rows = static_cast<long long>(max_seqlen_q) * group;
-  if (head_dim != 128 || num_kv_heads > 8 || rows > 8) return false;
+  if ((head_dim != 128 && !q4) || num_kv_heads > 8 || rows > 8) return false;
   pkv::DeviceInfo info;
   if (pkv::device_info(&info) != PKV_OK) return false;
   const bool one_wave = static_cast<long long>(batch) * num_kv_heads <= info.sms;
@@ -73,10 +74,25 @@ bool short_chunk(int batch, int group, int num_kv_heads, int head_dim, int max_s
 
 // The decode kernel runs a short chunk when its workspace is there, else the
 // tcgen05 kernel does.
-bool on_decode_kernel(const PrefillArgs& a, int max_seqlen_k) {
-  if (!a.block_tables || !short_chunk(a.batch, a.group, a.hkv, a.head_dim, a.max_seqlen_q, max_seqlen_k)) return false;
+bool on_decode_kernel(const PrefillArgs& a, int max_seqlen_k, bool q4 = false) {
+  if (!a.block_tables || !short_chunk(a.batch, a.group, a.hkv, a.head_dim, a.max_seqlen_q, max_seqlen_k, q4)) return false;
   const size_t need = pkv::chunk_decode_workspace_bytes(a.batch, a.hkv, a.head_dim);
   return need > 0 && a.workspace && a.workspace_bytes >= need;
+}
+
+}  // namespace
+
+namespace {
+
+size_t short_chunk_workspace(int batch, int num_q_heads, int num_kv_heads, int head_dim, int max_seqlen_q,
+                             int max_seqlen_k, bool q4) {
+  if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_seqlen_q <= 0)
+    return 0;
+  const int group = num_q_heads / num_kv_heads;
+  if ((group != 1 && group != 2 && group != 4 && group != 8) ||
+      !short_chunk(batch, group, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k, q4))
+    return 0;
+  return pkv::chunk_decode_workspace_bytes(batch, num_kv_heads, head_dim);
 }
 
 }  // namespace
@@ -84,13 +100,14 @@ bool on_decode_kernel(const PrefillArgs& a, int max_seqlen_k) {
 extern "C" size_t pkv_paged_short_chunk_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                         int32_t head_dim, int32_t max_seqlen_q,
                                                         int32_t max_seqlen_k) {
-  if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_seqlen_q <= 0)
-    return 0;
-  const int group = num_q_heads / num_kv_heads;
-  if ((group != 1 && group != 2 && group != 4 && group != 8) ||
-      !short_chunk(batch, group, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k))
-    return 0;
-  return pkv::chunk_decode_workspace_bytes(batch, num_kv_heads, head_dim);
+  return short_chunk_workspace(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k, false);
+}
+
+extern "C" size_t pkv_paged_short_chunk_q4_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                           int32_t head_dim, int32_t max_seqlen_q,
+                                                           int32_t max_seqlen_k) {
+  if (head_dim != 64 && head_dim != 128) return 0;
+  return short_chunk_workspace(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k, true);
 }
 
 extern "C" int pkv_paged_varlen_prefill_attn_mod(
@@ -217,5 +234,6 @@ extern "C" int pkv_paged_varlen_prefill_attn_q4(void* out, const void* q, const 
                                  block_tables, max_blocks_per_seq, batch, total_q, num_q_heads, num_kv_heads, head_dim,
                                  block_size, num_blocks, scale, k_scale, v_scale, causal, workspace, workspace_bytes);
   if (chk != PKV_OK) return chk > 0 ? PKV_OK : chk;
+  if (on_decode_kernel(a, max_seqlen_k, true)) return pkv::chunk_decode_q4_launch(a, stream);
   return pkv::chunk_q4_launch(a, stream);
 }

@@ -384,26 +384,28 @@ def _decode_workspace_args(workspace, batch: int, hq: int, d: int, num_splits: i
 
 def chunk_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int,
                           max_seqlen_k: int) -> int:
-    """Bytes of the workspace with which paged_varlen_prefill_attn_mod and _fp8 split these sizes (0: never)."""
-    short = int(_lib.load().pkv_paged_short_chunk_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim,
-                                                                  max_seqlen_q, max_seqlen_k))
+    """Bytes of the workspace with which paged_varlen_prefill_attn_mod, _fp8 and _q4 split these sizes (0: never)."""
+    lib = _lib.load()
+    short = max(int(size(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k))
+                for size in (lib.pkv_paged_short_chunk_workspace_bytes, lib.pkv_paged_short_chunk_q4_workspace_bytes))
     return max(short, prefill_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q))
 
 
 def chunk_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int,
                     max_seqlen_k: int, device=None) -> torch.Tensor | None:
-    """A zero-filled workspace (uint8) for paged_varlen_prefill_attn_mod and _fp8, or None when none is needed."""
+    """A zero-filled workspace (uint8) for paged_varlen_prefill_attn_mod, _fp8 and _q4, or None when none is needed."""
     n = chunk_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k)
     if n == 0:
         return None
     return torch.zeros(n, dtype=torch.uint8, device=device or torch.cuda.current_device())
 
 
-def _chunk_workspace_args(workspace, batch: int, hq: int, hkv: int, d: int, max_q: int, max_k: int, paged: bool, device):
+def _chunk_workspace_args(workspace, batch: int, hq: int, hkv: int, d: int, max_q: int, max_k: int, paged: bool, device,
+                          short_bytes: str = "pkv_paged_short_chunk_workspace_bytes"):
     """The workspace of a chunk call: the caller's if it is large enough for a short chunk, else one for this call."""
     short = 0
     if paged and max_q * hq <= 8 * hkv:
-        short = int(_lib.load().pkv_paged_short_chunk_workspace_bytes(batch, hq, hkv, d, max_q, max_k))
+        short = int(getattr(_lib.load(), short_bytes)(batch, hq, hkv, d, max_q, max_k))
     if short > 0 and (workspace is None or workspace is False or workspace.numel() * workspace.element_size() < short):
         return _workspace_args(None, short, batch, device)
     return _workspace_args(workspace, prefill_workspace_bytes(batch, hq, hkv, d, max_q) if workspace is None else 0,
@@ -749,7 +751,8 @@ def paged_varlen_prefill_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache
         raise ValueError("block_tables rows must equal the batch")
     handle = _stream(stream, dev)
     out, workspace, ws_ptr, ws_bytes = _buffers(stream, q, out, _chunk_workspace_args, workspace, B, hq, num_kv_heads, d,
-                                                int(max_seqlen_q), int(max_seqlen_k), True, dev)
+                                                int(max_seqlen_q), int(max_seqlen_k), True, dev,
+                                                "pkv_paged_short_chunk_q4_workspace_bytes")
     st = _lib.load().pkv_paged_varlen_prefill_attn_q4(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(max_seqlen_q),
         int(max_seqlen_k), _ptr(block_tables), block_tables.shape[1], B, total_q, hq, num_kv_heads, d, bs, nb, scale,

@@ -165,6 +165,8 @@ def test_decode_repeats_and_shares_its_workspace():
         decode_case(20 + seed, [5000, 3], 16, 2, 4, 64, workspace=ws)
         assert torch.equal(first, pkv.paged_decode_attn_q4(q, kp, vp, bt, cl, 0.1, T_K, T_V, 4, workspace=ws))
     assert torch.equal(first, pkv.paged_decode_attn_q4(q, kp, vp, bt, cl, 0.1, T_K, T_V, 4))
+    with pytest.raises(_lib.PagedKVError):
+        pkv.paged_decode_attn_q4(q, kp, vp, bt, cl, 0.1, T_K, T_V, 4, workspace=ws[:256])
 
 
 def chunk_case(seed, history, new, bs, hkv, g, d, causal=True, workspace=None, q_scale=1.0, scale=None):
