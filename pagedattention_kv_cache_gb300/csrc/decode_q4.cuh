@@ -7,13 +7,12 @@
 // per element of a lane, so what the kernel is built around is a short way from
 // codes to matrix operands:
 //  * A word of eight codes becomes four f16 pairs with two shifts, four
-//    and-ors and four fmas: a nibble in mantissa bits 9..6 under the exponent of
-//    16 is the number 16 + n, in bits 5..2 under the exponent of 256 it is
-//    256 + n, and x s - 24 s (or - 264 s) is (n - 8) s.  s is the group's scale
-//    over 4 (so that 264 s stays below f16's end); every step is exact, since
-//    (n - 8) s has 7 significant bits and 264 s at most 10.  (The conversion
-//    instructions of the FP8 kernel run at 16 results per clock and SM, which
-//    alone would take longer than the bytes.)
+//    and-ors and four fmas: a nibble n in mantissa bits 9..6 under the exponent of
+//    4 is the number 4 + n / 4, in bits 5..2 under the exponent of 64 it is
+//    64 + n / 4, and x s - 6 s (or - 66 s) is (n - 8) s / 4.  Every step is exact:
+//    (n - 8) s has 7 significant bits, 66 s at most 9 and stays below f16's end.
+//    (The conversion instructions of the FP8 kernel run at 16 results per clock
+//    and SM, which alone would take longer than the bytes.)
 //  * S^T = K Q^T: the 16 keys of a chunk in the M dimension and the R <= 8 rows
 //    in N, so one m16n8k16 per 16 elements of head_dim wastes only the rows past
 //    R.  A lane takes a whole quarter of its two keys' head rows (16 bytes each at
@@ -36,10 +35,11 @@
 
 namespace {
 
-constexpr int kQ4Warps = 16;  // consumer warps (at most): one per (KV head, token phase)
+constexpr int kQ4Warps = 8;   // consumer warps (at most): one per (KV head, token phase)
 constexpr int kQ4Stages = 6;  // at most
 constexpr int kQ4Smem = 224 * 1024;
-constexpr int kQ4Chunk = 16;  // keys per consumer warp and stage
+constexpr int kQ4Sub = 4;     // chunks of 16 keys per consumer warp and stage: their products overlap
+constexpr int kQ4Chunk = 16 * kQ4Sub;
 
 // d (16x8 fp32) += a (16x16 f16, row) * b (16x8 f16, col)
 __device__ __forceinline__ void mma_q4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -48,16 +48,6 @@ __device__ __forceinline__ void mma_q4(float (&d)[4], uint32_t a0, uint32_t a1, 
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
 }
 // Transposes an 8x8 matrix of 16-bit elements spread over the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -71,21 +61,6 @@ __device__ __forceinline__ void add_halves(uint32_t h, float& lo, float& hi) {
       "fma.rn.f32.f16 %0, a, one, %0;\n\tfma.rn.f32.f16 %1, b, one, %1;\n\t}"
       : "+f"(lo), "+f"(hi)
       : "r"(h));
-}
-
-// A scale pair (s, -24 s, -264 s), each over 4.
-struct Q4Scale {
-  uint32_t s, low, high;
-  __device__ __forceinline__ explicit Q4Scale(uint32_t quarter)
-      : s(quarter), low(hmul2(quarter, 0xce00ce00u)), high(hmul2(quarter, 0xdc20dc20u)) {}
-};
-// The four f16 pairs of a word: nibbles (0, 4), (1, 5), (2, 6) and (3, 7), as (n - 8) times the scale pair.
-__device__ __forceinline__ void widen_q4(uint32_t w, const Q4Scale& k, uint32_t (&f)[4]) {
-  const uint32_t y0 = w << 2, y1 = w >> 6;
-  f[0] = hfma2((y0 & 0x003c003cu) | 0x5c005c00u, k.s, k.high);
-  f[1] = hfma2((y0 & 0x03c003c0u) | 0x4c004c00u, k.s, k.low);
-  f[2] = hfma2((y1 & 0x003c003cu) | 0x5c005c00u, k.s, k.high);
-  f[3] = hfma2((y1 & 0x03c003c0u) | 0x4c004c00u, k.s, k.low);
 }
 
 // The token (of eight) that stands in fragment row i: rows i and i + 1, which one
@@ -159,17 +134,16 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
     // A stage's tokens are contiguous runs of rows, one per block: a copy of K and
     // one of V per run, a run per lane.
     const uint64_t policy = pkv::l2_evict_first_policy();
-    int it = 0;
+    int s = 0;
+    uint32_t parity = 1;  // (a ring's first pass finds every stage free)
     for_each_segment<true, kVar>(p, plan, [&](const Segment& seg) -> bool {
       const int32_t* table = p.block_tables + static_cast<size_t>(seg.b) * p.max_blocks;
-      for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
-        const int s = it % p.stages;
-        const uint32_t use = it / p.stages;
+      for (int t = seg.t0; t < seg.t1; t += p.t_stage) {
         const int end = min(t + p.t_stage, seg.t1);
         const int last = (end - 1) / p.block_size;
         const int first = t / p.block_size + lane;
         int phys = first <= last ? __ldg(table + first) : 0;
-        if (lane == 0 && use > 0) wait_or_abort(&empty[s], (use & 1u) ^ 1u, abort_flag, p.err);
+        if (lane == 0) wait_or_abort(&empty[s], parity, abort_flag, p.err);
         __syncwarp();
         for (int blk = first; blk <= last; blk += 32) {
           if (blk != first) phys = __ldg(table + blk);
@@ -188,6 +162,10 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
         }
         __syncwarp();
         if (lane == 0) pkv::mbar_arrive(&full[s]);
+        if (++s == p.stages) {
+          s = 0;
+          parity ^= 1u;
+        }
       }
       return true;
     });
@@ -211,7 +189,8 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
   const int v_codes = g * (D / 2) + r0 * (D / 16);
   const int v_scales = scales + (D == 128 ? r0 : r0 >> 1);
   const int half = 8 * row_bytes;  // from fragment rows r0 to r0 + 8
-  int it = 0;
+  int stage = 0;
+  uint32_t parity = 0;
 
   for_each_segment<true, kVar>(p, plan, [&](const Segment& seg) -> bool {
     // Q as the B operand: column r0, and for word w of this lane's quarter the pairs (0, 4), (1, 5), (2, 6), (3, 7)
@@ -254,74 +233,83 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
     for (int j = 0; j < NO; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY};
+    // the rows' reference m as the two numbers the loop takes: what a score must pass to move it (-infinity: no
+    // score yet), and what an exponent starts from
+    float limit[2] = {-INFINITY, -INFINITY};
+    float base[2] = {0.f, 0.f};
     float l[2] = {0.f, 0.f};
 
-    for (int t = seg.t0; t < seg.t1; t += p.t_stage, ++it) {
-      const int s = it % p.stages;
-      const uint32_t use = it / p.stages;
-      wait_or_abort(&full[s], use & 1u, abort_flag, p.err);
-      const int nv = min(seg.t1 - t - tw0, kQ4Chunk);  // keys of this chunk
+    for (int t = seg.t0; t < seg.t1; t += p.t_stage) {
+      if (!pkv::mbar_try_wait(&full[stage], parity)) wait_or_abort(&full[stage], parity, abort_flag, p.err);
+      const int nv = min(seg.t1 - t - tw0, kQ4Chunk);  // keys of this warp in the stage
       if (nv > 0) {
-        const unsigned char* ks = stage_base + s * p.stage_bytes;
+        const unsigned char* ks = stage_base + stage * p.stage_bytes;
         const unsigned char* vs = ks + p.stage_bytes / 2;
-        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-        {
+        float x[kQ4Sub][4];
+#pragma unroll
+        for (int u = 0; u < kQ4Sub; ++u) {
+          const unsigned char* kr = ks + u * 16 * row_bytes;
           uint32_t wx[NW], wy[NW], sx, sy;  // keys r0 and r0 + 8
           if constexpr (D == 128) {
-            const uint4 x = pkv::lds128(ks + k_codes), y = pkv::lds128(ks + k_codes + half);
-            wx[0] = x.x, wx[1] = x.y, wx[2] = x.z, wx[3] = x.w;
-            wy[0] = y.x, wy[1] = y.y, wy[2] = y.z, wy[3] = y.w;
-            sx = *reinterpret_cast<const uint16_t*>(ks + k_scales);
-            sy = *reinterpret_cast<const uint16_t*>(ks + k_scales + half);
+            const uint4 a = pkv::lds128(kr + k_codes), b = pkv::lds128(kr + k_codes + half);
+            wx[0] = a.x, wx[1] = a.y, wx[2] = a.z, wx[3] = a.w;
+            wy[0] = b.x, wy[1] = b.y, wy[2] = b.z, wy[3] = b.w;
+            sx = *reinterpret_cast<const uint16_t*>(kr + k_scales);
+            sy = *reinterpret_cast<const uint16_t*>(kr + k_scales + half);
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(ks + k_codes);
-            const uint2 y = *reinterpret_cast<const uint2*>(ks + k_codes + half);
-            wx[0] = x.x, wx[1] = x.y, wy[0] = y.x, wy[1] = y.y;
-            sx = ks[k_scales];
-            sy = ks[k_scales + half];
+            const uint2 a = *reinterpret_cast<const uint2*>(kr + k_codes);
+            const uint2 b = *reinterpret_cast<const uint2*>(kr + k_codes + half);
+            wx[0] = a.x, wx[1] = a.y, wy[0] = b.x, wy[1] = b.y;
+            sx = kr[k_scales];
+            sy = kr[k_scales + half];
           }
-          // (s, s') of the quarter's groups, over 4
-          const uint32_t hx = hmul2(pkv::e4m3x2_to_f16x2(sx), 0x34003400u);
-          const uint32_t hy = hmul2(pkv::e4m3x2_to_f16x2(sy), 0x34003400u);
+          const uint32_t hx = pkv::e4m3x2_to_f16x2(sx), hy = pkv::e4m3x2_to_f16x2(sy);  // the quarter's groups
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][e] = 0.f;
 #pragma unroll
           for (int grp = 0; grp < NW / 2; ++grp) {
-            const Q4Scale kx(pkv::prmt(hx, 0, grp ? 0x3232u : 0x1010u)), ky(pkv::prmt(hy, 0, grp ? 0x3232u : 0x1010u));
+            const pkv::Q4Scale kx(pkv::prmt(hx, 0, grp ? 0x3232u : 0x1010u)), ky(pkv::prmt(hy, 0, grp ? 0x3232u : 0x1010u));
 #pragma unroll
             for (int w = 2 * grp; w < 2 * grp + 2; ++w) {
               uint32_t fx[4], fy[4];
-              widen_q4(wx[w], kx, fx);
-              widen_q4(wy[w], ky, fy);
-              mma_q4(sa, fx[0], fy[0], fx[1], fy[1], qf[w][0], qf[w][1]);
-              mma_q4(sb, fx[2], fy[2], fx[3], fy[3], qf[w][2], qf[w][3]);
+              pkv::widen_q4(wx[w], kx, fx);
+              pkv::widen_q4(wy[w], ky, fy);
+              mma_q4(x[u], fx[0], fy[0], fx[1], fy[1], qf[w][0], qf[w][1]);
+              mma_q4(x[u], fx[2], fy[2], fx[3], fy[3], qf[w][2], qf[w][3]);
             }
           }
         }
-        // scores of keys r0 (e = 0, 1) and r0 + 8 (2, 3) for rows 2c and 2c + 1
-        float x[4];
+        // scores of keys r0 (e = 0, 1) and r0 + 8 (2, 3) of each chunk for rows 2c and 2c + 1
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = (sa[e] + sb[e]) * mul[e & 1];
-        const int key0 = t + tw0 + token_of(r0);
-        if (nv < kQ4Chunk || (kVar && t + tw0 + kQ4Chunk > seg.ctx - seg.nq)) {
+        for (int u = 0; u < kQ4Sub; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = key0 + (e >= 2 ? 8 : 0);
-            if (key >= seg.t1 || key > lim[e & 1]) x[e] = -INFINITY;
-          }
+          for (int e = 0; e < 4; ++e) x[u][e] *= mul[e & 1];
+        const bool partial = nv < kQ4Chunk;
+        if (partial || (kVar && t + tw0 + kQ4Chunk > seg.ctx - seg.nq)) {
+#pragma unroll
+          for (int u = 0; u < kQ4Sub; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = t + tw0 + 16 * u + token_of(r0) + (e >= 2 ? 8 : 0);
+              if (key >= seg.t1 || key > lim[e & 1]) x[u][e] = -INFINITY;
+            }
         }
-        const float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
-        if (__any_sync(0xffffffffu, top[0] > m[0] + kRescale || top[1] > m[1] + kRescale ||
-                                        (m[0] == -INFINITY && top[0] != -INFINITY) ||
-                                        (m[1] == -INFINITY && top[1] != -INFINITY))) {
+#pragma unroll
+        for (int u = 0; u < kQ4Sub; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], x[u][e]);
+        if (__any_sync(0xffffffffu, top[0] > limit[0] || top[1] > limit[1])) {
           // (a row moves by its own scores only)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float mx = top[i];
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            if (mx > m[i] + kRescale || (m[i] == -INFINITY && mx != -INFINITY)) {
-              const float corr = m[i] == -INFINITY ? 0.f : pkv::ex2(m[i] - mx);
-              m[i] = mx;
+            if (mx > limit[i]) {
+              const float corr = limit[i] == -INFINITY ? 0.f : pkv::ex2(base[i] + kWeightLog2 - mx);
+              limit[i] = mx + kRescale;
+              base[i] = mx - kWeightLog2;
               l[i] *= corr;
 #pragma unroll
               for (int j = 0; j < NO; ++j) {
@@ -331,54 +319,66 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
             }
           }
         }
-        const float base[2] = {m[0] == -INFINITY ? 0.f : m[0] - kWeightLog2, m[1] == -INFINITY ? 0.f : m[1] - kWeightLog2};
-        uint32_t pf[2];  // weights of keys r0 and r0 + 8, then of this lane's V rows
+        uint32_t pf[kQ4Sub][2];  // weights of keys r0 and r0 + 8, then of this lane's V rows
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          pf[i] = pkv::pack_f16x2(pkv::ex2(x[2 * i] - base[0]), pkv::ex2(x[2 * i + 1] - base[1]));
-          add_halves(pf[i], l[0], l[1]);
-          pf[i] = movmatrix(pf[i]);
-        }
-        uint32_t s_ab = vs[v_a + v_scales] | vs[v_b + v_scales] << 8;
-        uint32_t s_cd = vs[v_a + half + v_scales] | vs[v_b + half + v_scales] << 8;
-        if (nv < kQ4Chunk) {  // rows past the last key hold anything: scale 0 makes their values 0
-          s_ab &= (va < nv ? 0x00ffu : 0u) | (vb < nv ? 0xff00u : 0u);
-          s_cd &= (va + 8 < nv ? 0x00ffu : 0u) | (vb + 8 < nv ? 0xff00u : 0u);
-        }
-        const Q4Scale kab(hmul2(pkv::e4m3x2_to_f16x2(s_ab), 0x34003400u));
-        const Q4Scale kcd(hmul2(pkv::e4m3x2_to_f16x2(s_cd), 0x34003400u));
-        uint32_t wv[4][NW / 2];
-        const int v_off[4] = {v_a, v_b, v_a + half, v_b + half};
+        for (int u = 0; u < kQ4Sub; ++u)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if constexpr (D == 128) {
-            const uint2 z = *reinterpret_cast<const uint2*>(vs + v_off[u] + v_codes);
-            wv[u][0] = z.x, wv[u][1] = z.y;
-          } else {
-            wv[u][0] = *reinterpret_cast<const uint32_t*>(vs + v_off[u] + v_codes);
+          for (int i = 0; i < 2; ++i) {
+            pf[u][i] = pkv::pack_f16x2(pkv::ex2(x[u][2 * i] - base[0]), pkv::ex2(x[u][2 * i + 1] - base[1]));
+            add_halves(pf[u][i], l[0], l[1]);
+            pf[u][i] = movmatrix(pf[u][i]);
           }
-        }
 #pragma unroll
-        for (int w = 0; w < NW / 2; ++w)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            // four elements of keys (2c, 2c + 1) and of (2c + 8, 2c + 9), a pair of keys per word
-            uint32_t fab[4], fcd[4];
-            widen_q4(pkv::prmt(wv[0][w], wv[1][w], h ? 0x7632u : 0x5410u), kab, fab);
-            widen_q4(pkv::prmt(wv[2][w], wv[3][w], h ? 0x7632u : 0x5410u), kcd, fcd);
-            const int tm = 4 * w + 2 * h;
-            mma_q4(o[tm], fab[0], fab[1], fcd[0], fcd[1], pf[0], pf[1]);
-            mma_q4(o[tm + 1], fab[2], fab[3], fcd[2], fcd[3], pf[0], pf[1]);
+        for (int u = 0; u < kQ4Sub; ++u) {
+          const unsigned char* vr = vs + u * 16 * row_bytes;
+          uint32_t s_ab = vr[v_a + v_scales] + vr[v_b + v_scales] * 256u;
+          uint32_t s_cd = vr[v_a + half + v_scales] + vr[v_b + half + v_scales] * 256u;
+          if (partial) {  // rows past the last key hold anything: scale 0 makes their values 0
+            const int n = nv - 16 * u;
+            s_ab &= (va < n ? 0x00ffu : 0u) | (vb < n ? 0xff00u : 0u);
+            s_cd &= (va + 8 < n ? 0x00ffu : 0u) | (vb + 8 < n ? 0xff00u : 0u);
           }
+          const pkv::Q4Scale kab(pkv::e4m3x2_to_f16x2(s_ab)), kcd(pkv::e4m3x2_to_f16x2(s_cd));
+          uint32_t wv[4][NW / 2];
+          const int v_off[4] = {v_a, v_b, v_a + half, v_b + half};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if constexpr (D == 128) {
+              const uint2 z = *reinterpret_cast<const uint2*>(vr + v_off[y] + v_codes);
+              wv[y][0] = z.x, wv[y][1] = z.y;
+            } else {
+              wv[y][0] = *reinterpret_cast<const uint32_t*>(vr + v_off[y] + v_codes);
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < NW / 2; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // four elements of keys (2c, 2c + 1) and of (2c + 8, 2c + 9), a pair of keys per word
+              uint32_t fab[4], fcd[4];
+              pkv::widen_q4(pkv::prmt(wv[0][w], wv[1][w], h ? 0x7632u : 0x5410u), kab, fab);
+              pkv::widen_q4(pkv::prmt(wv[2][w], wv[3][w], h ? 0x7632u : 0x5410u), kcd, fcd);
+              const int tm = 4 * w + 2 * h;
+              mma_q4(o[tm], fab[0], fab[1], fcd[0], fcd[1], pf[u][0], pf[u][1]);
+              mma_q4(o[tm + 1], fab[2], fab[3], fcd[2], fcd[3], pf[u][0], pf[u][1]);
+            }
+        }
       }
       __syncwarp();
-      if (lane == 0) pkv::mbar_arrive(&empty[s]);
+      if (lane == 0) pkv::mbar_arrive(&empty[stage]);
+      if (++stage == p.stages) {
+        stage = 0;
+        parity ^= 1u;
+      }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
 
+    float m[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) m[i] = limit[i] == -INFINITY ? -INFINITY : base[i] + kWeightLog2;
     // accumulator (tm, i) is element d0 + 2 tm of row 2c + i, (tm, 2 + i) the next one
     const int d0 = r0 * (D / 8);
     if (p.wph > 1) {

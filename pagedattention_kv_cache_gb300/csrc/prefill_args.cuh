@@ -50,7 +50,7 @@ int prefill_tc_biased_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_capped_biased_launch(const PrefillArgs& a, cudaStream_t stream);
 int prefill_tc_fp8_launch(const PrefillArgs& a, cudaStream_t stream);
 // Chunks over a 4-bit cache.
-int chunk_q4_launch(const PrefillArgs& a, cudaStream_t stream);
+int prefill_tc_q4_launch(const PrefillArgs& a, cudaStream_t stream);
 // Those of at most 8 rows per KV head and 8 KV heads on the decode kernel, with a
 // workspace of chunk_decode_workspace_bytes.
 int chunk_decode_q4_launch(const PrefillArgs& a, cudaStream_t stream);

@@ -235,5 +235,5 @@ extern "C" int pkv_paged_varlen_prefill_attn_q4(void* out, const void* q, const 
                                  block_size, num_blocks, scale, k_scale, v_scale, causal, workspace, workspace_bytes);
   if (chk != PKV_OK) return chk > 0 ? PKV_OK : chk;
   if (on_decode_kernel(a, max_seqlen_k, true)) return pkv::chunk_decode_q4_launch(a, stream);
-  return pkv::chunk_q4_launch(a, stream);
+  return pkv::prefill_tc_q4_launch(a, stream);
 }

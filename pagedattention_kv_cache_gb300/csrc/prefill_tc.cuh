@@ -54,12 +54,20 @@
 //          keys) at a time through registers.  (A ring of its own for the codes
 //          fitted three half tiles; the loads in flight bounded it: a batch of 16
 //          chunks, 56 GFLOP, 79 us.)
+//   kInt4  a 4-bit cache: three warps (the producer's, which has only Q to load, is
+//          one) widen rows to f16, a lane per row and a quarter of a tile (32 keys)
+//          at a time.  A warp copies its quarters' codes and scales into a ring of
+//          its own, three quarters ahead (rows and scales need not suit a tensor
+//          copy).  The four pairs of a code word are stored as they come out,
+//          elements (0, 4), (1, 5), (2, 6), (3, 7): the rewritten Q has the same
+//          order, the epilogue undoes it for V.
 #pragma once
 
 #include <algorithm>
 #include <cfloat>
 
 #include "prefill_args.cuh"
+#include "q4.cuh"
 #include "tcgen05.cuh"
 
 namespace {
@@ -70,12 +78,12 @@ constexpr int kBM = 128;   // rows per query tile
 constexpr int kBN = 128;   // keys per tile
 constexpr int kStages = 2; // K ring and V ring depth
 constexpr int kSoftmaxWarps = 8;  // per query tile: two threads per row, one per half of the key tile
-constexpr int kWidenWarps = 2;    // kFp8: warps that widen E4M3 codes to f16
-template <bool kFp8>
-constexpr int threads() {
-  return 32 * (2 + 2 * kSoftmaxWarps + (kFp8 ? kWidenWarps : 0));
-}
-constexpr int kQuarter = 32;  // kFp8: keys widened at a time
+constexpr int kWidenWarps = 2;    // kFp8, kInt4: warps that widen codes to f16 (kInt4: and warp 0)
+enum Form { kPlain, kMasked, kCapped, kBiased, kCappedBiased, kE4m3, kInt4 };
+__host__ __device__ constexpr bool quantized(Form f) { return f == kE4m3 || f == kInt4; }
+__host__ __device__ constexpr int threads(Form f) { return 32 * (2 + 2 * kSoftmaxWarps + (quantized(f) ? kWidenWarps : 0)); }
+constexpr int kQuarter = 32;  // kFp8, kInt4: keys widened at a time
+constexpr int kInt4Depth = 4;  // kInt4: quarters in a widening warp's ring
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;    // S_A at 0, S_B at 128
 constexpr uint32_t kColO = 256;  // O_A at 256, O_B at 384
@@ -95,13 +103,20 @@ struct Geo {
   static constexpr uint32_t kRedOffset = 2 * kTileQ + 2 * kStages * kTileKV;
   static constexpr uint32_t kBarOffset = kRedOffset + kRedBytes;
   static constexpr uint32_t kSmemBytes = kBarOffset + 256 + 1024;  // barriers + 1 KB for alignment
+  // kInt4: the rings of codes, then of scales, follow the barriers
+  static constexpr uint32_t kInt4Codes = kQuarter * D / 2;
+  static constexpr uint32_t kInt4Slot = kInt4Codes + kQuarter * D / 16;
+  static constexpr uint32_t kInt4Offset = kBarOffset + 256;
+  static constexpr uint32_t kInt4Bytes = (kWidenWarps + 1) * kInt4Depth * kInt4Slot;
   // one CTA per SM even when two would fit (each holds all 512 TMEM columns)
-  static constexpr uint32_t kLaunchSmem = kSmemBytes > 120 * 1024 ? kSmemBytes : 120 * 1024;
+  static constexpr uint32_t launch_smem(Form f) {
+    return std::max<uint32_t>(kSmemBytes + (f == kInt4 ? kInt4Bytes : 0), 120 * 1024);
+  }
   static constexpr size_t kRecordBytes = static_cast<size_t>(kBM) * D * 4 + static_cast<size_t>(kBM) * 8;
 };
-static_assert(Geo<128>::kSmemBytes <= 227 * 1024, "shared memory plan exceeds an SM");
+static_assert(Geo<128>::launch_smem(kInt4) <= 227 * 1024, "shared memory plan exceeds an SM");
 constexpr float kRescaleLog2 = 8.0f;
-// kFp8: weights enter P V as f16, whose subnormals end at 2^-24, so they are taken 2^7 times
+// kFp8, kInt4: weights enter P V as f16, whose subnormals end at 2^-24, so they are taken 2^7 times
 // as large (with the lazy rescale at most 2^15): a weight then counts down to 2^-32 of the
 // row's largest.  Without the factor 131072 keys 17.4 below a dominant one, 0.36 % of the
 // mass, came out as nothing.
@@ -138,13 +153,11 @@ enum Bar {
   O_FINAL = P_FULL + 2,  // per query tile
   V_TAIL = O_FINAL + 2,
   V_HEAD,  // kMod: the first V tile, once its rows before the first visible key are zeroed
-  Q_READY,  // kFp8, per query tile: Q rewritten as scaled f16
+  Q_READY,  // kFp8, kInt4, per query tile: Q rewritten as scaled f16
   RAW_FULL = Q_READY + 2,  // kFp8, per K stage, then per V stage: the codes have arrived
   NUM_BARS = RAW_FULL + 2 * kStages
 };
 static_assert(NUM_BARS * 8 + 16 <= 256, "barrier area too small");
-
-enum Form { kPlain, kMasked, kCapped, kBiased, kCappedBiased, kE4m3 };
 
 // c log2e tanh(k s) of a raw score s as s P(s^2), k = raw_to_x: P of degree 2
 // for |k s| <= 0.4 and of degree 4 for |k s| <= 1.  The coefficients of tanh(x) / x
@@ -212,9 +225,11 @@ struct TcParams {
   ScoreMod mod;            // kMod
   TanhPoly tanh_poly;      // kMod with a cap
   float bias_mul;          // slopes to the units of bias_scores
-  const unsigned char* k_codes;  // kFp8: the pools, for block sizes whose pieces are single rows
+  const unsigned char* k_codes;  // kInt4: the pools; kFp8: for block sizes whose pieces are single rows
   const unsigned char* v_codes;
   float v_scale;
+  uint32_t block_mul;  // kInt4: key / block_size = key * block_mul >> block_shift
+  int block_shift;
 };
 
 }  // namespace
@@ -271,7 +286,7 @@ __device__ __forceinline__ uint32_t exp2_pair_bf16(uint32_t s0, uint32_t s1, flo
   return out;
 }
 
-// The same with f16 weights (kFp8), which reach 2^15 (kF16WeightLog2 and the lazy rescale).
+// The same with f16 weights (kFp8, kInt4), which reach 2^15 (kF16WeightLog2 and the lazy rescale).
 __device__ __forceinline__ uint32_t exp2_pair_f16(uint32_t s0, uint32_t s1, float scale, float neg_m, uint64_t& acc) {
   uint32_t out;
   asm("{\n\t.reg .b64 x, c, m;\n\t.reg .f32 a, b, sa, sb;\n\t.reg .b16 pa, pb, one;\n\t"
@@ -435,7 +450,7 @@ __device__ __forceinline__ int warp_uniform(int v) {
 }
 
 template <int G, int D, Form kForm>
-__global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
+__global__ void __launch_bounds__(threads(kForm), 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TcParams p) {
   pdl_enter();
@@ -446,7 +461,9 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   constexpr uint32_t kTileKV = Geo<D>::kTileKV;
   constexpr size_t kRecordBytes = Geo<D>::kRecordBytes;
   constexpr bool kFp8 = kForm == kE4m3;
-  constexpr bool kMod = kForm != kPlain && kForm != kE4m3;
+  constexpr bool kQ4 = kForm == kInt4;
+  constexpr bool kF16 = quantized(kForm);
+  constexpr bool kMod = kForm != kPlain && !kF16;
   constexpr bool kCap = kForm == kCapped || kForm == kCappedBiased;
   constexpr bool kBias = kForm == kBiased || kForm == kCappedBiased;
   // blocks launch in linear order: x runs over (sequence, KV head), y over
@@ -510,8 +527,8 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   const int n_a = max(0, min(n_tiles, n_need[0] - j0));
   const int n_b = max(0, min(n_tiles, n_need[1] - j0));
   // the last tile holds keys past nk: its V rows there are zeroed first
-  // (kFp8: the widening warps write those rows as zeros)
-  const bool v_tail = !kFp8 && (!kMod || n_tiles > 0) && (j0 + n_tiles) * kBN > nk;
+  // (kFp8, kInt4: the widening warps write those rows as zeros)
+  const bool v_tail = !kF16 && (!kMod || n_tiles > 0) && (j0 + n_tiles) * kBN > nk;
   // kMod: the first tile holds keys before lo_pair: its V rows there are zeroed too
   const bool v_head = kMod && n_tiles > 0 && j0 * kBN < lo_pair;
 
@@ -535,8 +552,9 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     *abort_flag = 0;
     mbar_init(&bars[Q_FULL], 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars[K_FULL + s], kFp8 ? kWidenWarps : 1);
-      mbar_init(&bars[V_FULL + s], kFp8 ? kWidenWarps : 1);
+      // kFp8: one arrival per widening warp, kInt4: per quarter
+      mbar_init(&bars[K_FULL + s], kFp8 ? kWidenWarps : kQ4 ? kBN / kQuarter : 1);
+      mbar_init(&bars[V_FULL + s], kFp8 ? kWidenWarps : kQ4 ? kBN / kQuarter : 1);
       mbar_init(&bars[K_EMPTY + s], 1);
       mbar_init(&bars[V_EMPTY + s], 1);
     }
@@ -548,7 +566,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     mbar_init(&bars[O_FINAL + 1], 1);
     mbar_init(&bars[V_TAIL], 1);
     if constexpr (kMod) mbar_init(&bars[V_HEAD], 1);
-    if constexpr (kFp8) {
+    if constexpr (kF16) {
       for (int x = 0; x < 2; ++x) mbar_init(&bars[Q_READY + x], kSoftmaxWarps);
       for (int s = 0; s < 2 * kStages; ++s) mbar_init(&bars[RAW_FULL + s], 1);
     }
@@ -653,8 +671,10 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   const int n_early = min(n_tiles, kStages);
   if (tid == 0) {
     tc::prefetch_tensormap(&tm_q);
-    tc::prefetch_tensormap(&tm_k);
-    tc::prefetch_tensormap(&tm_v);
+    if constexpr (!kQ4) {
+      tc::prefetch_tensormap(&tm_k);
+      tc::prefetch_tensormap(&tm_v);
+    }
     const int nx = n_b > 0 ? 2 : 1;
     mbar_expect_tx(&bars[Q_FULL], nx * kTileQ);
     for (int x = 0; x < nx; ++x) {
@@ -663,7 +683,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         tc::tma_load_3d(sq + x * kTileQ + kSlabQ, &tm_q, 64, g * G, q_begin + tok0 + x * TQ, &bars[Q_FULL]);
     }
     mbar_arrive(&bars[Q_FULL]);
-    if constexpr (!kMod && !kFp8) {
+    if constexpr (!kMod && !kF16) {
       for (int j = 0; j < n_early; ++j) {
         load_tile(j, false);
         load_tile(j, true);
@@ -689,7 +709,101 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
   // broadcast from lane 0 so the compiler treats the TMEM base as warp-uniform
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-  if (warp == 0) {
+  if (kQ4 && (warp == 0 || warp >= 2 + 2 * kSoftmaxWarps)) {
+    // ------------------------------------------------------------ kInt4: rows to f16
+    // The quarters of K(0), V(0), K(1), ... go round the three warps.
+    constexpr int kWorkers = kWidenWarps + 1;
+    constexpr int kChunks = D / 32;  // 16-byte chunks of a head's codes: 32 elements, 4 chunks of the f16 row
+    const int me = warp == 0 ? 0 : warp - 1 - 2 * kSoftmaxWarps;
+    const int n_units = 8 * n_tiles;
+    const int row_bytes = q4_row_bytes(p.hkv, D);
+    const int scale_at = q4_scale_offset(p.hkv, D) + g * (D / 16);
+    unsigned char* const ring = smem + Geo<D>::kInt4Offset + me * (kInt4Depth * Geo<D>::kInt4Slot);
+    // the block of this lane's key of a unit (-1: no such key), looked up a unit before it is copied
+    auto key_of = [&](int u) { return (j0 + (u >> 3)) * kBN + (u & 3) * kQuarter + lane; };
+    auto block_of = [&](int key) {
+      return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(key)) * p.block_mul >> p.block_shift);
+    };
+    // where chunk ch of row r lies in the ring: eight rows' same chunks (and eight neighbouring chunks) differ modulo 128 bytes
+    auto swizzle = [](int r) { return kChunks == 4 ? (r >> 1) & 3 : (r >> 2) & 1; };
+    auto look_up = [&](int u) { return u < n_units && key_of(u) < nk ? __ldg(table + block_of(key_of(u))) : -1; };
+    int phys = look_up(me);
+    int slot = 0;  // of the next unit to copy
+    // rows of no key and of bad blocks are filled with zeros
+    auto copy = [&](int u) {
+      if (u < n_units) {
+        const int key = key_of(u);
+        const bool ok = phys >= 0 && phys < p.num_blocks;
+        if (key < nk && !ok) raise_error(p.err, PKV_DERR_BLOCK_RANGE);
+        const int row = ok ? phys * p.block_size + (key - block_of(key) * p.block_size) : -1;
+        const unsigned char* pool = u & 4 ? p.v_codes : p.k_codes;
+        const uint32_t to = smem_u32(ring + slot * Geo<D>::kInt4Slot);
+        // neighbouring lanes take the chunks of one row
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int r = i * (32 / kChunks) + lane / kChunks;
+          const int from = __shfl_sync(0xffffffffu, row, r);
+          const int ch = lane % kChunks;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (r * kChunks + (ch ^ swizzle(r))) * 16),
+                       "l"(pool + static_cast<size_t>(max(from, 0)) * row_bytes + g * (D / 2) + ch * 16),
+                       "r"(from >= 0 ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to + Geo<D>::kInt4Codes + lane * (D / 16)),
+                     "l"(pool + static_cast<size_t>(max(row, 0)) * row_bytes + scale_at), "n"(D / 16),
+                     "r"(row >= 0 ? D / 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      phys = look_up(u + kWorkers);
+      slot = slot + 1 == kInt4Depth ? 0 : slot + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kInt4Depth - 1; ++i) copy(me + i * kWorkers);
+    int from = 0;
+    for (int u = me; u < n_units; u += kWorkers) {
+      copy(u + (kInt4Depth - 1) * kWorkers);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kInt4Depth - 1) : "memory");
+      __syncwarp();
+      const unsigned char* src = ring + from * Geo<D>::kInt4Slot;
+      from = from + 1 == kInt4Depth ? 0 : from + 1;
+      uint4 codes[kChunks];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) codes[i] = lds128(src + (lane * kChunks + (i ^ swizzle(lane))) * 16);
+      uint32_t scales[D / 64];  // E4M3, four groups each
+      if constexpr (D == 128) {
+        const uint2 x = *reinterpret_cast<const uint2*>(src + Geo<D>::kInt4Codes + lane * 8);
+        scales[0] = x.x, scales[1] = x.y;
+      } else {
+        scales[0] = *reinterpret_cast<const uint32_t*>(src + Geo<D>::kInt4Codes + lane * 4);
+      }
+      const int j = u >> 3;
+      const bool is_v = u & 4;
+      const int st = j % kStages;
+      if (j >= kStages) wait(&bars[(is_v ? V_EMPTY : K_EMPTY) + st], (j / kStages - 1) & 1);
+      const int row = (u & 3) * kQuarter + lane;
+      unsigned char* dst = (is_v ? sv : sk) + st * kTileKV + row * 128;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+        // the chunk's two groups: bytes 2 i and 2 i + 1 of the scales
+        const uint32_t s = e4m3x2_to_f16x2(scales[i / 2] >> (16 * (i & 1)) & 0xffffu);
+        const Q4Scale k[2] = {Q4Scale(prmt(s, 0, 0x1010u)), Q4Scale(prmt(s, 0, 0x3232u))};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t f[4];
+          widen_q4(w[e], k[e / 2], f);
+          const int ch = 4 * i + e;
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * kSlabKV + (((ch & 7) ^ (row & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[(is_v ? V_FULL : K_FULL) + st]);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     // V rows of tile j's stage from row `first` on, `count` of them, become zeros once the tile has arrived
     auto zero_v_rows = [&](int j, int first, int count) {
@@ -797,8 +911,8 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     // one elected lane issues the MMAs and commits.
     {
       const bool leader = tc::elect_one();
-      constexpr uint32_t idesc_qk = kFp8 ? tc::idesc_f16(kBM, kBN, 0, 0) : tc::idesc_bf16(kBM, kBN, 0, 0);
-      constexpr uint32_t idesc_pv = kFp8 ? tc::idesc_f16(kBM, kD, 0, 1) : tc::idesc_bf16(kBM, kD, 0, 1);
+      constexpr uint32_t idesc_qk = kF16 ? tc::idesc_f16(kBM, kBN, 0, 0) : tc::idesc_bf16(kBM, kBN, 0, 0);
+      constexpr uint32_t idesc_pv = kF16 ? tc::idesc_f16(kBM, kD, 0, 1) : tc::idesc_bf16(kBM, kD, 0, 1);
       // descriptors of the first Q, K and V slabs; later ones differ only in the
       // start-address field (address >> 4), so they are reached by adding offset >> 4
       const uint64_t q_desc = tc::smem_desc(smem_u32(sq), 16, 1024);
@@ -835,7 +949,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         tc::fence_after_sync();
         for (int x = 0; x < 2; ++x)
           if (n_x[x] > 0) {
-            if constexpr (kFp8) {
+            if constexpr (kF16) {
               wait(&bars[Q_READY + x], 0);
               tc::fence_after_sync();
             }
@@ -979,7 +1093,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     float m_run = -INFINITY;
     float l_run = 0.f;  // this half's keys only
     uint32_t r[64];
-    if constexpr (kFp8) {
+    if constexpr (kF16) {
       // Q becomes f16 in place, each row scaled by the power of two that puts its
       // largest element in [2^14, 2^15): exact but for elements 2^28 times
       // smaller than that.  The power comes off with the softmax scale.
@@ -1015,8 +1129,12 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         for (int i = 0; i < kChunksHalf; ++i) {
           float f[8];
           Chunk<__nv_bfloat16>::unpack(qc[i], f);
-          *q_chunk(i) = make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
-                                   pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
+          if constexpr (kQ4)
+            *q_chunk(i) = make_uint4(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up, f[5] * up),
+                                     pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up, f[7] * up));
+          else
+            *q_chunk(i) = make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
+                                     pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -1085,7 +1203,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       named_barrier_sync(pair_id, 64);
       const float mt = fmaxf(*red_at(j & 1, 0), *red_at(j & 1, 1));
       float m_tile = mt * mul;
-      if constexpr (kFp8) {
+      if constexpr (kF16) {
         // the reference of the weights, below the maximum: the factor cancels against the row sum and in the merge of
         // parts, which see the same reference (past 2^20 the difference would not be exact enough to bound them)
         if (fabsf(m_tile) < 0x1p20f) m_tile -= kF16WeightLog2;
@@ -1143,7 +1261,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          r[e] = kFp8 ? exp2_pair_f16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2])
+          r[e] = kF16 ? exp2_pair_f16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2])
                       : exp2_pair_bf16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2]);
       }
       tc::tmem_st32(s_addr + half * 32, r);
@@ -1180,6 +1298,8 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
     *red_at(0, half) = l_run;
     named_barrier_sync(pair_id, 64);
     l_run = *red_at(0, 0) + *red_at(0, 1);
+    // kInt4: where element u of eight lies among its columns
+    auto column = [](int u) { return !kQ4 ? u : u < 4 ? 2 * u : 2 * u - 7; };
     // this thread's 64 outputs, 32 at a time: TMEM O (zero when the tile saw no key in this part)
     auto load_o = [&](int c, uint32_t* o) {
       if (n_x > 0) {
@@ -1196,7 +1316,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
       // chunks per row) so the eight rows of a quarter-warp hit distinct banks;
       // then copied out 512 contiguous bytes (when G > 1) per warp instruction
       constexpr int kChunks = kD / 8;  // 16-byte chunks per row
-      const float inv = l_run > 0.f ? (kFp8 ? p.v_scale : 1.f) / l_run : 0.f;
+      const float inv = l_run > 0.f ? (kF16 ? p.v_scale : 1.f) / l_run : 0.f;
       unsigned char* stage = sq + x * kTileQ;
 #pragma unroll
       for (int c = 0; c < kD / 64; ++c) {
@@ -1206,7 +1326,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
         for (int e = 0; e < 32; e += 8) {
           float f[8];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) f[u] = __uint_as_float(o[e + u]) * inv;
+          for (int u = 0; u < 8; ++u) f[u] = __uint_as_float(o[e + column(u)]) * inv;
           const int chunk = half * (kChunks / 2) + (c * 32 + e) / 8;
           *reinterpret_cast<uint4*>(stage + row * (kD * 2) + ((chunk ^ (row & (kChunks - 1))) << 4)) =
               Chunk<__nv_bfloat16>::pack(f);
@@ -1308,7 +1428,7 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
             mq[q] = lq[q] != 0.f ? exp2f(mq[q] - mm) : kNone;
             if (mq[q] != kNone) total += mq[q] * lq[q];
           }
-          const float inv = total > 0.f ? (kFp8 ? p.v_scale : 1.f) / total : 0.f;
+          const float inv = total > 0.f ? (kF16 ? p.v_scale : 1.f) / total : 0.f;
 #pragma unroll
           for (int c = 0; c < kD / 64; ++c) {
             uint32_t o[32];
@@ -1344,7 +1464,10 @@ __global__ void __launch_bounds__(threads<kForm == kE4m3>(), 1)
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) f[u] *= inv;
-                reinterpret_cast<uint4*>(dst + c * 32 + e)[0] = Chunk<__nv_bfloat16>::pack(f);
+                float elements[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) elements[u] = f[column(u)];
+                reinterpret_cast<uint4*>(dst + c * 32 + e)[0] = Chunk<__nv_bfloat16>::pack(elements);
               }
             }
           }
@@ -1380,6 +1503,7 @@ inline int piece_rows(const PrefillArgs& a, int tile) {
 template <int G, int D, Form kForm>
 int launch(const PrefillArgs& a, cudaStream_t stream) {
   constexpr bool kFp8 = kForm == kE4m3;
+  constexpr bool kQ4 = kForm == kInt4;
   constexpr int TQ = kBM / G;
   constexpr int kD = D;
   alignas(64) CUtensorMap tm_q, tm_k, tm_v;
@@ -1389,7 +1513,9 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
   const void* kb = paged ? a.k_cache : a.k;
   const void* vb = paged ? a.v_cache : a.v;
   const uint64_t rows = paged ? static_cast<uint64_t>(a.num_blocks) * a.block_size : a.total_k;
-  if constexpr (kFp8) {
+  if constexpr (kQ4) {
+    tm_k = tm_v = tm_q;  // not used
+  } else if constexpr (kFp8) {
     if (encode_u8_3d(&tm_k, kb, kD, a.hkv, rows, piece) != PKV_OK) return PKV_ECUDA;
     if (encode_u8_3d(&tm_v, vb, kD, a.hkv, rows, piece) != PKV_OK) return PKV_ECUDA;
   } else {
@@ -1417,11 +1543,19 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
   if constexpr (kForm == kCapped || kForm == kCappedBiased)
     p.tanh_poly = make_tanh_poly(a.mod.cap_log2, a.mod.raw_to_x);
   p.bias_mul = kForm == kBiased ? 1.f / a.scale : kLog2e;
-  if constexpr (kFp8) {
-    p.scale_log2 *= a.k_scale;
-    p.v_scale = a.v_scale;
+  if constexpr (quantized(kForm)) {
+    constexpr float kUp = kQ4 ? 4.f : 1.f;  // (widened 4-bit rows hold a quarter of the values)
+    p.scale_log2 *= a.k_scale * kUp;
+    p.v_scale = a.v_scale * kUp;
     p.k_codes = static_cast<const unsigned char*>(a.k_cache);
     p.v_codes = static_cast<const unsigned char*>(a.v_cache);
+  }
+  if constexpr (kQ4) {
+    // m = ceil(2^(31 + s) / d) with d <= 2^s: key m is off by less than 2^s key < 2^(31 + s)
+    int s = 0;
+    while ((1ll << s) < a.block_size) ++s;
+    p.block_shift = 31 + s;
+    p.block_mul = static_cast<uint32_t>(((1ull << p.block_shift) + a.block_size - 1) / a.block_size);
   }
   p.piece_rows = piece;
   const int pairs = (a.max_seqlen_q + 2 * TQ - 1) / (2 * TQ);
@@ -1440,11 +1574,11 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
     p.records = ws + 2 * flags;
   }
   auto kernel = prefill_tc_kernel<G, D, kForm>;
-  constexpr uint32_t kSmemBytes = Geo<D>::kLaunchSmem;
+  constexpr uint32_t kSmemBytes = Geo<D>::launch_smem(kForm);
   static std::atomic<uint64_t> smem_allowed{0};
   if (allow_smem(kernel, kSmemBytes, smem_allowed) != cudaSuccess) return PKV_ECUDA;
   dim3 grid(a.batch * a.hkv, pairs * p.parts_max);
-  return launch_pdl(kernel, grid, dim3(threads<kFp8>()), kSmemBytes, stream, tm_q, tm_k, tm_v, p) == cudaSuccess ? PKV_OK
+  return launch_pdl(kernel, grid, dim3(threads(kForm)), kSmemBytes, stream, tm_q, tm_k, tm_v, p) == cudaSuccess ? PKV_OK
                                                                                                   : PKV_ECUDA;
 }
 

@@ -57,4 +57,35 @@ __device__ __forceinline__ uint32_t q4_codes8(const float (&x)[8], uint32_t scal
   return w;
 }
 
+// Codes to matrix operands.  A word of eight codes becomes four f16 pairs with two
+// shifts, four and-ors and four fmas: a nibble n in mantissa bits 9..6 under the
+// exponent of 4 is the number 4 + n / 4, in bits 5..2 under the exponent of 64 it is
+// 64 + n / 4, and x s - 6 s (or - 66 s) is (n - 8) s / 4.  Every step is exact:
+// (n - 8) s has 7 significant bits, 66 s at most 9 and stays below f16's end.
+// (Conversion instructions run at 16 results per clock and SM.)
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// A scale pair with what the two nibble positions subtract.
+struct Q4Scale {
+  uint32_t s, low, high;
+  __device__ __forceinline__ explicit Q4Scale(uint32_t pair)
+      : s(pair), low(hmul2(pair, 0xc600c600u)), high(hmul2(pair, 0xd420d420u)) {}
+};
+// The four f16 pairs of a word: nibbles (0, 4), (1, 5), (2, 6) and (3, 7), as (n - 8) / 4 times the scale pair.
+__device__ __forceinline__ void widen_q4(uint32_t w, const Q4Scale& k, uint32_t (&f)[4]) {
+  const uint32_t y0 = w << 2, y1 = w >> 6;
+  f[0] = hfma2((y0 & 0x003c003cu) | 0x54005400u, k.s, k.high);
+  f[1] = hfma2((y0 & 0x03c003c0u) | 0x44004400u, k.s, k.low);
+  f[2] = hfma2((y1 & 0x003c003cu) | 0x54005400u, k.s, k.high);
+  f[3] = hfma2((y1 & 0x03c003c0u) | 0x44004400u, k.s, k.low);
+}
+
 }  // namespace pkv
