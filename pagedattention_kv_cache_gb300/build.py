@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libpagedkv.so")
 SOURCES = ["api.cu", "kv_store.cu", "decode.cu", "decode_mod.cu", "verify.cu", "fp8.cu", "blocks.cu", "prefill.cu",
            "prefill_tc.cu", "prefill_tc_masked.cu", "prefill_tc_capped.cu", "prefill_tc_biased.cu",
            "prefill_tc_capped_biased.cu", "prefill_tc_fp8.cu", "prefill_chunk.cu", "chunk_decode.cu", "kv_rope.cu",
-           "prefill_tc_q4.cu", "decode_q4.cu"]
+           "prefill_tc_q4.cu", "decode_q4.cu", "decode_q4_d64.cu", "decode_q4_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{os.path.join(ROOT, 'include')}"]

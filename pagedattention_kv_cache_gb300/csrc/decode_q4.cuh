@@ -6,13 +6,7 @@
 // 128).  At 4.5 bits an element the bytes leave about three issued instructions
 // per element of a lane, so what the kernel is built around is a short way from
 // codes to matrix operands:
-//  * A word of eight codes becomes four f16 pairs with two shifts, four
-//    and-ors and four fmas: a nibble n in mantissa bits 9..6 under the exponent of
-//    4 is the number 4 + n / 4, in bits 5..2 under the exponent of 64 it is
-//    64 + n / 4, and x s - 6 s (or - 66 s) is (n - 8) s / 4.  Every step is exact:
-//    (n - 8) s has 7 significant bits, 66 s at most 9 and stays below f16's end.
-//    (The conversion instructions of the FP8 kernel run at 16 results per clock
-//    and SM, which alone would take longer than the bytes.)
+//  * widen_q4 (q4.cuh): nine instructions for a word of eight codes.
 //  * S^T = K Q^T: the 16 keys of a chunk in the M dimension and the R <= 8 rows
 //    in N, so one m16n8k16 per 16 elements of head_dim wastes only the rows past
 //    R.  A lane takes a whole quarter of its two keys' head rows (16 bytes each at
@@ -30,7 +24,8 @@
 // weights as f16 times 2^7, so that they count down to 2^-31 of the row's largest.
 #pragma once
 
-#include "decode_plan.cuh"
+#include "decode_launch.cuh"
+#include "decode_q4_args.cuh"
 #include "q4.cuh"
 
 namespace {
@@ -40,6 +35,10 @@ constexpr int kQ4Stages = 6;  // at most
 constexpr int kQ4Smem = 224 * 1024;
 constexpr int kQ4Sub = 4;     // chunks of 16 keys per consumer warp and stage: their products overlap
 constexpr int kQ4Chunk = 16 * kQ4Sub;
+// Split points fall on multiples of this many tokens: with parts of a few tokens
+// their merge costs more than it saves (4 sequences of 32k-131k: 102 us at 1, 100 at 64
+// and at 128, 104 at 256; one of 777 14.7 up to 128, 19 at 256).
+constexpr int kQ4Align = 128;
 
 // d (16x8 fp32) += a (16x16 f16, row) * b (16x8 f16, col)
 __device__ __forceinline__ void mma_q4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -49,27 +48,40 @@ __device__ __forceinline__ void mma_q4(float (&d)[4], uint32_t a0, uint32_t a1, 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+template <int kBytes>
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[kBytes / 4]) {
+  if constexpr (kBytes == 16)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+  else if constexpr (kBytes == 8)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+}
+template <int kBytes>  // 1 or 2
+__device__ __forceinline__ uint32_t lds_short(uint32_t at) {
+  uint32_t v;
+  if constexpr (kBytes == 2)
+    asm volatile("{\n\t.reg .u16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(v) : "r"(at));
+  else
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
 // Transposes an 8x8 matrix of 16-bit elements spread over the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// acc + the f16 in the low (high) half of h
-__device__ __forceinline__ void add_halves(uint32_t h, float& lo, float& hi) {
-  asm("{\n\t.reg .b16 a, b, one;\n\tmov.b32 {a, b}, %2;\n\tmov.b16 one, 0x3c00;\n\t"
-      "fma.rn.f32.f16 %0, a, one, %0;\n\tfma.rn.f32.f16 %1, b, one, %1;\n\t}"
-      : "+f"(lo), "+f"(hi)
-      : "r"(h));
-}
-
 // The token (of eight) that stands in fragment row i: rows i and i + 1, which one
 // 16-byte load phase reads, differ in parity, and so do rows 0, 2, 4, 6 from one
 // to the next, which V's loads take together (two rows of 8 heads of 128, 576
 // bytes each, are 64 bytes apart modulo 128).
 __device__ __forceinline__ int token_of(int i) { return i & 1 ? 4 + ((i >> 1) ^ 1) : i >> 1; }
 
-template <int G, int QL, int D, bool kVar>
+constexpr int kChunkRows = 8;  // G * QL of the chunk instantiations
+
+// kHeads: 8, which makes every offset of a row a constant (256 sequences of 1k-8k, 298 -> 285 us), or 0, any number.
+template <int G, int QL, int D, bool kVar, int kHeads>
 __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel(const Params p) {
   pkv::pdl_enter();
   {
@@ -94,7 +106,8 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
   const int warp = tid / 32;
   const int lane = tid % 32;
   const int nw = p.nw;
-  const int row_bytes = pkv::q4_row_bytes(p.hkv, D);
+  const int hkv = kHeads ? kHeads : p.hkv;
+  const int row_bytes = pkv::q4_row_bytes(hkv, D);
   unsigned char* stage_base = smem;
   uint64_t* full = reinterpret_cast<uint64_t*>(stage_base + p.stages * p.stage_bytes);
   uint64_t* empty = full + kQ4Stages;
@@ -173,14 +186,14 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
   }
 
   // -------------------------------------------------------------- consumers
-  const int g = warp % p.hkv;
-  const int phase = warp / p.hkv;
+  const int g = warp % hkv;
+  const int phase = warp / hkv;
   const int r0 = lane >> 2;  // fragment rows r0 and r0 + 8 (keys of S^T, elements of O^T); column r0 of B operands
   const int c = lane & 3;
   const int nthreads_c = nw * 32;
   const int tw0 = phase * kQ4Chunk;  // this warp's keys of a stage
   // offsets in a stage of what this lane reads: two keys' quarter and scales, four V rows' elements and scales
-  const int scales = pkv::q4_scale_offset(p.hkv, D) + g * (D / 16);
+  const int scales = pkv::q4_scale_offset(hkv, D) + g * (D / 16);
   const int k_at = (tw0 + token_of(r0)) * row_bytes;
   const int k_codes = k_at + g * (D / 2) + c * (D / 8);
   const int k_scales = k_at + scales + c * (D / 64);
@@ -189,13 +202,16 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
   const int v_codes = g * (D / 2) + r0 * (D / 16);
   const int v_scales = scales + (D == 128 ? r0 : r0 >> 1);
   const int half = 8 * row_bytes;  // from fragment rows r0 to r0 + 8
+  const uint32_t ring = pkv::smem_u32(stage_base);
+  const uint32_t stage_bytes = static_cast<uint32_t>(p.stage_bytes);
   int stage = 0;
+  uint32_t at = ring;  // the stage's K rows, its V rows half a stage further
   uint32_t parity = 0;
 
   for_each_segment<true, kVar>(p, plan, [&](const Segment& seg) -> bool {
     // Q as the B operand: column r0, and for word w of this lane's quarter the pairs (0, 4), (1, 5), (2, 6), (3, 7)
     uint32_t qf[NW][4];
-    float mul[2];  // of rows 2c and 2c + 1: the power that scaled q comes off with the scale (and K's 1/4)
+    float mul[2];  // of rows 2c and 2c + 1: the power that scaled q comes off with the scale (and K's unit)
     {
       const bool row_here = kVar ? r0 / G < seg.nq && r0 < R : r0 < R;
       const size_t row = kVar ? static_cast<size_t>(seg.q0) + r0 / G : static_cast<size_t>(seg.b) * QL + r0 / G;
@@ -213,8 +229,10 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const int ex = amax > 0.f ? min(max(14 - ilogbf(amax), -113), 126) : 0;
-      const float up = ldexpf(1.f, ex);
-      const float down = p.scale_log2 * 4.f * ldexpf(1.f, -ex);
+      // (the scale's sign goes with q; kept above zero, so that -infinity, a hidden key, stays -infinity)
+      const float up = copysignf(ldexpf(1.f, ex), p.scale_log2);
+      float down = fabsf(p.scale_log2) * pkv::kQ4Unit * ldexpf(1.f, -ex);
+      if (down == 0.f) down = FLT_MIN;
       mul[0] = __shfl_sync(0xffffffffu, down, 8 * c);
       mul[1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
 #pragma unroll
@@ -237,32 +255,21 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
     // score yet), and what an exponent starts from
     float limit[2] = {-INFINITY, -INFINITY};
     float base[2] = {0.f, 0.f};
-    float l[2] = {0.f, 0.f};
+    float l[4] = {0.f, 0.f, 0.f, 0.f};  // of rows 2c and 2c + 1, twice: a product of ones with the weights
 
     for (int t = seg.t0; t < seg.t1; t += p.t_stage) {
       if (!pkv::mbar_try_wait(&full[stage], parity)) wait_or_abort(&full[stage], parity, abort_flag, p.err);
       const int nv = min(seg.t1 - t - tw0, kQ4Chunk);  // keys of this warp in the stage
       if (nv > 0) {
-        const unsigned char* ks = stage_base + stage * p.stage_bytes;
-        const unsigned char* vs = ks + p.stage_bytes / 2;
+        const uint32_t kc = at + k_codes, ks = at + k_scales;
+        const uint32_t vs = at + stage_bytes / 2;
         float x[kQ4Sub][4];
 #pragma unroll
         for (int u = 0; u < kQ4Sub; ++u) {
-          const unsigned char* kr = ks + u * 16 * row_bytes;
-          uint32_t wx[NW], wy[NW], sx, sy;  // keys r0 and r0 + 8
-          if constexpr (D == 128) {
-            const uint4 a = pkv::lds128(kr + k_codes), b = pkv::lds128(kr + k_codes + half);
-            wx[0] = a.x, wx[1] = a.y, wx[2] = a.z, wx[3] = a.w;
-            wy[0] = b.x, wy[1] = b.y, wy[2] = b.z, wy[3] = b.w;
-            sx = *reinterpret_cast<const uint16_t*>(kr + k_scales);
-            sy = *reinterpret_cast<const uint16_t*>(kr + k_scales + half);
-          } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(kr + k_codes);
-            const uint2 b = *reinterpret_cast<const uint2*>(kr + k_codes + half);
-            wx[0] = a.x, wx[1] = a.y, wy[0] = b.x, wy[1] = b.y;
-            sx = kr[k_scales];
-            sy = kr[k_scales + half];
-          }
+          uint32_t wx[NW], wy[NW];  // keys r0 and r0 + 8
+          lds_words<D / 8>(kc + 2 * u * half, wx);
+          lds_words<D / 8>(kc + (2 * u + 1) * half, wy);
+          const uint32_t sx = lds_short<D / 64>(ks + 2 * u * half), sy = lds_short<D / 64>(ks + (2 * u + 1) * half);
           const uint32_t hx = pkv::e4m3x2_to_f16x2(sx), hy = pkv::e4m3x2_to_f16x2(sy);  // the quarter's groups
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[u][e] = 0.f;
@@ -279,12 +286,8 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
             }
           }
         }
-        // scores of keys r0 (e = 0, 1) and r0 + 8 (2, 3) of each chunk for rows 2c and 2c + 1
+        // raw scores of keys r0 (e = 0, 1) and r0 + 8 (2, 3) of each chunk for rows 2c and 2c + 1
         float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int u = 0; u < kQ4Sub; ++u)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[u][e] *= mul[e & 1];
         const bool partial = nv < kQ4Chunk;
         if (partial || (kVar && t + tw0 + kQ4Chunk > seg.ctx - seg.nq)) {
 #pragma unroll
@@ -299,6 +302,8 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
         for (int u = 0; u < kQ4Sub; ++u)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], x[u][e]);
+        top[0] *= mul[0];
+        top[1] *= mul[1];
         if (__any_sync(0xffffffffu, top[0] > limit[0] || top[1] > limit[1])) {
           // (a row moves by its own scores only)
 #pragma unroll
@@ -311,6 +316,7 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
               limit[i] = mx + kRescale;
               base[i] = mx - kWeightLog2;
               l[i] *= corr;
+              l[2 + i] *= corr;
 #pragma unroll
               for (int j = 0; j < NO; ++j) {
                 o[j][i] *= corr;
@@ -324,15 +330,17 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
         for (int u = 0; u < kQ4Sub; ++u)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            pf[u][i] = pkv::pack_f16x2(pkv::ex2(x[u][2 * i] - base[0]), pkv::ex2(x[u][2 * i + 1] - base[1]));
-            add_halves(pf[u][i], l[0], l[1]);
-            pf[u][i] = movmatrix(pf[u][i]);
+            pf[u][i] = movmatrix(pkv::pack_f16x2(pkv::ex2(fmaf(x[u][2 * i], mul[0], -base[0])),
+                                                 pkv::ex2(fmaf(x[u][2 * i + 1], mul[1], -base[1]))));
           }
 #pragma unroll
         for (int u = 0; u < kQ4Sub; ++u) {
-          const unsigned char* vr = vs + u * 16 * row_bytes;
-          uint32_t s_ab = vr[v_a + v_scales] + vr[v_b + v_scales] * 256u;
-          uint32_t s_cd = vr[v_a + half + v_scales] + vr[v_b + half + v_scales] * 256u;
+          constexpr uint32_t kOnes = 0x3c003c00u;
+          mma_q4(l, kOnes, kOnes, kOnes, kOnes, pf[u][0], pf[u][1]);
+          const uint32_t va_at = vs + v_a, vb_at = vs + v_b;
+          const int lo = 2 * u * half, hi = lo + half;
+          uint32_t s_ab = lds_short<1>(va_at + v_scales + lo) + lds_short<1>(vb_at + v_scales + lo) * 256u;
+          uint32_t s_cd = lds_short<1>(va_at + v_scales + hi) + lds_short<1>(vb_at + v_scales + hi) * 256u;
           if (partial) {  // rows past the last key hold anything: scale 0 makes their values 0
             const int n = nv - 16 * u;
             s_ab &= (va < n ? 0x00ffu : 0u) | (vb < n ? 0xff00u : 0u);
@@ -340,16 +348,10 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
           }
           const pkv::Q4Scale kab(pkv::e4m3x2_to_f16x2(s_ab)), kcd(pkv::e4m3x2_to_f16x2(s_cd));
           uint32_t wv[4][NW / 2];
-          const int v_off[4] = {v_a, v_b, v_a + half, v_b + half};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if constexpr (D == 128) {
-              const uint2 z = *reinterpret_cast<const uint2*>(vr + v_off[y] + v_codes);
-              wv[y][0] = z.x, wv[y][1] = z.y;
-            } else {
-              wv[y][0] = *reinterpret_cast<const uint32_t*>(vr + v_off[y] + v_codes);
-            }
-          }
+          lds_words<D / 16>(va_at + v_codes + lo, wv[0]);
+          lds_words<D / 16>(vb_at + v_codes + lo, wv[1]);
+          lds_words<D / 16>(va_at + v_codes + hi, wv[2]);
+          lds_words<D / 16>(vb_at + v_codes + hi, wv[3]);
 #pragma unroll
           for (int w = 0; w < NW / 2; ++w)
 #pragma unroll
@@ -366,16 +368,13 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
       }
       __syncwarp();
       if (lane == 0) pkv::mbar_arrive(&empty[stage]);
+      at += stage_bytes;
       if (++stage == p.stages) {
         stage = 0;
+        at = ring;
         parity ^= 1u;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
-
     float m[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) m[i] = limit[i] == -INFINITY ? -INFINITY : base[i] + kWeightLog2;
@@ -431,7 +430,7 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
     }
     // the result (whole sequence) or this part's state; V's scale comes off here (the weights' 2^7 cancels against l)
     if (phase == 0) {
-      const float vscale = p.v_scale * 4.f;
+      const float vscale = p.v_scale * pkv::kQ4Unit;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int row = 2 * c + i;
@@ -474,14 +473,16 @@ int launch_q4(Params& p, int sms, cudaStream_t stream) {
   p.nw = p.hkv * p.wph;
   p.t_stage = kQ4Chunk * p.wph;
   p.stage_bytes = static_cast<size_t>(p.t_stage) * row * 2;
-  p.align = 1;
+  p.align = kQ4Align;
   const size_t misc = 2 * kQ4Stages * sizeof(uint64_t) + 64 * sizeof(long long) + 32 * sizeof(int) +
                       static_cast<size_t>(p.nw - p.hkv) * R * (D + 2) * sizeof(float);
   p.stages = std::min<int>(kQ4Stages, static_cast<int>((kQ4Smem - misc) / p.stage_bytes));
   if (p.stages < 2) return PKV_EUNSUPPORTED;
-  auto kernel = paged_decode_q4_kernel<G, QL, D, kVar>;
-  static std::atomic<uint64_t> smem_allowed{0};  // the limit for every number of KV heads
-  if (pkv::allow_smem(kernel, kQ4Smem, smem_allowed) != cudaSuccess) return PKV_ECUDA;
+  // (chunks gain nothing from it)
+  const bool eight = !kVar && p.hkv == 8;
+  auto kernel = eight ? paged_decode_q4_kernel<G, QL, D, kVar, kVar ? 0 : 8> : paged_decode_q4_kernel<G, QL, D, kVar, 0>;
+  static std::atomic<uint64_t> smem_allowed[2];
+  if (pkv::allow_smem(kernel, kQ4Smem, smem_allowed[eight]) != cudaSuccess) return PKV_ECUDA;
   const unsigned grid = p.num_splits > 0 ? static_cast<unsigned>(static_cast<long long>(p.batch) * p.num_splits)
                                          : static_cast<unsigned>(sms * kAutoCtasPerSm);
   if (grid == 0) return PKV_OK;
@@ -489,6 +490,58 @@ int launch_q4(Params& p, int sms, cudaStream_t stream) {
                  cudaSuccess
              ? PKV_OK
              : PKV_ECUDA;
+}
+
+template <int D, bool kVar>
+int dispatch_q4(Params& p, int group, int sms, cudaStream_t stream) {
+  switch (group) {
+    case 1: return launch_q4<1, kVar ? kChunkRows : 1, D, kVar>(p, sms, stream);
+    case 2: return launch_q4<2, kVar ? kChunkRows / 2 : 1, D, kVar>(p, sms, stream);
+    case 4: return launch_q4<4, kVar ? kChunkRows / 4 : 1, D, kVar>(p, sms, stream);
+    default: return launch_q4<8, 1, D, kVar>(p, sms, stream);
+  }
+}
+
+template <int D>
+int run_q4(const pkv::Q4Decode& a, cudaStream_t stream) {
+  const bool chunk = a.cu_q != nullptr;
+  pkv::DeviceInfo info;
+  if (pkv::device_info(&info) != PKV_OK) return PKV_ECUDA;
+  Params p{};
+  size_t off_o = 0, off_ml = 0;
+  const size_t need = workspace_layout(a.batch, chunk ? kChunkRows * a.hkv : a.hq, D, a.num_splits, info.sms, &off_o, &off_ml);
+  if (need > 0) {
+    if (!a.workspace || a.workspace_bytes < need) return PKV_EWORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(a.workspace) & 255u) != 0) return PKV_EALIGN;
+    unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+    p.counters = reinterpret_cast<int32_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(ws + off_o);
+    p.part_ml = reinterpret_cast<float*>(ws + off_ml);
+  }
+  p.out = a.out;
+  p.q = a.q;
+  p.k_cache = static_cast<const unsigned char*>(a.k_cache);
+  p.v_cache = static_cast<const unsigned char*>(a.v_cache);
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  p.err = a.err;
+  p.max_blocks = a.max_blocks;
+  p.batch = a.batch;
+  p.hq = a.hq;
+  p.ql = 1;
+  p.hkv = a.hkv;
+  p.block_size = a.block_size;
+  p.num_blocks = a.num_blocks;
+  p.scale_log2 = a.scale * pkv::kLog2e * a.k_scale;
+  p.v_scale = a.v_scale;
+  p.num_splits = a.num_splits;
+  p.cu_q = a.cu_q;
+  p.cu_k = a.cu_k;
+  p.total_q = a.total_q;
+  p.max_seqlen_q = a.max_seqlen_q;
+  p.causal = a.causal;
+  const int group = a.hq / a.hkv;
+  return chunk ? dispatch_q4<D, true>(p, group, info.sms, stream) : dispatch_q4<D, false>(p, group, info.sms, stream);
 }
 
 }  // namespace

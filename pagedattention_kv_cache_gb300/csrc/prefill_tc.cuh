@@ -1544,7 +1544,7 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
     p.tanh_poly = make_tanh_poly(a.mod.cap_log2, a.mod.raw_to_x);
   p.bias_mul = kForm == kBiased ? 1.f / a.scale : kLog2e;
   if constexpr (quantized(kForm)) {
-    constexpr float kUp = kQ4 ? 4.f : 1.f;  // (widened 4-bit rows hold a quarter of the values)
+    constexpr float kUp = kQ4 ? kQ4Unit : 1.f;
     p.scale_log2 *= a.k_scale * kUp;
     p.v_scale = a.v_scale * kUp;
     p.k_codes = static_cast<const unsigned char*>(a.k_cache);

@@ -135,6 +135,71 @@ def test_rope_store_q4(n, hq, hkv, d, rot, interleaved):
     assert np.array_equal(gv.cpu().numpy(), oq.store(vc.numpy(), as_np(v), slots.numpy(), T_V))
 
 
+MANY = [(1500, 16, 8, 128, 128, 3), (2100, 5, 3, 96, 64, 1), (900, 2, 2, 512, 256, 1), (1111, 40, 5, 64, 32, 2),
+        (4100, 8, 1, 64, 64, 1), (1400, 7, 7, 32, 32, 1), (160000, 1, 1, 32, 32, 50)]
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,rot,every", MANY)
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "e4m3", "q4"])
+def test_many_tokens_as_few_at_a_time(n, hq, hkv, d, rot, every, fmt):
+    """Large calls, which take other kernels, give bit for bit what calls of 100 tokens give."""
+    if fmt == "q4" and d not in (64, 128):
+        pytest.skip("4-bit rows have heads of 64 or 128")
+    dtype = torch.float32 if fmt == "f32" else torch.bfloat16
+    gen, q, k, v, pos, table = _inputs(n, n, hq, hkv, d, dtype, fused=n % 2 == 0, rot=rot)
+    q[5, 0, 3], k[6, 0, 1], k[7, 0, 0] = float("inf"), float("nan"), 3e38
+    nb, bs = n // 8 + 2, 8
+    slots = _slots(gen, n, nb * bs, 7)
+    slots[n // 2], pos[n // 3] = nb * bs, 500
+    row = oq.row_bytes(hkv, d) if fmt == "q4" else hkv * d * {"f32": 4, "bf16": 2, "e4m3": 1}[fmt]
+    pools = [torch.randint(0, 120, (nb, bs, row), generator=gen, dtype=torch.uint8).cuda() for _ in range(2)]
+    pools += [x.clone() for x in pools]
+    table, pos, slots = torch.from_numpy(table).cuda(), pos.cuda(), slots.cuda()
+
+    def call(kc, vc, a, b, interleaved, q_out):
+        args = (q[a:b], k[a:b], v[a:b], pos[a:b], table)
+        if fmt == "q4":
+            pkv.kv_rope_store_q4(*args, kc, vc, slots[a:b], T_K, T_V, interleaved=interleaved, q_out=q_out)
+            return
+        kc, vc = [x if fmt == "e4m3" else x.view(dtype) for x in (kc, vc)]
+        kc, vc = [x.view(nb, bs, hkv, d) for x in (kc, vc)]
+        if fmt == "e4m3":
+            pkv.kv_rope_store_fp8(*args, kc, vc, slots[a:b], T_K, T_V, interleaved=interleaved, q_out=q_out)
+        else:
+            pkv.kv_rope_store(*args, kc, vc, slots[a:b], interleaved=interleaved, q_out=q_out)
+
+    pkv.device_error(reset=True)
+    for interleaved in (False, True):
+        whole, parts = torch.full((n, hq, d), 7.0, dtype=dtype).cuda(), torch.full((n, hq, d), 7.0, dtype=dtype).cuda()
+        call(pools[0], pools[1], 0, n, interleaved, whole)
+        assert pkv.device_error() == _lib.DERR_SLOT_RANGE | _lib.DERR_POSITION_RANGE
+        near = [(a, min(n, a + 100)) for a in range(0, n, 100)][::every]
+        for a, b in near:
+            call(pools[2], pools[3], a, b, interleaved, parts[a:b])
+        torch.cuda.synchronize()
+        pkv.device_error(reset=True)
+        rows = torch.cat([torch.arange(a, b) for a, b in near]).cuda()
+        bits = torch.int32 if fmt == "f32" else torch.int16
+        assert torch.equal(whole[rows].view(bits), parts[rows].view(bits))
+        to = slots[rows]
+        to = to[(to >= 0) & (to < nb * bs)].long()
+        for x, y in ((0, 2), (1, 3)):
+            assert torch.equal(pools[x].view(-1, row)[to], pools[y].view(-1, row)[to])
+
+
+@pytest.mark.parametrize("hkv,d,n", [(8, 128, 1500), (1, 64, 12000), (3, 64, 4097)])
+def test_many_rows_loaded(hkv, d, n):
+    gen = torch.Generator().manual_seed(n)
+    kc, vc = [torch.randint(0, 127, (n // 8 + 1, 8, oq.row_bytes(hkv, d)), generator=gen, dtype=torch.uint8).cuda()
+              for _ in range(2)]
+    slots = _slots(gen, n, (n // 8 + 1) * 8, 9).cuda()
+    k, v = pkv.kv_load_q4(kc, vc, slots, T_K, T_V, hkv, d)
+    for a in range(0, n, 300):
+        part = pkv.kv_load_q4(kc, vc, slots[a:a + 300], T_K, T_V, hkv, d)
+        assert torch.equal(k[a:a + 300], part[0]) and torch.equal(v[a:a + 300], part[1])
+    assert pkv.device_error() == 0
+
+
 @pytest.mark.parametrize("hkv,d", [(1, 64), (8, 128), (3, 64), (5, 128)])
 @pytest.mark.parametrize("t", [1.0, 3.0 / 256, 0.37, 1e-30, 1e30])
 def test_store_and_load_q4(hkv, d, t):
