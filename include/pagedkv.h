@@ -550,7 +550,7 @@ int pkv_kv_store_q4(const void* k, const void* v, void* k_cache, void* v_cache,
 /*
  * kv_load_q4: the rows at slot_mapping read back from a 4-bit cache as bf16
  * [num_tokens, num_kv_heads, head_dim] (a prefix moved to another cache or to
- * the host).  The value (code - 8) * (scale * T) in float32, rounded to bf16.
+ * the host).  (code - 8) * scale is exact; times T in float32, rounded to bf16.
  * Slot -1 gives a row of zeros; a slot outside the cache too, and raises
  * PKV_DERR_SLOT_RANGE.
  */

@@ -575,8 +575,8 @@ __global__ void __launch_bounds__(256) kv_load_q4_kernel(const LoadArgs a, int l
       for (int e = 0; e < 4; ++e) {
         const uint32_t whole = pkv::hmul2(f[e], 0x54005400u);
         const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&whole));
-        x[e] = valid ? __fmul_rn(y.x, tensor) : 0.f;
-        x[e + 4] = valid ? __fmul_rn(y.y, tensor) : 0.f;
+        x[e] = __fmul_rn(y.x, tensor);
+        x[e + 4] = __fmul_rn(y.y, tensor);
       }
       __nv_bfloat16* dst = (is_v ? a.v : a.k) + (static_cast<int64_t>(token) * a.hkv + head) * a.head_dim;
       reinterpret_cast<uint4*>(dst)[j] = Chunk<__nv_bfloat16>::pack(x);

@@ -61,6 +61,9 @@
 //          copy).  The four pairs of a code word are stored as they come out,
 //          elements (0, 4), (1, 5), (2, 6), (3, 7): the rewritten Q has the same
 //          order, the epilogue undoes it for V.
+//          A batch of 16 chunks, 56 GFLOP, 85 us (the E4M3 form 70): in copies of the
+//          kernel 76 without the loads, 72 without the widening, 66 without both.
+//          (Rows copied by their own lanes, 16 bytes at a time, 91.)
 #pragma once
 
 #include <algorithm>
@@ -719,23 +722,31 @@ __global__ void __launch_bounds__(threads(kForm), 1)
     const int row_bytes = q4_row_bytes(p.hkv, D);
     const int scale_at = q4_scale_offset(p.hkv, D) + g * (D / 16);
     unsigned char* const ring = smem + Geo<D>::kInt4Offset + me * (kInt4Depth * Geo<D>::kInt4Slot);
-    // the block of this lane's key of a unit (-1: no such key), looked up a unit before it is copied
+    // the block of this lane's key of a unit (-1: no such key) is looked up a unit before its copy
     auto key_of = [&](int u) { return (j0 + (u >> 3)) * kBN + (u & 3) * kQuarter + lane; };
     auto block_of = [&](int key) {
       return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(key)) * p.block_mul >> p.block_shift);
     };
     // where chunk ch of row r lies in the ring: eight rows' same chunks (and eight neighbouring chunks) differ modulo 128 bytes
     auto swizzle = [](int r) { return kChunks == 4 ? (r >> 1) & 3 : (r >> 2) & 1; };
-    auto look_up = [&](int u) { return u < n_units && key_of(u) < nk ? __ldg(table + block_of(key_of(u))) : -1; };
-    int phys = look_up(me);
+    int phys = -1, in_block = 0;
+    auto look_up = [&](int u) {
+      const int key = key_of(u);
+      phys = -1;
+      if (u < n_units && key < nk) {
+        const int blk = block_of(key);
+        in_block = key - blk * p.block_size;
+        phys = __ldg(table + blk);
+      }
+    };
+    look_up(me);
     int slot = 0;  // of the next unit to copy
     // rows of no key and of bad blocks are filled with zeros
     auto copy = [&](int u) {
       if (u < n_units) {
-        const int key = key_of(u);
         const bool ok = phys >= 0 && phys < p.num_blocks;
-        if (key < nk && !ok) raise_error(p.err, PKV_DERR_BLOCK_RANGE);
-        const int row = ok ? phys * p.block_size + (key - block_of(key) * p.block_size) : -1;
+        if (!ok && key_of(u) < nk) raise_error(p.err, PKV_DERR_BLOCK_RANGE);
+        const int row = ok ? phys * p.block_size + in_block : -1;
         const unsigned char* pool = u & 4 ? p.v_codes : p.k_codes;
         const uint32_t to = smem_u32(ring + slot * Geo<D>::kInt4Slot);
         // neighbouring lanes take the chunks of one row
@@ -755,7 +766,7 @@ __global__ void __launch_bounds__(threads(kForm), 1)
                      : "memory");
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      phys = look_up(u + kWorkers);
+      look_up(u + kWorkers);
       slot = slot + 1 == kInt4Depth ? 0 : slot + 1;
     };
 #pragma unroll

@@ -113,6 +113,8 @@ __device__ __forceinline__ uint2 e4m3_codes8(const float (&x)[8], float scale) {
       const uint64_t q = quotient2(pair(x[i], x[i + 1]), scale, inv);
       nan = fma2(q, 0ull, nan);
       split(q, y[i], y[i + 1]);
+      y[i] = copysignf(y[i], x[i]);  // (the correction of a zero loses its sign)
+      y[i + 1] = copysignf(y[i + 1], x[i + 1]);
     }
     float n0, n1;
     split(nan, n0, n1);

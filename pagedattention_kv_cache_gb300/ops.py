@@ -11,6 +11,7 @@ in the library's CUDA kernels; nothing here computes.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -31,6 +32,11 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, ndim=None, device=None, shape=None) -> None:
+    # (each question to a tensor takes 0.1 us of a call's host time, so the usual answer is looked for first)
+    if (device is not None and isinstance(t, torch.Tensor) and t.get_device() == device.index and t.is_contiguous()
+            and (dtype is None or t.dtype is dtype) and (ndim is None or t.dim() == ndim)
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -50,8 +56,10 @@ def _need(t: torch.Tensor, name: str, dtype=None, ndim=None, device=None, shape=
 def _device(t: torch.Tensor, name: str) -> torch.device:
     """The device every argument of a call must be on: the current CUDA device, where the
     library launches its kernels."""
-    _need(t, name)
     cur = torch.cuda.current_device()
+    if isinstance(t, torch.Tensor) and t.get_device() == cur and t.is_contiguous():
+        return t.device
+    _need(t, name)
     if t.device.index != cur:
         raise ValueError(f"{name} is on {t.device} but the current CUDA device is cuda:{cur}")
     return t.device
@@ -549,6 +557,7 @@ def paged_varlen_prefill_attn_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     return out
 
 
+@functools.lru_cache(maxsize=64)
 def q4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
     """Bytes of a token's row in a 4-bit K (or V) cache; head_dim 64 or 128."""
     n = int(_lib.load().pkv_q4_row_bytes(num_kv_heads, head_dim))
@@ -560,7 +569,7 @@ def q4_row_bytes(num_kv_heads: int, head_dim: int) -> int:
 def q4_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
     """A zero-filled 4-bit K (or V) cache, uint8 [num_blocks, block_size, q4_row_bytes]; it reads as zeros."""
     return torch.zeros(num_blocks, block_size, q4_row_bytes(num_kv_heads, head_dim), dtype=torch.uint8,
-                       device=device or torch.cuda.current_device())
+                       device=torch.cuda.current_device() if device is None else device)
 
 
 def _need_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, num_kv_heads: int, head_dim: int, device) -> None:
@@ -595,32 +604,36 @@ def kv_load_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch
     _need(slot_mapping, "slot_mapping", dtype=torch.int32, ndim=1, device=dev)
     n, (nb, bs, _) = slot_mapping.shape[0], k_cache.shape
     handle = _stream(stream, dev)
-    with torch.cuda.stream(stream):  # (None: the current one)
+    if stream is None:
         k, v = [torch.empty(n, num_kv_heads, head_dim, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    else:
+        with torch.cuda.stream(stream):
+            k, v = [torch.empty(n, num_kv_heads, head_dim, dtype=torch.bfloat16, device=dev) for _ in range(2)]
     st = _lib.load().pkv_kv_load_q4(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n, nb, bs,
                                     num_kv_heads, head_dim, k_scale, v_scale, handle)
     _lib.check("pkv_kv_load_q4", st)
     return k, v
 
 
-def _need_rows(t: torch.Tensor, name: str, dtype, device) -> int:
-    """Checks rows [N, heads, D] whose heads are contiguous; returns the stride from one token to the next."""
+def _need_rows(t: torch.Tensor, name: str, dtype, device):
+    """Checks rows [N, heads, D] whose heads are contiguous; returns their shape and the stride from one token to the next."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 3:
+            n, heads, d = shape
+            if (d > 1 and stride[2] != 1) or (heads > 1 and stride[1] != d):
+                raise ValueError(f"{name}'s heads must be contiguous")
+            if n <= 1:
+                return shape, heads * d
+            if stride[0] < heads * d:
+                raise ValueError(f"{name}'s rows overlap")
+            return shape, stride[0]
+        raise ValueError(f"{name} must have 3 dims, got {len(shape)}")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.get_device() != device.index:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
-    n, heads, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}'s heads must be contiguous")
-    if n <= 1:
-        return heads * d
-    if t.stride(0) < heads * d:
-        raise ValueError(f"{name}'s rows overlap")
-    return t.stride(0)
+    raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
 def _rope_store(fn: str, q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, fmt: int, k_scale: float,
@@ -630,41 +643,46 @@ def _rope_store(fn: str, q, k, v, positions, cos_sin, k_cache, v_cache, slot_map
     dev = q.device
     if dev.index != torch.cuda.current_device():
         raise ValueError(f"q is on {dev} but the current CUDA device is cuda:{torch.cuda.current_device()}")
-    dtype = q.dtype if fmt == _lib.CACHE_SAME else torch.bfloat16
     code = _dtype_code(q)
-    qs, ks, vs = _need_rows(q, "q", dtype, dev), _need_rows(k, "k", dtype, dev), _need_rows(v, "v", dtype, dev)
-    n, hq, d = q.shape
-    hkv = k.shape[1]
-    if k.shape != (n, hkv, d) or v.shape != k.shape:
+    dtype = q.dtype if fmt == _lib.CACHE_SAME else torch.bfloat16
+    (q_shape, qs), (k_shape, ks), (v_shape, vs) = [_need_rows(t, name, dtype, dev)
+                                                   for t, name in ((q, "q"), (k, "k"), (v, "v"))]
+    n, hq, d = q_shape
+    hkv = k_shape[1]
+    if k_shape != (n, hkv, d) or v_shape != k_shape:
         raise ValueError("expected q [N, Hq, D] and k, v [N, Hkv, D]")
-    _need(positions, "positions", dtype=torch.int32, device=dev, shape=(n,))
-    _need(slot_mapping, "slot_mapping", dtype=torch.int32, device=dev, shape=(n,))
-    _need(cos_sin, "cos_sin", dtype=torch.float32, ndim=2, device=dev)
+    _need(positions, "positions", torch.int32, None, dev, (n,))
+    _need(slot_mapping, "slot_mapping", torch.int32, None, dev, (n,))
+    _need(cos_sin, "cos_sin", torch.float32, 2, dev)
     if fmt == _lib.CACHE_Q4:
         _need_q4(k_cache, v_cache, hkv, d, dev)
     else:
-        _need(k_cache, "k_cache", ndim=4, device=dev)
-        _need(v_cache, "v_cache", dtype=k_cache.dtype, device=dev, shape=k_cache.shape)
-        if fmt == _lib.CACHE_SAME and k_cache.dtype != dtype:
-            raise TypeError(f"k_cache must be {dtype}, got {k_cache.dtype}")
-        if fmt == _lib.CACHE_E4M3 and k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        _need(k_cache, "k_cache", None, 4, dev)
+        cache_dtype, cache_shape = k_cache.dtype, k_cache.shape
+        _need(v_cache, "v_cache", cache_dtype, None, dev, cache_shape)
+        if fmt == _lib.CACHE_SAME and cache_dtype != dtype:
+            raise TypeError(f"k_cache must be {dtype}, got {cache_dtype}")
+        if fmt == _lib.CACHE_E4M3 and cache_dtype not in (torch.uint8, torch.float8_e4m3fn):
             raise TypeError("k_cache must hold E4M3 codes (uint8 or float8_e4m3fn)")
-        if k_cache.shape[2:] != k.shape[1:]:
+        if cache_shape[2:] != k_shape[1:]:
             raise ValueError("k/v rows and the cache disagree on (Hkv, D)")
     handle = _stream(stream, dev)
     if q_out is None:
         if stream is None:
-            q_out = torch.empty((n, hq, d), dtype=dtype, device=dev)
+            q_out = torch.empty(q_shape, dtype=dtype, device=dev)
         else:
             with torch.cuda.stream(stream):
-                q_out = torch.empty((n, hq, d), dtype=dtype, device=dev)
+                q_out = torch.empty(q_shape, dtype=dtype, device=dev)
     else:
-        _need(q_out, "q_out", dtype=dtype, device=dev, shape=q.shape)
+        _need(q_out, "q_out", dtype, None, dev, q_shape)
+    max_position, rot_dim = cos_sin.shape
+    blocks, block_size = k_cache.shape[:2]
     st = _lib.load().pkv_kv_rope_store(
-        _ptr(q_out), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
-        cos_sin.shape[1], 1 if interleaved else 0, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n, k_cache.shape[0],
-        k_cache.shape[1], hq, hkv, d, fmt, k_scale, v_scale, code, handle)
-    _lib.check(fn, st)
+        q_out.data_ptr(), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), cos_sin.data_ptr(),
+        max_position, rot_dim, 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n,
+        blocks, block_size, hq, hkv, d, fmt, k_scale, v_scale, code, handle)
+    if st != _lib.OK:
+        _lib.check(fn, st)
     return q_out
 
 

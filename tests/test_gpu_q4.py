@@ -287,6 +287,67 @@ def test_bad_lengths_and_blocks_raise_bits(max_q):
     assert pkv.device_error() == _lib.DERR_LEN_RANGE and not out[0].any()
 
 
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 1e-42, 3.0])
+def test_decode_scales(scale):
+    decode_case(31, [0, 1, 700, 64, 65], 16, 8, 2, 128, scale=scale)
+    decode_case(32, [900, 3], 16, 2, 4, 64, scale=scale, splits=2)
+
+
+def test_rows_past_32_bits_of_bytes():
+    """A pool of 4.5 GB: its last blocks give what the same rows give in a small pool, bit for bit."""
+    hkv, d, bs, n, hq = 8, 128, 256, 1000, 16
+    row = oq.row_bytes(hkv, d)
+    blocks = (9 << 29) // (row * bs)
+    gen = torch.Generator().manual_seed(5)
+    k, v = [torch.randn(n, hkv, d, generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+    q = torch.randn(n, hq, d, generator=gen).to(torch.bfloat16).cuda()
+    cu_q = torch.tensor([0, 300], dtype=torch.int32).cuda()
+    cu_k = torch.tensor([0, n], dtype=torch.int32).cuda()
+    lens = torch.tensor([n, n - 1], dtype=torch.int32).cuda()
+    results = []
+    for pool_blocks in (5, blocks):
+        pools = [torch.zeros(pool_blocks, bs, row, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        order = pool_blocks - 1 - torch.tensor([2, 0, 3, 1])
+        slots = (order[torch.arange(n) // bs] * bs + torch.arange(n) % bs).int().cuda()
+        bt = order.int()[None].cuda()
+        pkv.kv_store_q4(k, v, *pools, slots, T_K, T_V)
+        results.append((*pkv.kv_load_q4(*pools, slots, T_K, T_V, hkv, d),
+                        pkv.paged_decode_attn_q4(q[:2], *pools, bt.repeat(2, 1), lens, 0.1, T_K, T_V, hkv),
+                        pkv.paged_varlen_prefill_attn_q4(q[:300], *pools, bt, cu_q, cu_k, 300, n, 0.1, T_K, T_V, hkv)))
+        assert pkv.device_error() == 0
+        del pools
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_refusals_of_the_binding():
+    hkv, d = 2, 64
+    kp, vp = pkv.q4_cache(4, 16, hkv, d), pkv.q4_cache(4, 16, hkv, d)
+    q = torch.zeros(2, 4, d, dtype=torch.bfloat16, device="cuda")
+    bt, cl = torch.zeros(2, 2, dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+
+    def decode(q=q, kp=kp, vp=vp, bt=bt, cl=cl, hkv=hkv, **kw):
+        return pkv.paged_decode_attn_q4(q, kp, vp, bt, cl, 0.1, T_K, T_V, hkv, **kw)
+
+    def chunk(q=q, kp=kp, vp=vp, bt=bt, cl=cu, hkv=hkv, **kw):
+        return pkv.paged_varlen_prefill_attn_q4(q, kp, vp, bt, cl, cl, 1, 1, 0.1, T_K, T_V, hkv, **kw)
+
+    for call in (decode, chunk):
+        assert not call().any()
+        for kw in (dict(q=q.cpu()), dict(q=q[0]), dict(q=q.transpose(0, 1)), dict(kp=kp[:2]), dict(vp=vp[..., :64]), dict(hkv=4),
+                   dict(bt=bt[:1]), dict(bt=bt[0]), dict(out=q[:1]), dict(kp=kp.cpu())):
+            with pytest.raises(ValueError):
+                call(**kw)
+        for kw in (dict(q=q.float()), dict(kp=kp.view(torch.int8)), dict(bt=bt.long()), dict(cl=cl.long()),
+                   dict(out=torch.zeros(2, 4, d, device="cuda"))):
+            with pytest.raises(TypeError):
+                call(**kw)
+    with pytest.raises(_lib.PagedKVError):
+        decode(q=torch.zeros(2, 6, d, dtype=torch.bfloat16, device="cuda"))
+    assert pkv.device_error() == 0
+
+
 def test_a_serving_run():
     """Prompt, decode steps and drafted tokens with the rotating store, eager and captured, against the oracle."""
     hq, hkv, d, bs, base = 4, 2, 128, 16, 10000.0

@@ -114,6 +114,25 @@ def test_rope_store_fp8(n, hq, hkv, d, rot, interleaved):
     assert np.array_equal(gk.cpu().numpy(), wk) and np.array_equal(gv.cpu().numpy(), wv)
 
 
+@pytest.mark.parametrize("t", [1.0, 3.0 / 256, 1e-30, 1e30])
+@pytest.mark.parametrize("n", [70, 2500])
+def test_fp8_codes_are_those_of_kv_store_fp8(t, n):
+    """Every bf16 value of both signs, infinities and NaN, at scales that leave the quotient's range too."""
+    hkv, d, hq = 8, 128, 2
+    values = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    gen = torch.Generator().manual_seed(n)
+    v = values[torch.randint(0, 65536, (n, hkv, d), generator=gen)]
+    v.view(-1)[:65536] = values
+    v = v.cuda()
+    q, k = [torch.randn(n, h, d, generator=gen).to(torch.bfloat16).cuda() for h in (hq, hkv)]
+    table = torch.from_numpy(md.rope_cos_sin(10, d, 1e4)).cuda()
+    slots = torch.randperm(n, generator=gen).int().cuda()
+    pools = [torch.zeros(n, 1, hkv, d, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    pkv.kv_rope_store_fp8(q, k, v, slots % 10, table, pools[0], pools[1], slots, t, t)
+    pkv.kv_store_fp8(k, v, pools[2], pools[3], slots, t, t)
+    assert torch.equal(pools[1], pools[3]) and pkv.device_error() == 0
+
+
 Q4_SHAPES = [(7, 16, 8, 128, 128), (1, 1, 1, 64, 64), (33, 8, 1, 64, 32), (50, 6, 3, 128, 96), (31, 10, 5, 64, 64),
              (300, 2, 2, 128, 32)]
 
@@ -224,7 +243,7 @@ def test_store_and_load_q4(hkv, d, t):
         with np.errstate(over="ignore"):
             want = _bf16(oq.values(pool.reshape(nb * bs, -1)[slots.numpy()], hkv, d, t))
         want[slots.numpy() < 0] = 0
-        # (code - 8) times the float32 step is rounded once more: an element may fall on bf16's other neighbour only
+        # the value times T is rounded to float32 before bf16: an element may fall on bf16's other neighbour only
         # where the exact value lies within 2^-23 of the middle, which the comparison allows as one bf16 step
         got = as_np(got)
         same = (got == want) | (np.isnan(got) & np.isnan(want))
