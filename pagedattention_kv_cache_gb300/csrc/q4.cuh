@@ -162,13 +162,20 @@ struct Q4Scale {
   __device__ __forceinline__ explicit Q4Scale(uint32_t pair)
       : s(pair), low(hmul2(pair, 0xcc08cc08u)), high(hmul2(pair, 0xbc80bc80u)) {}
 };
+// (a & b) | c
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 // The four f16 pairs of a word: nibbles (0, 4), (1, 5), (2, 6) and (3, 7), as (n - 8) / 64 times the scale pair.
 __device__ __forceinline__ void widen_q4(uint32_t w, const Q4Scale& k, uint32_t (&f)[4]) {
-  const uint32_t y = w >> 8;
-  f[0] = hfma2((w & 0x000f000fu) | 0x4c004c00u, k.s, k.low);
-  f[1] = hfma2((w & 0x00f000f0u) | 0x3c003c00u, k.s, k.high);
-  f[2] = hfma2((y & 0x000f000fu) | 0x4c004c00u, k.s, k.low);
-  f[3] = hfma2((y & 0x00f000f0u) | 0x3c003c00u, k.s, k.high);
+  uint32_t y;
+  asm("shr.u32 %0, %1, 8;" : "=r"(y) : "r"(w));
+  f[0] = hfma2(and_or(w, 0x000f000fu, 0x4c004c00u), k.s, k.low);
+  f[1] = hfma2(and_or(w, 0x00f000f0u, 0x3c003c00u), k.s, k.high);
+  f[2] = hfma2(and_or(y, 0x000f000fu, 0x4c004c00u), k.s, k.low);
+  f[3] = hfma2(and_or(y, 0x00f000f0u, 0x3c003c00u), k.s, k.high);
 }
 
 }  // namespace pkv
