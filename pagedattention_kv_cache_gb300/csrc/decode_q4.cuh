@@ -3,7 +3,7 @@
 // decode_plan.cuh's.
 //
 // Bound: instructions, then HBM (each token's K and V row once, 576 bytes each with
-// 8 KV heads of 128).  256 sequences of 1k-8k tokens, 1.30 GB: 277 us, 4.7 TB/s; in
+// 8 KV heads of 128).  256 sequences of 1k-8k tokens, 1.30 GB: 237 us, 5.5 TB/s; in
 // copies of the kernel the stream alone takes 188 us, with only one of the two
 // products 191-193.  At 4.5 bits an element the way from codes to matrix operands
 // is what the kernel is built around:
@@ -20,8 +20,8 @@
 //    row maximum is a reference only: it moves when a score passes it by 2^8
 //    (a vote per stage), so the usual stage takes no maximum across lanes.  The row
 //    sums are a product of ones with the weights.
-//  * Eight warps with four chunks of 16 keys each per stage: two chunks 308-325 us, one
-//    339, three 302; 16 warps with two 295 (they spill at 112 registers), with one 331.
+//  * Eight warps with four chunks of 16 keys each per stage: three chunks 244 us, two 258,
+//    one 337 (four 235 in that measurement); 16 warps at 112 registers with two 250.
 //  * Which token stands in which fragment row is free as long as K and V agree;
 //    token_of spreads the rows over the banks.
 // q enters as f16 after a power-of-two scaling of each row (as in the FP8 kernel);
@@ -39,10 +39,13 @@ constexpr int kQ4Stages = 6;  // at most
 constexpr int kQ4Smem = 224 * 1024;
 constexpr int kQ4Sub = 4;     // chunks of 16 keys per consumer warp and stage: their products overlap
 constexpr int kQ4Chunk = 16 * kQ4Sub;
-// Split points fall on multiples of this many tokens: with parts of a few tokens
-// their merge costs more than it saves (4 sequences of 32k-131k: 102 us at 1, 100 at 64
-// and at 128, 104 at 256; one of 777 14.7 up to 128, 19 at 256).
-constexpr int kQ4Align = 128;
+// Split points fall on multiples of this many tokens: parts of a few tokens cost more to
+// merge than they save, large ones leave SMs idle (us at 1, 64, 128, 256: one sequence of
+// 777 12.8, 12.9, 14.6, 16.8; 32 of 128-2048 24.9, 22.7, 24.9, 20.7; 4 of 32k-131k 85.2, 84.3,
+// 83.1, 87.2).  A chunk has up to eight times the rows to merge (24 sequences of 1k-8k with 4
+// drafted tokens: 54.9 at 64, 51.2 at 128).
+constexpr int kQ4Align = 64;
+constexpr int kQ4AlignChunk = 128;
 
 // d (16x8 fp32) += a (16x16 f16, row) * b (16x8 f16, col)
 __device__ __forceinline__ void mma_q4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -84,8 +87,7 @@ __device__ __forceinline__ int token_of(int i) { return i & 1 ? 4 + ((i >> 1) ^ 
 
 constexpr int kChunkRows = 8;  // G * QL of the chunk instantiations
 
-// kHeads: 8, which makes every offset of a row a constant (256 sequences of 1k-8k, 298 -> 285 us), or 0, any number.
-template <int G, int QL, int D, bool kVar, int kHeads>
+template <int G, int QL, int D, bool kVar>
 __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel(const Params p) {
   pkv::pdl_enter();
   {
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
   const int warp = tid / 32;
   const int lane = tid % 32;
   const int nw = p.nw;
-  const int hkv = kHeads ? kHeads : p.hkv;
+  const int hkv = p.hkv;
   const int row_bytes = pkv::q4_row_bytes(hkv, D);
   unsigned char* stage_base = smem;
   uint64_t* full = reinterpret_cast<uint64_t*>(stage_base + p.stages * p.stage_bytes);
@@ -477,16 +479,14 @@ int launch_q4(Params& p, int sms, cudaStream_t stream) {
   p.nw = p.hkv * p.wph;
   p.t_stage = kQ4Chunk * p.wph;
   p.stage_bytes = static_cast<size_t>(p.t_stage) * row * 2;
-  p.align = kQ4Align;
+  p.align = kVar ? kQ4AlignChunk : kQ4Align;
   const size_t misc = 2 * kQ4Stages * sizeof(uint64_t) + 64 * sizeof(long long) + 32 * sizeof(int) +
                       static_cast<size_t>(p.nw - p.hkv) * R * (D + 2) * sizeof(float);
   p.stages = std::min<int>(kQ4Stages, static_cast<int>((kQ4Smem - misc) / p.stage_bytes));
   if (p.stages < 2) return PKV_EUNSUPPORTED;
-  // (chunks gain nothing from it)
-  const bool eight = !kVar && p.hkv == 8;
-  auto kernel = eight ? paged_decode_q4_kernel<G, QL, D, kVar, kVar ? 0 : 8> : paged_decode_q4_kernel<G, QL, D, kVar, 0>;
-  static std::atomic<uint64_t> smem_allowed[2];
-  if (pkv::allow_smem(kernel, kQ4Smem, smem_allowed[eight]) != cudaSuccess) return PKV_ECUDA;
+  auto kernel = paged_decode_q4_kernel<G, QL, D, kVar>;
+  static std::atomic<uint64_t> smem_allowed{0};  // the limit for every number of KV heads
+  if (pkv::allow_smem(kernel, kQ4Smem, smem_allowed) != cudaSuccess) return PKV_ECUDA;
   const unsigned grid = p.num_splits > 0 ? static_cast<unsigned>(static_cast<long long>(p.batch) * p.num_splits)
                                          : static_cast<unsigned>(sms * kAutoCtasPerSm);
   if (grid == 0) return PKV_OK;
