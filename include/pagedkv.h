@@ -565,7 +565,7 @@ int pkv_kv_load_q4(void* k, void* v, const void* k_cache, const void* v_cache,
  * argument, the workspace and its size function are pkv_paged_decode_attn's.
  * q's rows may have any magnitude (they enter the products scaled by a power of two).
  * Supported: head_dim 64 or 128; at most 8 KV heads; G in {1, 2, 4, 8}; every
- * block size.
+ * block size; k_scale and v_scale in [2^-64, 2^64] (others: PKV_EINVAL).
  */
 int pkv_paged_decode_attn_q4(void* out, const void* q, const void* k_cache, const void* v_cache,
                              const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -588,7 +588,8 @@ size_t pkv_paged_short_chunk_q4_workspace_bytes(int32_t batch, int32_t num_q_hea
  * cache; the new rows are stored first (pkv_kv_store_q4, pkv_kv_rope_store).
  * Arguments, range checks and the workspace are the E4M3 call's (short chunks:
  * pkv_paged_short_chunk_q4_workspace_bytes).
- * Supported: head_dim 64 or 128; G in {1, 2, 4, 8}; every block size.
+ * Supported: head_dim 64 or 128; G in {1, 2, 4, 8}; every block size; k_scale and
+ * v_scale in [2^-64, 2^64] (others: PKV_EINVAL).
  */
 int pkv_paged_varlen_prefill_attn_q4(void* out, const void* q, const void* k_cache, const void* v_cache,
                                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,

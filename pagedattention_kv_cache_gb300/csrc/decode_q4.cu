@@ -6,6 +6,7 @@
 #include "decode_launch.cuh"
 #include "decode_q4_args.cuh"
 #include "prefill_args.cuh"
+#include "q4.cuh"
 
 namespace pkv {
 
@@ -45,7 +46,7 @@ extern "C" int pkv_paged_decode_attn_q4(void* out, const void* q, const void* k_
                                         int32_t num_blocks, float scale, float k_scale, float v_scale,
                                         int32_t num_splits, void* workspace, size_t workspace_bytes,
                                         pkv_stream_t stream) {
-  if (!(k_scale > 0.f) || !(v_scale > 0.f) || isinf(k_scale) || isinf(v_scale)) return PKV_EINVAL;
+  if (!pkv::q4_attention_scale(k_scale) || !pkv::q4_attention_scale(v_scale)) return PKV_EINVAL;
   const int chk = check_decode_args(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, batch,
                                     num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, num_splits, PKV_BF16);
   if (chk < 0) return chk;

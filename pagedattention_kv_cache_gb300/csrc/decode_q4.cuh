@@ -237,7 +237,7 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
       const int ex = amax > 0.f ? min(max(14 - ilogbf(amax), -113), 126) : 0;
       // (the scale's sign goes with q; kept above zero, so that -infinity, a hidden key, stays -infinity)
       const float up = copysignf(ldexpf(1.f, ex), p.scale_log2);
-      float down = fabsf(p.scale_log2) * pkv::kQ4Unit * ldexpf(1.f, -ex);
+      float down = fabsf(p.scale_log2) * ldexpf(pkv::kQ4Unit, -ex);
       if (down == 0.f) down = FLT_MIN;
       mul[0] = __shfl_sync(0xffffffffu, down, 8 * c);
       mul[1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);

@@ -488,7 +488,7 @@ struct Split {
   int lanes, tokens;
   Split(int heads, int units_per_head, int batch)
       : lanes(std::min((heads + batch - 1) / batch, 256 / units_per_head)), tokens(256 / (lanes * units_per_head)) {}
-  unsigned blocks(int num_tokens) const { return static_cast<unsigned>((num_tokens + tokens - 1) / tokens); }
+  unsigned blocks(int64_t num_tokens) const { return static_cast<unsigned>((num_tokens + tokens - 1) / tokens); }
 };
 // More work than one head to a thread keeps on the GPU at once.
 bool many(int num_tokens, int units, int sms) { return static_cast<int64_t>(num_tokens) * units > sms * 1024ll; }

@@ -11,6 +11,7 @@
 #include <cfloat>
 
 #include "prefill_args.cuh"
+#include "q4.cuh"
 #include "score_mod.cuh"
 
 namespace {
@@ -229,6 +230,7 @@ extern "C" int pkv_paged_varlen_prefill_attn_q4(void* out, const void* q, const 
                                                 int32_t num_blocks, float scale, float k_scale, float v_scale,
                                                 int32_t causal, void* workspace, size_t workspace_bytes,
                                                 pkv_stream_t stream) {
+  if (!pkv::q4_attention_scale(k_scale) || !pkv::q4_attention_scale(v_scale)) return PKV_EINVAL;
   PrefillArgs a{};
   const int chk = quantized_args(a, out, q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                                  block_tables, max_blocks_per_seq, batch, total_q, num_q_heads, num_kv_heads, head_dim,

@@ -20,6 +20,8 @@ __host__ __device__ constexpr int q4_scale_offset(int hkv, int head_dim) { retur
 __host__ __device__ constexpr int q4_row_bytes(int hkv, int head_dim) {
   return (hkv * (head_dim / 2 + head_dim / 16) + 15) / 16 * 16;
 }
+// Tensor scales the attention calls take: unnormalized sums of weighted values times one stay in float32.
+inline bool q4_attention_scale(float t) { return t >= 0x1p-64f && t <= 0x1p64f; }
 inline bool q4_head_dim(int head_dim) { return head_dim == 64 || head_dim == 128; }
 
 // Maximum that keeps a NaN.

@@ -293,6 +293,32 @@ def test_decode_scales(scale):
     decode_case(32, [900, 3], 16, 2, 4, 64, scale=scale, splits=2)
 
 
+@pytest.mark.parametrize("power", [-64, -50, 50, 64])
+def test_tensor_scales_up_to_their_ends(power):
+    """Values times 2^power, q's scale divided by it: the same scores, and outputs times 2^power, bit for bit."""
+    hkv, d, bs, n, hq = 2, 128, 16, 3000, 8
+    gen = torch.Generator().manual_seed(6)
+    k, v = [torch.randn(n, hkv, d, generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+    q = torch.randn(n, hq, d, generator=gen).to(torch.bfloat16).cuda()
+    slots = torch.arange(n, dtype=torch.int32).cuda()
+    bt = torch.arange(-(-n // bs), dtype=torch.int32)[None].cuda()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    cu_k = torch.tensor([0, n], dtype=torch.int32).cuda()
+    results = []
+    for t in (1.0, 2.0 ** power):
+        pools = [pkv.q4_cache(bt.shape[1], bs, hkv, d) for _ in range(2)]
+        pkv.kv_store_q4((k.float() * t).to(torch.bfloat16), (v.float() * t).to(torch.bfloat16), *pools, slots, t, t)
+        outs = [pkv.paged_decode_attn_q4(q[:1], *pools, bt, lens, 0.1 / t, t, t, hkv, num_splits=s) for s in (0, 1)]
+        for new in (2, 200):
+            cu_q = torch.tensor([0, new], dtype=torch.int32).cuda()
+            outs += [pkv.paged_varlen_prefill_attn_q4(q[:new], *pools, bt, cu_q, cu_k, new, n, 0.1 / t, t, t, hkv, workspace=w)
+                     for w in (None, False)]
+        results.append([(o.float() / t) for o in outs])
+    assert pkv.device_error() == 0
+    for a, b in zip(*results):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
 def test_rows_past_32_bits_of_bytes():
     """A pool of 4.5 GB: its last blocks give what the same rows give in a small pool, bit for bit."""
     hkv, d, bs, n, hq = 8, 128, 256, 1000, 16

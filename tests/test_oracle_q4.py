@@ -165,5 +165,7 @@ def test_q4_attention_refuses_on_the_host():
             assert call(**kw) == _lib.EUNSUPPORTED, kw
         for kw in (dict(out=PTR + 8), dict(q=PTR + 8), dict(kc=PTR + 8), dict(vc=PTR + 8)):
             assert call(**kw) == _lib.EALIGN, kw
+        for t in (2.0 ** 65, 2.0 ** -65, -1.0):
+            assert call(ks=t) == _lib.EINVAL and call(vs=t) == _lib.EINVAL
     assert decode(splits=-1) == _lib.EINVAL and decode(hkv=16, hq=16) == _lib.EUNSUPPORTED
     assert chunk(causal=2) == _lib.EINVAL and chunk(scale=0.0) == _lib.EINVAL and chunk(scale=float("nan")) == _lib.EINVAL
