@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) kv_rope_stream_kernel(co
     const Item coming = look_up(next);
     next += step;
     const Item it = queue[0];
-    if (!pkv::mbar_wait(&full[st], parity)) {
+    if (!__all_sync(0xffffffffu, pkv::mbar_wait(&full[st], parity))) {  // (the lanes leave together)
       if (tid == 0) pkv::raise_error(a.err, PKV_DERR_WAIT_TIMEOUT);
       // the block must not end with copies on their way into its shared memory
 #pragma unroll
