@@ -16,10 +16,14 @@
 //    eight keys.  A lane takes 16 (head_dim 64: 8) consecutive elements of four keys:
 //    one scale each.
 //  * Both products see the softmax rows in the columns of their accumulators, so a
-//    lane owns the state of rows 2c and 2c + 1 and rescaling needs no exchange.  The
-//    row maximum is a reference only: it moves when a score passes it by 2^8
-//    (a vote per stage), so the usual stage takes no maximum across lanes.  The row
-//    sums are a product of ones with the weights.
+//    lane owns the state of rows 2c and 2c + 1 and rescaling needs no exchange.  A
+//    row's reference moves when a score passes it by 15 (a vote per stage), to 7 below
+//    the largest, so the usual stage takes no maximum across lanes.  The row sums are a
+//    product of ones with the weights.
+//  * f16 ends at 2^16, so a weight's exponent is the difference of the scaled score,
+//    rounded to float32, and the reference, and that difference alone decides whether
+//    the reference moves: no rounding of either, however large, lets a weight pass 2^15.
+//    (A fused multiply and add would take the unrounded product.)
 //  * Eight warps with four chunks of 16 keys each per stage: three chunks 244 us, two 258,
 //    one 337 (four 235 in that measurement); 16 warps at 112 registers with two 250.
 //  * Which token stands in which fragment row is free as long as K and V agree;
@@ -104,8 +108,8 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
   static_assert(R <= 8, "at most 8 rows per KV head");
   constexpr int NW = D / 32;   // code words of a lane's quarter of a key
   constexpr int NO = D / 16;   // m-tiles of O^T
-  constexpr float kRescale = 8.0f;
-  constexpr float kWeightLog2 = 7.0f;
+  constexpr float kWeightLog2 = 7.0f;  // a row's largest weight when its reference is taken
+  constexpr float kMost = 15.0f;       // and what one may grow to before it is taken again
   const int rows_per_seq = QL * p.hq;
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x;
@@ -257,10 +261,9 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
     for (int j = 0; j < NO; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    // the rows' reference m as the two numbers the loop takes: what a score must pass to move it (-infinity: no
-    // score yet), and what an exponent starts from
-    float limit[2] = {-INFINITY, -INFINITY};
-    float base[2] = {0.f, 0.f};
+    // the rows' references, what an exponent starts from (kNoScore, below every score: none yet)
+    constexpr float kNoScore = -FLT_MAX;
+    float base[2] = {kNoScore, kNoScore};
     float l[4] = {0.f, 0.f, 0.f, 0.f};  // of rows 2c and 2c + 1, twice: a product of ones with the weights
 
     for (int t = seg.t0; t < seg.t1; t += p.t_stage) {
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
             }
           }
         }
-        // raw scores of keys r0 (e = 0, 1) and r0 + 8 (2, 3) of each chunk for rows 2c and 2c + 1
+        // raw scores of keys r0 (e = 0, 1) and r0 + 8 (2, 3) of each chunk for rows 2c and 2c + 1, then scaled
         float top[2] = {-INFINITY, -INFINITY};
         const bool partial = nv < kQ4Chunk;
         if (partial || (kVar && t + tw0 + kQ4Chunk > seg.ctx - seg.nq)) {
@@ -304,23 +307,26 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
               if (key >= seg.t1 || key > lim[e & 1]) x[u][e] = -INFINITY;
             }
         }
+        const uint64_t muls = pkv::pair(mul[0], mul[1]);
 #pragma unroll
         for (int u = 0; u < kQ4Sub; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], x[u][e]);
-        top[0] *= mul[0];
-        top[1] *= mul[1];
-        if (__any_sync(0xffffffffu, top[0] > limit[0] || top[1] > limit[1])) {
+          for (int e = 0; e < 4; e += 2) {
+            pkv::split(pkv::mul2(pkv::pair(x[u][e], x[u][e + 1]), muls), x[u][e], x[u][e + 1]);
+            top[0] = fmaxf(top[0], x[u][e]);
+            top[1] = fmaxf(top[1], x[u][e + 1]);
+          }
+        if (__any_sync(0xffffffffu, top[0] - base[0] > kMost || top[1] - base[1] > kMost)) {
           // (a row moves by its own scores only)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float mx = top[i];
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            if (mx > limit[i]) {
-              const float corr = limit[i] == -INFINITY ? 0.f : pkv::ex2(base[i] + kWeightLog2 - mx);
-              limit[i] = mx + kRescale;
-              base[i] = mx - kWeightLog2;
+            if (mx - base[i] > kMost) {
+              const float next = mx - kWeightLog2;
+              const float corr = pkv::ex2(base[i] - next);  // 0 while there is no score
+              base[i] = next;
               l[i] *= corr;
               l[2 + i] *= corr;
 #pragma unroll
@@ -332,12 +338,14 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
           }
         }
         uint32_t pf[kQ4Sub][2];  // weights of keys r0 and r0 + 8, then of this lane's V rows
+        const uint64_t from = pkv::pair(-base[0], -base[1]);
 #pragma unroll
         for (int u = 0; u < kQ4Sub; ++u)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            pf[u][i] = movmatrix(pkv::pack_f16x2(pkv::ex2(fmaf(x[u][2 * i], mul[0], -base[0])),
-                                                 pkv::ex2(fmaf(x[u][2 * i + 1], mul[1], -base[1]))));
+            float a, b;
+            pkv::split(pkv::add2(pkv::pair(x[u][2 * i], x[u][2 * i + 1]), from), a, b);
+            pf[u][i] = movmatrix(pkv::pack_f16x2(pkv::ex2(a), pkv::ex2(b)));
           }
 #pragma unroll
         for (int u = 0; u < kQ4Sub; ++u) {
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
     }
     float m[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) m[i] = limit[i] == -INFINITY ? -INFINITY : base[i] + kWeightLog2;
+    for (int i = 0; i < 2; ++i) m[i] = base[i] == kNoScore ? -INFINITY : base[i];  // (sums are relative to it)
     // accumulator (tm, i) is element d0 + 2 tm of row 2c + i, (tm, 2 + i) the next one
     const int d0 = r0 * (D / 8);
     if (p.wph > 1) {
