@@ -1103,6 +1103,7 @@ __global__ void __launch_bounds__(threads(kForm), 1)
     auto red_at = [&](int parity, int h) { return red + ((parity * 2 + x) * 2 + h) * kBM + row; };
     float m_run = -INFINITY;
     float l_run = 0.f;  // this half's keys only
+    bool large = false;  // kF16: a row of the warp has a reference of 2^20 or more
     uint32_t r[64];
     if constexpr (kF16) {
       // Q becomes f16 in place, each row scaled by the power of two that puts its
@@ -1213,22 +1214,24 @@ __global__ void __launch_bounds__(threads(kForm), 1)
       *red_at(j & 1, half) = mx_half;
       named_barrier_sync(pair_id, 64);
       const float mt = fmaxf(*red_at(j & 1, 0), *red_at(j & 1, 1));
-      float m_tile = mt * mul;
-      if constexpr (kF16) {
-        // the reference of the weights, below the maximum: the factor cancels against the row sum and in the merge of
-        // parts, which see the same reference (past 2^20 the difference would not be exact enough to bound them)
-        if (fabsf(m_tile) < 0x1p20f) m_tile -= kF16WeightLog2;
-      }
+      const float top = __fmul_rn(mt, mul);
+      // kF16: the reference of the weights is below the maximum; the factor cancels against the row sum and in the
+      // merge of parts, which see the same reference
+      float m_tile = kF16 ? __fadd_rn(top, -kF16WeightLog2) : top;
       if constexpr (kCap && !kBias) {
         m_tile = mt == -INFINITY ? mt : p.mod.cap_log2 * tanh_by_exp(mt * p.mod.raw_to_x);
       }
       const float m_new = fmaxf(m_run, m_tile);
-      const bool grow = m_new > m_run + kRescaleLog2 || (m_run == -INFINITY && m_new != -INFINITY);
+      // (kF16: the largest exponent itself decides, so that no rounding of a large reference lets a weight pass f16's range)
+      const bool grow = kF16 ? top - m_run > kRescaleLog2 + kF16WeightLog2
+                             : m_new > m_run + kRescaleLog2 || (m_run == -INFINITY && m_new != -INFINITY);
       const bool rescale = __any_sync(0xffffffffu, grow);  // the same in both halves' warps
       float factor = 1.f;
       if (rescale) {
         factor = (m_run == -INFINITY || m_new <= m_run) ? 1.f : exp2f(m_run - m_new);
         m_run = fmaxf(m_run, m_new);
+        // (-infinity, no key yet, is not such a reference)
+        if constexpr (kF16) large = __any_sync(0xffffffffu, fabsf(m_run) >= 0x1p20f && m_run != -INFINITY);
       }
       const float m_use = m_run == -INFINITY ? 0.f : m_run;
       // P = exp2(scale * s - m) rounded to bf16, packed two per column: keys
@@ -1270,9 +1273,16 @@ __global__ void __launch_bounds__(threads(kForm), 1)
           for (int e = 0; e < 32; ++e) r[e] = exp2_pair_bf16(r[2 * e], r[2 * e + 1], 1.f, -m_use, l_pair[e % 2]);
         }
       } else {
+        // kF16, at references whose float32 step is 2^-3 or more: the unrounded product may stand above the rounded maximum
+        // by half a step, so the scores are rounded first
+        if (kF16 && large) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) r[e] = __float_as_uint(__fmul_rn(__uint_as_float(r[e]), mul));
+        }
+        const float by = kF16 && large ? 1.f : mul;
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          r[e] = kF16 ? exp2_pair_f16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2])
+          r[e] = kF16 ? exp2_pair_f16(r[2 * e], r[2 * e + 1], by, -m_use, l_pair[e % 2])
                       : exp2_pair_bf16(r[2 * e], r[2 * e + 1], mul, -m_use, l_pair[e % 2]);
       }
       tc::tmem_st32(s_addr + half * 32, r);

@@ -117,6 +117,14 @@ def test_decode_of_large_scores(cache, g, d, power):
 
 
 @pytest.mark.parametrize("power", POWERS)
-@pytest.mark.parametrize("cache,d", [("q4", 128), ("q4", 64)])
+@pytest.mark.parametrize("cache,d", [("q4", 128), ("q4", 64), ("e4m3", 128)])
 def test_drafted_tokens_of_large_scores(cache, d, power):
     Case(cache, power, CONTEXTS, [1, 2, 4, 4], 2, d).chunk()
+
+
+@pytest.mark.parametrize("power", POWERS)
+@pytest.mark.parametrize("cache,d", [("q4", 128), ("q4", 64), ("e4m3", 128), ("e4m3", 64)])
+def test_chunks_of_large_scores(cache, d, power):
+    case = Case(cache, power, CONTEXTS, [1, 2, 65, 70], 2, d)
+    case.chunk()
+    case.chunk(workspace=False)
