@@ -446,7 +446,10 @@ __global__ void __launch_bounds__(288, 1)
           mt[hh] = fmaxf(mt[hh], __shfl_xor_sync(0xffffffffu, mt[hh], 1));
           mt[hh] = fmaxf(mt[hh], __shfl_xor_sync(0xffffffffu, mt[hh], 2));
           const float mn = fmaxf(m[hh], mt[hh]);
-          const bool need = mn > m[hh] + kRescale || (m[hh] == -INFINITY && mn != -INFINITY);
+          // (FP8: by the difference, which is the largest exponent: 8 above a reference past 2^27 may round to 16 above it,
+          // and f16 weights, 2^7 times as large, end at 2^16)
+          const bool need = kFp8 ? mn - m[hh] > kRescale
+                                 : mn > m[hh] + kRescale || (m[hh] == -INFINITY && mn != -INFINITY);
           if constexpr (kT) {
             // row r0's state lives in quad r0; the accumulators hold rows 2c and 2c + 1
             if (__any_sync(0xffffffffu, need)) {

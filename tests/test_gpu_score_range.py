@@ -109,7 +109,7 @@ class Case:
 
 
 @pytest.mark.parametrize("power", POWERS)
-@pytest.mark.parametrize("cache,g,d", [("q4", 2, 128), ("q4", 8, 64)])
+@pytest.mark.parametrize("cache,g,d", [("q4", 2, 128), ("q4", 8, 64), ("e4m3", 2, 128), ("e4m3", 8, 128)])
 def test_decode_of_large_scores(cache, g, d, power):
     case = Case(cache, power, CONTEXTS, [1] * len(CONTEXTS), g, d)
     for splits in (0, 1, 3):
