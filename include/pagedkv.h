@@ -563,7 +563,9 @@ int pkv_kv_load_q4(void* k, void* v, const void* k_cache, const void* v_cache,
  * paged_decode_attn_q4: pkv_paged_decode_attn over a 4-bit cache: the same result
  * as on the values that the cache stands for.  q, out bf16; every other
  * argument, the workspace and its size function are pkv_paged_decode_attn's.
- * q's rows may have any magnitude (they enter the products scaled by a power of two).
+ * q's rows may have any magnitude (they enter the products scaled by a power of two),
+ * and so may scale and k_scale, whose product need not be a float32: only the
+ * scores, scale * q . K in units of ln 2, have to be (they are rounded to float32).
  * Supported: head_dim 64 or 128; at most 8 KV heads; G in {1, 2, 4, 8}; every
  * block size; k_scale and v_scale in [2^-64, 2^64] (others: PKV_EINVAL).
  */
@@ -589,7 +591,7 @@ size_t pkv_paged_short_chunk_q4_workspace_bytes(int32_t batch, int32_t num_q_hea
  * Arguments, range checks and the workspace are the E4M3 call's (short chunks:
  * pkv_paged_short_chunk_q4_workspace_bytes).
  * Supported: head_dim 64 or 128; G in {1, 2, 4, 8}; every block size; k_scale and
- * v_scale in [2^-64, 2^64] (others: PKV_EINVAL).
+ * v_scale in [2^-64, 2^64] (others: PKV_EINVAL); magnitudes as for paged_decode_attn_q4.
  */
 int pkv_paged_varlen_prefill_attn_q4(void* out, const void* q, const void* k_cache, const void* v_cache,
                                      const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,

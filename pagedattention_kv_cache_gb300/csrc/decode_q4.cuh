@@ -239,10 +239,8 @@ __global__ void __launch_bounds__((kQ4Warps + 1) * 32, 1) paged_decode_q4_kernel
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const int ex = amax > 0.f ? min(max(14 - ilogbf(amax), -113), 126) : 0;
-      // (the scale's sign goes with q; kept above zero, so that -infinity, a hidden key, stays -infinity)
-      const float up = copysignf(ldexpf(1.f, ex), p.scale_log2);
-      float down = fabsf(p.scale_log2) * ldexpf(pkv::kQ4Unit, -ex);
-      if (down == 0.f) down = FLT_MIN;
+      const float up = copysignf(pkv::power_of_two(ex), p.scale_log2);  // (the scale's sign goes with q)
+      const float down = pkv::row_scale(fabsf(p.scale_log2), p.scale_exp - ex);
       mul[0] = __shfl_sync(0xffffffffu, down, 8 * c);
       mul[1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
 #pragma unroll
@@ -544,7 +542,7 @@ int run_q4(const pkv::Q4Decode& a, cudaStream_t stream) {
   p.hkv = a.hkv;
   p.block_size = a.block_size;
   p.num_blocks = a.num_blocks;
-  p.scale_log2 = a.scale * pkv::kLog2e * a.k_scale;
+  p.scale_log2 = pkv::split_scale(a.scale, a.k_scale * pkv::kQ4Unit, &p.scale_exp);
   p.v_scale = a.v_scale;
   p.num_splits = a.num_splits;
   p.cu_q = a.cu_q;

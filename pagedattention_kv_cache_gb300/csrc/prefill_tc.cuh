@@ -216,7 +216,7 @@ struct TcParams {
   int hkv;
   int block_size;
   int num_blocks;
-  float scale_log2;
+  float scale_log2;  // scale * log2(e); kFp8, kInt4: times 2^scale_exp that, times the K scale
   int causal;
   int paged;
   int piece_rows;  // rows per K/V TMA box (paged: min(block_size, kBN))
@@ -233,6 +233,7 @@ struct TcParams {
   float v_scale;
   uint32_t block_mul;  // kInt4: key / block_size = key * block_mul >> block_shift
   int block_shift;
+  int scale_exp;
 };
 
 }  // namespace
@@ -1109,6 +1110,7 @@ __global__ void __launch_bounds__(threads(kForm), 1)
       // Q becomes f16 in place, each row scaled by the power of two that puts its
       // largest element in [2^14, 2^15): exact but for elements 2^28 times
       // smaller than that.  The power comes off with the softmax scale.
+      int ex = 0;
       if (n_x > 0) {
         // tile A first: its products can start while B's rows are rewritten
         wait(&bars[x == 1 && n_a > 0 ? Q_READY : Q_FULL], 0);
@@ -1133,10 +1135,8 @@ __global__ void __launch_bounds__(threads(kForm), 1)
         named_barrier_sync(pair_id, 64);
         top = fmaxf(*red_at(0, 0), *red_at(0, 1));
         const int exponent = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127 for zero and subnormals
-        const int ex = min(max(14 - exponent, -113), 126);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-        // (kept above zero: -infinity, a hidden key, times it stays -infinity)
-        mul = fmaxf(mul * __uint_as_float(static_cast<uint32_t>(127 - ex) << 23), FLT_MIN);
+        ex = min(max(14 - exponent, -113), 126);
+        const float up = power_of_two(ex);
 #pragma unroll
         for (int i = 0; i < kChunksHalf; ++i) {
           float f[8];
@@ -1152,6 +1152,7 @@ __global__ void __launch_bounds__(threads(kForm), 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[Q_READY + x]);
+      mul = row_scale(mul, p.scale_exp - ex);
     }
 
     // kMod: keys the row does not see get -infinity; lo <= key <= hi in one unsigned comparison
@@ -1566,7 +1567,7 @@ int launch(const PrefillArgs& a, cudaStream_t stream) {
   p.bias_mul = kForm == kBiased ? 1.f / a.scale : kLog2e;
   if constexpr (quantized(kForm)) {
     constexpr float kUp = kQ4 ? kQ4Unit : 1.f;
-    p.scale_log2 *= a.k_scale * kUp;
+    p.scale_log2 = split_scale(a.scale, a.k_scale * kUp, &p.scale_exp);
     p.v_scale = a.v_scale * kUp;
     p.k_codes = static_cast<const unsigned char*>(a.k_cache);
     p.v_codes = static_cast<const unsigned char*>(a.v_cache);
