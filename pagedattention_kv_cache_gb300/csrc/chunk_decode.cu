@@ -58,7 +58,7 @@ int chunk_decode_launch(const PrefillArgs& a, bool fp8, cudaStream_t stream) {
   p.hkv = a.hkv;
   p.block_size = a.block_size;
   p.num_blocks = a.num_blocks;
-  p.scale_log2 = a.scale * kLog2e * (fp8 ? a.k_scale : 1.f);
+  p.scale_log2 = fp8 ? split_scale(a.scale, a.k_scale, &p.scale_exp) : a.scale * kLog2e;
   p.v_scale = fp8 ? a.v_scale : 1.f;
   p.mod = a.mod;
   p.cu_q = a.cu_q;

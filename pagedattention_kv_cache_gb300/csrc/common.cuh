@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 #include <utility>
 
 #include "../../include/pagedkv.h"
@@ -85,6 +86,15 @@ inline cudaError_t allow_smem(F* kernel, size_t bytes, std::atomic<uint64_t>& do
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
+}
+
+// scale * log2(e) * t, t a quantized cache's K scale, as a float of magnitude [0.5, 1] and a power of two: the product
+// itself may leave float32's range where what a row's products are multiplied by does not (q large or small the other way).
+inline float split_scale(float scale, float t, int* exponent) {
+  const double x = static_cast<double>(scale) * 1.4426950408889634 * t;
+  if (x != 0.0) return static_cast<float>(std::frexp(x, exponent));
+  *exponent = -1024;  // (row_scale's least)
+  return 0.5f;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -258,6 +268,13 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, ui
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(codes));
+}
+// 2^e of a normal number.
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// What a row's products are multiplied by, from split_scale and the row's power of two: kept a normal number, so that
+// -infinity, a hidden key, stays -infinity, and a product of 0 a score of 0.
+__device__ __forceinline__ float row_scale(float mantissa, int exponent) {
+  return mantissa * power_of_two(min(max(exponent, -125), 127));
 }
 // Byte permute: result byte i = byte sel_i of the eight bytes {b, a} (a's are 0-3).
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

@@ -73,7 +73,7 @@ struct Params {
   int hkv;
   int block_size;
   int num_blocks;
-  float scale_log2;  // scale * log2(e) (times the K scale for an FP8 cache; 4 bits: times 2^scale_exp is that)
+  float scale_log2;  // scale * log2(e); quantized caches: times 2^scale_exp that, times the K scale
   float v_scale;     // V scale of an FP8 cache (1 otherwise)
   int num_splits;    // 0 = automatic
   int nw;            // consumer warps

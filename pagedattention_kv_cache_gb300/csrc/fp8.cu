@@ -156,7 +156,7 @@ extern "C" int pkv_paged_decode_attn_fp8(void* out, const void* q, const void* k
   p.hkv = num_kv_heads;
   p.block_size = block_size;
   p.num_blocks = num_blocks;
-  p.scale_log2 = scale * 1.4426950408889634f * k_scale;
+  p.scale_log2 = pkv::split_scale(scale, k_scale, &p.scale_exp);
   p.v_scale = v_scale;
   p.num_splits = num_splits;
   switch (group) {

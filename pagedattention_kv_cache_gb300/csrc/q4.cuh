@@ -12,8 +12,6 @@
 // see the cached values themselves.
 #pragma once
 
-#include <cmath>
-
 #include "common.cuh"
 
 namespace pkv {
@@ -24,15 +22,6 @@ __host__ __device__ constexpr int q4_row_bytes(int hkv, int head_dim) {
 }
 // Tensor scales the attention calls take: unnormalized sums of weighted values times one stay in float32.
 inline bool q4_attention_scale(float t) { return t >= 0x1p-64f && t <= 0x1p64f; }
-// scale * log2(e) * t as a float of magnitude [0.5, 1] and a power of two: the product itself may leave float32's range
-// (t goes to 2^-64 and 2^64, scale is as small or large as q and K are the other way), where what a row's products are
-// multiplied by does not.
-inline float split_scale(float scale, float t, int* exponent) {
-  const double x = static_cast<double>(scale) * 1.4426950408889634 * t;
-  if (x != 0.0) return static_cast<float>(std::frexp(x, exponent));
-  *exponent = -1024;  // (row_scale's least)
-  return 0.5f;
-}
 inline bool q4_head_dim(int head_dim) { return head_dim == 64 || head_dim == 128; }
 
 // Maximum that keeps a NaN.
@@ -52,14 +41,6 @@ __device__ __forceinline__ uint32_t to_e4m3(float x) {
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
   const uint32_t h = e4m3x2_to_f16x2(code & 0xffu);
   return __low2float(*reinterpret_cast<const __half2*>(&h));
-}
-
-// 2^e of a normal number.
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-// What a row's products are multiplied by, from split_scale and the row's power of two: kept a normal number, so that
-// -infinity, a hidden key, stays -infinity, and a product of 0 a score of 0.
-__device__ __forceinline__ float row_scale(float mantissa, int exponent) {
-  return mantissa * power_of_two(min(max(exponent, -125), 127));
 }
 
 // Two-lane fp32 arithmetic.

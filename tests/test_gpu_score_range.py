@@ -130,24 +130,42 @@ def test_chunks_of_large_scores(cache, d, power):
     case.chunk(workspace=False)
 
 
-def _calls(q, pools, n, scale, t, hkv):
+def _pools(cache, k, v, t):
+    """K, V rows [n, Hkv, D] in blocks in order, and the values that the pools hold."""
+    n, hkv, d = k.shape
+    slots = torch.arange(n, dtype=torch.int32).cuda()
+    if cache == "q4":
+        pools = [pkv.q4_cache(-(-n // BS), BS, hkv, d) for _ in range(2)]
+        pkv.kv_store_q4(k.cuda(), v.cuda(), *pools, slots, t, t)
+        return pools, [oq.values(x.cpu().numpy().reshape(-1, x.shape[2])[:n], hkv, d, t) for x in pools]
+    pools = [torch.zeros(-(-n // BS), BS, hkv, d, dtype=torch.uint8).cuda() for _ in range(2)]
+    pkv.kv_store_fp8(k.cuda(), v.cuda(), *pools, slots, t, t)
+    return pools, [of8.e4m3_decode(x.cpu().numpy().reshape(-1, hkv, d)[:n]) * float(np.float32(t)) for x in pools]
+
+
+def _calls(cache, q, pools, n, scale, t, hkv):
     """Decode (split and not), drafted tokens and a chunk over n keys in order; q [150, Hq, D], every row alike."""
     bt = torch.arange(pools[0].shape[0], dtype=torch.int32)[None].cuda()
     lens, cu_k = [torch.tensor(x, dtype=torch.int32).cuda() for x in ([n], [0, n])]
-    for splits in (0, 1):
-        yield "decode", pkv.paged_decode_attn_q4(q[:1], *pools, bt, lens, scale, t, t, hkv, num_splits=splits)
+    decode, chunk = ((pkv.paged_decode_attn_q4, pkv.paged_varlen_prefill_attn_q4) if cache == "q4" else
+                     (pkv.paged_decode_attn_fp8, pkv.paged_varlen_prefill_attn_fp8))
+    heads = (hkv,) if cache == "q4" else ()
+    if cache == "q4" or q.shape[2] == 128:
+        for splits in (0, 1):
+            yield "decode", decode(q[:1], *pools, bt, lens, scale, t, t, *heads, num_splits=splits)
     for new in (2, 150):
         cu_q = torch.tensor([0, new], dtype=torch.int32).cuda()
-        yield f"chunk of {new}", pkv.paged_varlen_prefill_attn_q4(q[:new], *pools, bt, cu_q, cu_k, new, n, scale, t, t, hkv,
-                                                                  causal=False)
+        yield f"chunk of {new}", chunk(q[:new], *pools, bt, cu_q, cu_k, new, n, scale, t, t, *heads, causal=False)
 
 
-@pytest.mark.parametrize("t,scale,q,level", [
-    (2.0 ** -64, 1.05 * 2.0 ** -80, 1.5 * 2.0 ** 127, 448.0),  # scale times the tensor scale is far below the normal numbers
-    (2.0 ** 64, 2.0 ** 67, 2.0 ** -132, 2.0 ** -6),            # and past the largest
+@pytest.mark.parametrize("cache,t,scale,q,level", [
+    ("q4", 2.0 ** -64, 1.05 * 2.0 ** -80, 1.5 * 2.0 ** 127, 7 * 448.0),  # scale times the tensor scale is far below the
+    ("e4m3", 2.0 ** -64, 1.05 * 2.0 ** -78, 1.5 * 2.0 ** 127, 448.0),    # normal numbers
+    ("q4", 2.0 ** 64, 2.0 ** 67, 2.0 ** -132, 7 * 2.0 ** -6),            # and past the largest
+    ("e4m3", 2.0 ** 64, 2.0 ** 70, 2.0 ** -132, 2.0 ** -6),
 ])
 @pytest.mark.parametrize("d", [64, 128])
-def test_softmax_scale_times_tensor_scale(t, scale, q, level, d):
+def test_softmax_scale_times_tensor_scale(cache, t, scale, q, level, d):
     """Ordinary scores from factors at their ends."""
     n, hkv = 600, 2
     gen = torch.Generator().manual_seed(3)
@@ -155,24 +173,22 @@ def test_softmax_scale_times_tensor_scale(t, scale, q, level, d):
     sign[::7] = 1.0  # keys along q
     v = torch.randn(n, hkv, d, generator=gen)
     v[::7] += 2.0
-    pools = [pkv.q4_cache(-(-n // BS), BS, hkv, d) for _ in range(2)]
-    # keys of one magnitude, 7 times an E4M3 number times T, are stored exactly
-    pkv.kv_store_q4((sign * 7 * level * t).to(torch.bfloat16).cuda(), (v * t).to(torch.bfloat16).cuda(), *pools,
-                    torch.arange(n, dtype=torch.int32).cuda(), t, t)
-    k, v = [oq.values(x.cpu().numpy().reshape(-1, x.shape[2])[:n], hkv, d, t) for x in pools]
+    # keys of one magnitude, an E4M3 number (4 bits: 7 times one) times T, are stored exactly
+    pools, (k, v) = _pools(cache, (sign * level * t).to(torch.bfloat16), (v * t).to(torch.bfloat16), t)
     s = np.einsum("d,nhd->hn", np.full(d, q), k) * scale
-    assert 2 < np.abs(s).max() < 16
+    assert 1 < np.abs(s).max() < 16  # what the case is to be
     p = np.exp(s - s.max(1, keepdims=True))
     p /= p.sum(1, keepdims=True)
     ref, weight = [np.einsum("hn,nhd->hd", p, x).repeat(2, 0)[None] / t for x in (v, np.abs(v))]
     rows = torch.full((150, 2 * hkv, d), q, dtype=torch.bfloat16).cuda()
-    for label, got in _calls(rows, pools, n, scale, t, hkv):
+    for label, got in _calls(cache, rows, pools, n, scale, t, hkv):
         close(got.float() / t, ref, weight, np.abs(v).max() / t * 2.0 ** -32, n, label)
     assert pkv.device_error() == 0
 
 
+@pytest.mark.parametrize("cache", ["q4", "e4m3"])
 @pytest.mark.parametrize("power", [30, 64])
-def test_zero_scores_of_a_large_q(power):
+def test_zero_scores_of_a_large_q(cache, power):
     """q.K is 0 at every key: the mean of V, however large q and the tensor scale are."""
     n, hkv, d, t = 300, 2, 128, 2.0 ** power
     gen = torch.Generator().manual_seed(4)
@@ -181,10 +197,8 @@ def test_zero_scores_of_a_large_q(power):
     v = torch.randn(n, hkv, d, generator=gen)
     q = torch.zeros(150, 2 * hkv, d, dtype=torch.bfloat16)
     q[..., :16] = 2.0 ** 120
-    pools = [pkv.q4_cache(-(-n // BS), BS, hkv, d) for _ in range(2)]
-    pkv.kv_store_q4(*[(x * t).to(torch.bfloat16).cuda() for x in (k, v)], *pools, torch.arange(n, dtype=torch.int32).cuda(), t, t)
-    value = oq.values(pools[1].cpu().numpy().reshape(-1, pools[1].shape[2])[:n], hkv, d, t) / t
-    ref, weight = [x.mean(0).repeat(2, 0)[None] for x in (value, np.abs(value))]
-    for label, got in _calls(q.cuda(), pools, n, 0.1, t, hkv):
-        close(got.float() / t, ref, weight, np.abs(value).max() * 2.0 ** -32, n, label)
+    pools, (_, value) = _pools(cache, *[(x * t).to(torch.bfloat16) for x in (k, v)], t)
+    ref, weight = [x.mean(0).repeat(2, 0)[None] / t for x in (value, np.abs(value))]
+    for label, got in _calls(cache, q.cuda(), pools, n, 0.1, t, hkv):
+        close(got.float() / t, ref, weight, np.abs(value).max() / t * 2.0 ** -32, n, label)
     assert pkv.device_error() == 0
