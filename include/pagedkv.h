@@ -492,7 +492,9 @@ int pkv_paged_varlen_prefill_attn_fp8(void* out, const void* q, const void* k_ca
  * is 8 + x / (scale * T) rounded to nearest even, between 0 and 15 (8 where that
  * step is 0).  All in float32.  A group that holds a NaN gets a NaN scale and
  * reads as NaN; infinities saturate.
- * A zero-filled cache reads as zeros.  head_dim 64 or 128.
+ * A zero-filled cache reads as zeros.  head_dim 64 or 128.  Stores and loads take
+ * every finite T > 0; attention takes T in [2^-64, 2^64], so that a cache stored
+ * with another can only be read by pkv_kv_load_q4.
  */
 typedef enum {
   PKV_CACHE_SAME = 0, /* the rows' own type */

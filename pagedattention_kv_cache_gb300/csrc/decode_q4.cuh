@@ -2,9 +2,11 @@
 // (kVar), over the 4-bit cache of q4.cuh.  The CTA plan, split and merge are
 // decode_plan.cuh's.
 //
-// Bound: instructions, then HBM (each token's K and V row once, 576 bytes each with
-// 8 KV heads of 128).  256 sequences of 1k-8k tokens, 1.30 GB: 237 us, 5.5 TB/s; in
-// copies of the kernel the stream alone takes 188 us, with only one of the two
+// Bound: latency of the instructions between codes and products with two consumer
+// warps per scheduler (issue slots 43 % busy, ALU pipe 39 %, tensor pipe 22 %, HBM 49 %
+// over 32 sequences of 8192), then HBM (each token's K and V row once, 576 bytes each
+// with 8 KV heads of 128).  256 sequences of 1k-8k tokens, 1.30 GB: 237 us, 5.5 TB/s;
+// in copies of the kernel the stream alone takes 188 us, with only one of the two
 // products 191-193.  At 4.5 bits an element the way from codes to matrix operands
 // is what the kernel is built around:
 //  * widen_q4 (q4.cuh): nine instructions for a word of eight codes.

@@ -47,9 +47,9 @@ int check_args(const PrefillArgs& a, int max_seqlen_k) {
 }
 
 // Whether the decode kernel takes a chunk: at most 8 rows per KV head (its own
-// limits are head_dim 128 and 8 KV heads), and work enough.  The tcgen05 kernel
-// needs about 6 us and 1 us per 128 keys for each wave of one (sequence, KV head)
-// per SM; the decode kernel 8 us, the time of the bytes, and up to 17 us of
+// limits are 8 KV heads and, but for 4 bits, head_dim 128), and work enough.  The
+// tcgen05 kernel needs about 6 us and 1 us per 128 keys for each wave of one
+// (sequence, KV head) per SM; the decode kernel 8 us, the time of the bytes, and up to 17 us of
 // merging, more with more rows.  Measured with 8 KV heads, G = 2, E4M3 (us,
 // decode / tcgen05): 4 tokens x 1 sequence after 512 keys 16.9 / 13.8, after
 // 2048 21.0 / 25.2; x 16 sequences 27.6 / 14.5 and 30.2 / 35.6; 1 token x 1
@@ -63,6 +63,14 @@ int check_args(const PrefillArgs& a, int max_seqlen_k) {
 // x 16 sequences after 512 keys 20.7 / 13.7 (bf16 20.1 / 12.2), after 1024 22.9 / 19.2
 // (24.0 / 17.1), bf16 after 2048 30.9 / 27.9 and after 8192 89.0 / 87.2; 2 KV heads,
 // G = 4, 1 token x 64 after 2048 bf16 30.9 / 27.9 (E4M3 23.4 / 30.1).
+// 4 bits (L2 flushed), 8 KV heads, G = 2, head_dim 128: 4 tokens x 1 after 512 keys 21.6
+// / 19.6, after 2048 25.8 / 29.8; x 16 after 512 23.6 / 21.6, after 2048 38.0 / 42.1, after
+// 8192 56.4 / 122; 1 token x 1 after 128 17.5 / 15.5, after 512 17.5 / 19.6; two waves, x 64
+// after 32 13.4 / 31.9.  head_dim 64: 4 tokens x 16 after 512 19.6 / 17.5, after 2048 31.9 /
+// 31.9, after 8192 43.1 / 91.3; 1 token x 1 after 128 15.5 / 13.4, after 512 15.5 / 15.5; x 64
+// after 32 13.4 / 27.8.  Of 252 such shapes with 1 to 8 KV heads the rule is on the wrong
+// side by more than a tenth in 14, all next to its border; the worst two are 1 token of 8
+// heads, G = 1, after 128 keys (17.5 / 13.5), and of 1 head, G = 8, after 512 (15.5 / 19.6).
 bool short_chunk(int batch, int group, int num_kv_heads, int head_dim, int max_seqlen_q, int max_seqlen_k,
                  bool q4 = false) {
   const long long rows = static_cast<long long>(max_seqlen_q) * group;

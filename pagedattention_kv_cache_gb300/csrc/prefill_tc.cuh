@@ -61,7 +61,7 @@
 //          copy).  The four pairs of a code word are stored as they come out,
 //          elements (0, 4), (1, 5), (2, 6), (3, 7): the rewritten Q has the same
 //          order, the epilogue undoes it for V.
-//          A batch of 16 chunks, 56 GFLOP, 80 us (the E4M3 form 70); when it took 86, in
+//          A batch of 16 chunks, 56 GFLOP, 78 us (the E4M3 form 74); when it took 86, in
 //          copies of the kernel 76 without the loads, 72 without the widening, 66
 //          without both.  (Rows copied by their own lanes, 16 bytes at a time, 91.)
 #pragma once

@@ -2,9 +2,9 @@
 //
 // A token's K (or V) row: for each KV head head_dim / 2 code bytes (byte i holds
 // the codes of elements 2i, low nibble, and 2i + 1), then for each KV head
-// head_dim / 16 scale bytes (E4M3, one per 16 elements), then zeros up to a
-// multiple of 16 bytes, so that every row can be copied by the TMA engine
-// whatever the number of heads.  An element is (code - 8) * scale * T with one
+// head_dim / 16 scale bytes (E4M3, one per 16 elements), then unused bytes, which
+// no store writes, up to a multiple of 16, so that every row can be copied by the
+// TMA engine whatever the number of heads.  An element is (code - 8) * scale * T with one
 // float T per tensor.
 //
 // E4M3 scales over 16 elements: (code - 8) * scale has at most 7 significant
@@ -146,7 +146,8 @@ __device__ __forceinline__ uint32_t q4_scale_code(float top, float tensor_scale)
   return to_e4m3(__fdiv_rn(top, __fmul_rn(7.f, tensor_scale)));
 }
 
-// Codes to matrix operands.  A word of eight codes becomes four f16 pairs with one
+// Codes to matrix operands, small integers made floats by putting their bits under a
+// constant exponent.  A word of eight codes becomes four f16 pairs with one
 // shift, four and-ors and four fmas: a nibble n in mantissa bits 3..0 under the
 // exponent of 16 is the number 16 + n / 64, in bits 7..4 under the exponent of 1 it is
 // 1 + n / 64, and x s - 16.125 s (or - 1.125 s) is (n - 8) s / 64.  Every step is

@@ -392,7 +392,10 @@ def _decode_workspace_args(workspace, batch: int, hq: int, d: int, num_splits: i
 
 def chunk_workspace_bytes(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_seqlen_q: int,
                           max_seqlen_k: int) -> int:
-    """Bytes of the workspace with which paged_varlen_prefill_attn_mod, _fp8 and _q4 split these sizes (0: never)."""
+    """Bytes of the workspace with which paged_varlen_prefill_attn_mod, _fp8 and _q4 split these sizes (0: never).
+
+    One size for the three: with head_dim 64 and a few new tokens only _q4 makes use of it.
+    """
     lib = _lib.load()
     short = max(int(size(batch, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k))
                 for size in (lib.pkv_paged_short_chunk_workspace_bytes, lib.pkv_paged_short_chunk_q4_workspace_bytes))
@@ -583,7 +586,10 @@ def _need_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, num_kv_heads: int, he
 
 def kv_store_q4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                 slot_mapping: torch.Tensor, k_scale: float, v_scale: float, stream=None) -> None:
-    """Quantizing store: bf16 rows [N, Hkv, D] into 4-bit caches (q4_cache); slot -1 skips."""
+    """Quantizing store: bf16 rows [N, Hkv, D] into 4-bit caches (q4_cache); slot -1 skips.
+
+    Every finite scale > 0 can be stored and loaded; attention reads caches with scales in [2^-64, 2^64].
+    """
     dev = _device(k, "k")
     _need(k, "k", dtype=torch.bfloat16, ndim=3)
     _need(v, "v", dtype=torch.bfloat16, device=dev, shape=k.shape)
@@ -713,7 +719,7 @@ def kv_rope_store_q4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, position
                      k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor, k_scale: float,
                      v_scale: float, *, interleaved: bool = False, q_out: torch.Tensor | None = None,
                      stream=None) -> torch.Tensor:
-    """kv_rope_store of bf16 rows into 4-bit caches (kv_store_q4's rows of the rotated k, and of v)."""
+    """kv_rope_store of bf16 rows into 4-bit caches (kv_store_q4's rows of the rotated k, and of v; its scales)."""
     return _rope_store("pkv_kv_rope_store", q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping, _lib.CACHE_Q4,
                        k_scale, v_scale, interleaved, q_out, stream)
 
@@ -724,7 +730,7 @@ def paged_decode_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
                          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Decode attention over 4-bit caches (q4_cache); q / out bf16 [B, Hq, D].
 
-    num_splits, workspace: as for paged_decode_attn.
+    num_splits, workspace: as for paged_decode_attn.  k_scale, v_scale in [2^-64, 2^64].
     """
     dev = _device(q, "q")
     _need(q, "q", dtype=torch.bfloat16, ndim=3)
@@ -752,7 +758,8 @@ def paged_varlen_prefill_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache
                                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Varlen prefill attention of new tokens over 4-bit caches (q4_cache); q / out bf16 [total_q, Hq, D].
 
-    The new rows are stored first (kv_store_q4, kv_rope_store_q4).  workspace: as for paged_varlen_prefill_attn_mod.
+    The new rows are stored first (kv_store_q4, kv_rope_store_q4).  workspace: as for paged_varlen_prefill_attn_mod;
+    k_scale, v_scale: in [2^-64, 2^64].
     """
     dev = _device(q, "q")
     _need(q, "q", dtype=torch.bfloat16, ndim=3)
